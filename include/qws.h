@@ -249,6 +249,96 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
                             void* ws, size_t ws_bytes, qws_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Prompts and batches.  The pages run a prompt through the same layers as a
+ * decoded token (infer-compute README §Quick Start and §Architecture,
+ * prefill_q4: the seq > 1 path) and print no formulas for what lies between
+ * the products; these are the forms for many tokens of rope_at_pos and
+ * kv_attention, and the table lookup before them.
+ *
+ * Heads of many tokens: element i of head h of token t is
+ * data[t * token_stride + h * head_stride + i] (f32, device); strides in
+ * elements, multiples of 4; data 16-byte aligned.  Views of a fused QKV
+ * product's rows and of a [n_kv][max_seq][head_dim] cache (head_stride =
+ * max_seq * head_dim, token_stride = head_dim) have this form.
+ * Host arrays (cu_q, cu_k, n_ctx) and the structs are read during the call
+ * only; a captured call keeps its lengths.
+ * head_dim in {32, 64, 128, 256}, n_q_heads / n_kv_heads in 1..4 everywhere.
+ * All four calls: identical results run to run.
+ *
+ * qws_embed_tokens: out[t][i] = scale * dequant(W)[tokens[t]][i].
+ *   W  vocab x hidden in fmt (QWS_Q4_0, QWS_Q8_0, QWS_Q4_K, QWS_Q6_K; device,
+ *      16-byte aligned); tokens [n_tokens] int64 (device, 8-byte aligned); out
+ *      [n_tokens][hidden] f32 (device, 16-byte aligned).  hidden a positive
+ *      multiple of the block (32 or 256); n_tokens >= 0; scale finite.
+ *   A token outside [0, vocab) gives a row of zeros and records device error
+ *   code 512 (read by qws_device_error).  The weight is rounded at most once
+ *   to f32, the scaling once more.
+ *
+ * qws_qk_norm_rope: for every head x of q (n_q_heads) and k (n_kv_heads) of
+ *   every token: y = x / sqrt(mean x^2 + eps) * w (w_q for q, w_k for k, each
+ *   [head_dim] f32, device, 4-byte aligned; NULL = no norm for that one), then
+ *   rotated at the token's position as in qws_rope_at_pos.  positions
+ *   [n_tokens] int64 (device, 8-byte aligned), any sign.  An output may be its
+ *   own input (same pointer and strides); otherwise outputs overlap no input
+ *   and not one another.  rot_dim even, 0 < rot_dim <= head_dim;
+ *   base >= 1; eps >= 0; n_tokens >= 0.  The angle modulo a turn is exact to
+ *   2^-53 of the rotation per position, whatever the position; its sine and
+ *   cosine and the rotation are f32.
+ *
+ * qws_prompt_attention: causal attention of packed sequences.  Sequence s has
+ *   query tokens cu_q[s] .. cu_q[s+1]-1 and keys cu_k[s] .. cu_k[s+1]-1; query
+ *   i of n_q sees key j of n_k iff j <= i + n_k - n_q (its last query sees all:
+ *   n_k > n_q continues a prompt whose first keys are already there, n_k < n_q
+ *   leaves the first rows without a key).  cu_k NULL = cu_q.
+ *     s_j = scale * q_ih . k_j, softcap as in qws_kv_attention, out_ih = sum_j
+ *     softmax(s)_j v_j, head h reading kv head h / (n_q / n_kv); a row without
+ *     a key is zero.  Rows that belong to no sequence are not touched.
+ *   cu_q, cu_k: host, n_seqs + 1 non-decreasing offsets from 0 up, below 2^31.
+ *   ws: device, 16-byte aligned, >= qws_prompt_attention_workspace_bytes of
+ *   the same arguments (0: may be NULL).  Keys that a row does not see may
+ *   hold anything, infinities and NaN included.
+ *
+ * qws_prefix_attention: one decode step of a batch over a shared prefix.  Row
+ *   b of q attends to positions 0 .. n_prefix-1 of the shared caches k_prefix,
+ *   v_prefix ([n_kv_heads][max_prefix][head_dim]) and then to positions 0 ..
+ *   n_ctx[b]-1 of its own ([batch][n_kv_heads][max_seq][head_dim]), as in
+ *   qws_kv_attention over the two one after the other; a row without any
+ *   position is zero.  Caches 16-byte aligned; k_prefix and v_prefix may be
+ *   NULL when n_prefix is 0, the own caches when every n_ctx is 0.
+ *   0 <= n_prefix <= max_prefix < 2^31, 0 <= n_ctx[b] <= max_seq < 2^31 (host
+ *   array), batch >= 0.  ws as above, qws_prefix_attention_workspace_bytes.
+ *   Positions from the lengths on may hold anything.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  float* data;
+  int64_t token_stride, head_stride;
+} qws_heads;
+
+qws_status qws_embed_tokens(qws_format fmt, const void* W, const int64_t* tokens, float* out,
+                            int64_t vocab, int64_t hidden, int64_t n_tokens, float scale,
+                            qws_stream stream);
+qws_status qws_qk_norm_rope(const qws_heads* q, const qws_heads* k, const qws_heads* q_out,
+                            const qws_heads* k_out, const float* w_q, const float* w_k,
+                            const int64_t* positions, int64_t n_tokens, int n_q_heads,
+                            int n_kv_heads, int head_dim, int rot_dim, double base, float eps,
+                            qws_stream stream);
+size_t qws_prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k, int n_seqs,
+                                            int n_q_heads, int n_kv_heads, int head_dim);
+qws_status qws_prompt_attention(const qws_heads* q, const qws_heads* k, const qws_heads* v,
+                                const qws_heads* out, const int64_t* cu_q, const int64_t* cu_k,
+                                int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                                float scale, float softcap, void* ws, size_t ws_bytes,
+                                qws_stream stream);
+size_t qws_prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_ctx, int batch,
+                                            int n_q_heads, int n_kv_heads, int head_dim);
+qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const float* v_prefix,
+                                int64_t max_prefix, int64_t n_prefix, const float* k_caches,
+                                const float* v_caches, int64_t max_seq, const int64_t* n_ctx,
+                                const qws_heads* out, int batch, int n_q_heads, int n_kv_heads,
+                                int head_dim, float scale, float softcap, void* ws,
+                                size_t ws_bytes, qws_stream stream);
+
+/* ------------------------------------------------------------------------
  * Gated FFN (infer-compute README §Shaders "Q4_K fused FFN": q4k_ffn_gate_up,
  * q4k_geglu_gelu_tanh_down; infer-inference README §WalkFfn steps 1-3):
  *   g = Wg x, u = Wu x            (one pass over x for both, inter rows)
@@ -438,7 +528,7 @@ qws_status qws_decode_kv(const qws_layer* layers, int n_layers, float* h, const 
  *   for data, 2 = a producer gave up waiting for a free stage, 4 = a grid
  *   barrier gave up, 8 = a producer gave up draining its copies; 16..128 the
  *   prefill kernel's waits; 256 = a prefill weight outside the f16 split's
- *   range) and clears them.  Returns QWS_ERR_TIMEOUT when the code is
+ *   range; 512 = a token outside the embedding table) and clears them.  Returns QWS_ERR_TIMEOUT when the code is
  *   non-zero.
  * qws_version: library version string.
  * ---------------------------------------------------------------------- */

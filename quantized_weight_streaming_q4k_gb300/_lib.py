@@ -46,8 +46,13 @@ class QwsKv(C.Structure):
     ]
 
 
+class QwsHeads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 # name -> (restype, argtypes); mirrors include/qws.h
 P, F, I64, I, SZ, U = C.c_void_p, C.c_void_p, C.c_int64, C.c_int, C.c_size_t, C.c_uint
+H, N64 = C.POINTER(QwsHeads), C.POINTER(C.c_int64)
 SIGNATURES = {
     "qws_q4k_matvec": (I, [P, F, F, I64, I64, I, P]),
     "qws_q6k_matvec": (I, [P, F, F, I64, I64, I, P]),
@@ -82,6 +87,14 @@ SIGNATURES = {
     "qws_decode_kv_workspace_bytes": (SZ, [C.POINTER(QwsDims), I64]),
     "qws_decode_kv": (I, [C.POINTER(QwsLayer), I, F, C.POINTER(QwsDims), C.POINTER(QwsKv), P,
                           SZ, P]),
+    "qws_embed_tokens": (I, [I, P, P, F, I64, I64, I64, C.c_float, P]),
+    "qws_qk_norm_rope": (I, [H, H, H, H, F, F, P, I64, I, I, I, I, C.c_double, C.c_float, P]),
+    "qws_prompt_attention_workspace_bytes": (SZ, [N64, N64, I, I, I, I]),
+    "qws_prompt_attention": (I, [H, H, H, H, N64, N64, I, I, I, I, C.c_float, C.c_float, P, SZ,
+                                 P]),
+    "qws_prefix_attention_workspace_bytes": (SZ, [I64, N64, I, I, I, I]),
+    "qws_prefix_attention": (I, [H, F, F, I64, I64, F, F, I64, N64, H, I, I, I, I, C.c_float,
+                                 C.c_float, P, SZ, P]),
 }
 
 _lib = None

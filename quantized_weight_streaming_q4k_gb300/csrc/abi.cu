@@ -380,6 +380,247 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
   return ok();
 }
 
+namespace {
+
+// strided heads (qws_heads): 16-byte loads and stores of whole heads
+qws_status check_heads(const char* fn, const char* name, const qws_heads* x) {
+  if (!x) return fail(QWS_ERR_NULL, "%s: %s is NULL", fn, name);
+  if (!x->data) return fail(QWS_ERR_NULL, "%s: %s data is NULL", fn, name);
+  if (!aligned(x->data, 16))
+    return fail(QWS_ERR_ALIGN, "%s: %s is not 16-byte aligned", fn, name);
+  if (x->token_stride % 4 || x->head_stride % 4)
+    return fail(QWS_ERR_ALIGN, "%s: %s strides are not multiples of 4", fn, name);
+  if (x->token_stride < 0 || x->head_stride < 0)
+    return fail(QWS_ERR_SHAPE, "%s: %s has a negative stride", fn, name);
+  return QWS_OK;
+}
+
+// an output's heads may not overlap one another
+qws_status check_out_heads(const char* fn, const char* name, const qws_heads* x, int64_t tokens,
+                           int heads, int head_dim) {
+  const qws_status rc = check_heads(fn, name, x);
+  if (rc != QWS_OK) return rc;
+  const int64_t a = x->token_stride, b = x->head_stride;
+  const bool by_token = heads == 1 || (b >= head_dim && (tokens == 1 || a >= (heads - 1) * b + head_dim));
+  const bool by_head = tokens <= 1 || (a >= head_dim && (heads == 1 || b >= (tokens - 1) * a + head_dim));
+  if (!by_head && !(by_token && (tokens <= 1 || a >= head_dim)))
+    return fail(QWS_ERR_SHAPE, "%s: the strides of %s make its heads overlap", fn, name);
+  return QWS_OK;
+}
+
+qws_status check_head_counts(const char* fn, int n_q, int n_kv, int head_dim) {
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(QWS_ERR_SHAPE, "%s: head_dim = %d not in {32, 64, 128, 256}", fn, head_dim);
+  if (n_kv < 1 || n_kv > 16384 || n_q < n_kv || n_q % n_kv || n_q / n_kv > 4)
+    return fail(QWS_ERR_SHAPE, "%s: n_q_heads / n_kv_heads must be an integer in 1..4", fn);
+  return QWS_OK;
+}
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+
+qws_status check_offsets(const char* fn, const char* name, const int64_t* cu, int n_seqs) {
+  if (cu[0] < 0) return fail(QWS_ERR_SHAPE, "%s: %s[0] < 0", fn, name);
+  for (int s = 0; s < n_seqs; ++s)
+    if (cu[s + 1] < cu[s]) return fail(QWS_ERR_SHAPE, "%s: %s decreases at %d", fn, name, s);
+  if (cu[n_seqs] > kMaxTokens) return fail(QWS_ERR_SHAPE, "%s: %s passes 2^31", fn, name);
+  return QWS_OK;
+}
+
+qws_status check_scale(const char* fn, float scale, float softcap) {
+  if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
+    return fail(QWS_ERR_SHAPE, "%s: scale must be finite and softcap >= 0", fn);
+  return QWS_OK;
+}
+
+qws_status check_ws(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+  if (need && (!ws || ws_bytes < need))
+    return fail(QWS_ERR_WORKSPACE, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
+  if (!aligned(ws, 16)) return fail(QWS_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  return QWS_OK;
+}
+
+#define QWS_TRY(call)                        \
+  do {                                       \
+    const qws_status rc_ = (call);           \
+    if (rc_ != QWS_OK) return rc_;           \
+  } while (0)
+
+}  // namespace
+
+qws_status qws_embed_tokens(qws_format fmt, const void* W, const int64_t* tokens, float* out,
+                            int64_t vocab, int64_t hidden, int64_t n_tokens, float scale,
+                            qws_stream stream) {
+  const char* fn = "qws_embed_tokens";
+  if (!known_format(fmt) && fmt != QWS_Q8_0)
+    return fail(QWS_ERR_FORMAT, "%s: unknown format %d", fn, static_cast<int>(fmt));
+  QWS_CHECK_W(W);
+  QWS_CHECK_PTR(tokens);
+  if (!aligned(tokens, 8)) return fail(QWS_ERR_ALIGN, "%s: tokens is not 8-byte aligned", fn);
+  QWS_CHECK_PTR(out);
+  if (!aligned(out, 16)) return fail(QWS_ERR_ALIGN, "%s: out is not 16-byte aligned", fn);
+  if (vocab < 1) return fail(QWS_ERR_SHAPE, "%s: vocab = %lld < 1", fn, (long long)vocab);
+  if (hidden <= 0 || hidden % qws::block_weights(fmt) || hidden > (int64_t(1) << 24))
+    return fail(QWS_ERR_SHAPE, "%s: hidden = %lld is not a positive multiple of %lld", fn,
+                (long long)hidden, (long long)qws::block_weights(fmt));
+  if (n_tokens < 0 || n_tokens > kMaxTokens / ((hidden + 511) / 512))
+    return fail(QWS_ERR_SHAPE, "%s: n_tokens = %lld out of range", fn, (long long)n_tokens);
+  if (!std::isfinite(scale)) return fail(QWS_ERR_SHAPE, "%s: scale must be finite", fn);
+  if (n_tokens == 0) return ok();
+  const cudaError_t e =
+      qws::launch_embed(fmt, static_cast<const uint8_t*>(W), tokens, out, vocab, hidden, n_tokens,
+                        scale, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn, "");
+  return ok();
+}
+
+qws_status qws_qk_norm_rope(const qws_heads* q, const qws_heads* k, const qws_heads* q_out,
+                            const qws_heads* k_out, const float* w_q, const float* w_k,
+                            const int64_t* positions, int64_t n_tokens, int n_q_heads,
+                            int n_kv_heads, int head_dim, int rot_dim, double base, float eps,
+                            qws_stream stream) {
+  const char* fn = "qws_qk_norm_rope";
+  QWS_TRY(check_head_counts(fn, n_q_heads, n_kv_heads, head_dim));
+  if (n_tokens < 0 || n_tokens > kMaxTokens)
+    return fail(QWS_ERR_SHAPE, "%s: n_tokens = %lld out of range", fn, (long long)n_tokens);
+  QWS_TRY(check_heads(fn, "q", q));
+  QWS_TRY(check_heads(fn, "k", k));
+  QWS_TRY(check_out_heads(fn, "q_out", q_out, n_tokens, n_q_heads, head_dim));
+  QWS_TRY(check_out_heads(fn, "k_out", k_out, n_tokens, n_kv_heads, head_dim));
+  QWS_CHECK_PTR(positions);
+  if (!aligned(positions, 8))
+    return fail(QWS_ERR_ALIGN, "%s: positions is not 8-byte aligned", fn);
+  if (!aligned(w_q, 4) || !aligned(w_k, 4))
+    return fail(QWS_ERR_ALIGN, "%s: w_q and w_k must be 4-byte aligned", fn);
+  if (rot_dim < 2 || rot_dim % 2 || rot_dim > head_dim)
+    return fail(QWS_ERR_SHAPE, "%s: need an even 0 < rot_dim <= head_dim", fn);
+  if (!(base >= 1.0) || !std::isfinite(base))
+    return fail(QWS_ERR_SHAPE, "%s: need a finite base >= 1", fn);
+  if (!(eps >= 0.f)) return fail(QWS_ERR_SHAPE, "%s: eps must be >= 0", fn);
+  const auto moved = [](const qws_heads* in, const qws_heads* o) {
+    return in->data == o->data &&
+           (in->token_stride != o->token_stride || in->head_stride != o->head_stride);
+  };
+  if (moved(q, q_out) || moved(k, k_out))
+    return fail(QWS_ERR_SHAPE, "%s: an output in place has its input's strides", fn);
+  if (q_out->data == k_out->data || q_out->data == k->data || k_out->data == q->data)
+    return fail(QWS_ERR_SHAPE, "%s: q and k must not share an output", fn);
+  if (n_tokens == 0) return ok();
+  const cudaError_t e = qws::launch_qk_norm_rope(
+      *q, *k, *q_out, *k_out, w_q, w_k, positions, n_tokens, n_q_heads, n_kv_heads, head_dim,
+      rot_dim, base, eps, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn, "");
+  return ok();
+}
+
+size_t qws_prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k, int n_seqs,
+                                            int n_q_heads, int n_kv_heads, int head_dim) {
+  const char* fn = "qws_prompt_attention_workspace_bytes";
+  if (!cu_k) cu_k = cu_q;
+  if (n_seqs < 1 || !cu_q || check_head_counts(fn, n_q_heads, n_kv_heads, head_dim) != QWS_OK ||
+      check_offsets(fn, "cu_q", cu_q, n_seqs) != QWS_OK ||
+      check_offsets(fn, "cu_k", cu_k, n_seqs) != QWS_OK)
+    return 0;
+  return round256(qws::prompt_attention_workspace_bytes(cu_q, cu_k, n_seqs, n_q_heads, n_kv_heads,
+                                                        head_dim));
+}
+
+qws_status qws_prompt_attention(const qws_heads* q, const qws_heads* k, const qws_heads* v,
+                                const qws_heads* out, const int64_t* cu_q, const int64_t* cu_k,
+                                int n_seqs, int n_q_heads, int n_kv_heads, int head_dim,
+                                float scale, float softcap, void* ws, size_t ws_bytes,
+                                qws_stream stream) {
+  const char* fn = "qws_prompt_attention";
+  QWS_TRY(check_head_counts(fn, n_q_heads, n_kv_heads, head_dim));
+  QWS_CHECK_PTR(cu_q);
+  if (n_seqs < 0) return fail(QWS_ERR_SHAPE, "%s: n_seqs = %d < 0", fn, n_seqs);
+  if (!cu_k) cu_k = cu_q;
+  QWS_TRY(check_offsets(fn, "cu_q", cu_q, n_seqs));
+  QWS_TRY(check_offsets(fn, "cu_k", cu_k, n_seqs));
+  QWS_TRY(check_scale(fn, scale, softcap));
+  QWS_TRY(check_heads(fn, "q", q));
+  QWS_TRY(check_heads(fn, "k", k));
+  QWS_TRY(check_heads(fn, "v", v));
+  QWS_TRY(check_out_heads(fn, "out", out, cu_q[n_seqs], n_q_heads, head_dim));
+  if (out->data == q->data || out->data == k->data || out->data == v->data)
+    return fail(QWS_ERR_SHAPE, "%s: out must not be q, k or v", fn);
+  if (cu_q[n_seqs] == cu_q[0]) return ok();
+  QWS_TRY(check_ws(fn, ws, ws_bytes,
+                   qws::prompt_attention_workspace_bytes(cu_q, cu_k, n_seqs, n_q_heads,
+                                                         n_kv_heads, head_dim)));
+  const cudaError_t e = qws::launch_prompt_attention(
+      *q, *k, *v, *out, cu_q, cu_k, n_seqs, n_q_heads, n_kv_heads, head_dim, scale, softcap, ws,
+      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn, "");
+  return ok();
+}
+
+namespace {
+
+qws_status check_prefix_lengths(const char* fn, int64_t n_prefix, int64_t max_prefix,
+                                const int64_t* n_ctx, int batch, int64_t max_seq) {
+  if (batch < 0 || batch > (1 << 20))
+    return fail(QWS_ERR_SHAPE, "%s: batch = %d out of range", fn, batch);
+  if (n_prefix < 0 || n_prefix > max_prefix || max_prefix > kMaxTokens)
+    return fail(QWS_ERR_SHAPE, "%s: need 0 <= n_prefix <= max_prefix < 2^31", fn);
+  if (batch && !n_ctx) return fail(QWS_ERR_NULL, "%s: n_ctx is NULL", fn);
+  if (max_seq < 0 || max_seq > kMaxTokens)
+    return fail(QWS_ERR_SHAPE, "%s: need 0 <= max_seq < 2^31", fn);
+  for (int b = 0; b < batch; ++b)
+    if (n_ctx[b] < 0 || n_ctx[b] > max_seq)
+      return fail(QWS_ERR_SHAPE, "%s: need 0 <= n_ctx[%d] <= max_seq", fn, b);
+  return QWS_OK;
+}
+
+}  // namespace
+
+size_t qws_prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_ctx, int batch,
+                                            int n_q_heads, int n_kv_heads, int head_dim) {
+  const char* fn = "qws_prefix_attention_workspace_bytes";
+  if (batch < 1 || check_head_counts(fn, n_q_heads, n_kv_heads, head_dim) != QWS_OK ||
+      check_prefix_lengths(fn, n_prefix, n_prefix, n_ctx, batch, kMaxTokens) != QWS_OK)
+    return 0;
+  return round256(qws::prefix_attention_workspace_bytes(n_prefix, n_ctx, batch, n_q_heads,
+                                                        n_kv_heads, head_dim));
+}
+
+qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const float* v_prefix,
+                                int64_t max_prefix, int64_t n_prefix, const float* k_caches,
+                                const float* v_caches, int64_t max_seq, const int64_t* n_ctx,
+                                const qws_heads* out, int batch, int n_q_heads, int n_kv_heads,
+                                int head_dim, float scale, float softcap, void* ws,
+                                size_t ws_bytes, qws_stream stream) {
+  const char* fn = "qws_prefix_attention";
+  QWS_TRY(check_head_counts(fn, n_q_heads, n_kv_heads, head_dim));
+  QWS_TRY(check_prefix_lengths(fn, n_prefix, max_prefix, n_ctx, batch, max_seq));
+  QWS_TRY(check_scale(fn, scale, softcap));
+  if (batch == 0) return ok();
+  QWS_TRY(check_heads(fn, "q", q));
+  QWS_TRY(check_out_heads(fn, "out", out, batch, n_q_heads, head_dim));
+  if (out->data == q->data) return fail(QWS_ERR_SHAPE, "%s: out must not be q", fn);
+  int64_t longest = 0;
+  for (int b = 0; b < batch; ++b) longest = n_ctx[b] > longest ? n_ctx[b] : longest;
+  if (n_prefix) {
+    QWS_CHECK_PTR(k_prefix);
+    QWS_CHECK_PTR(v_prefix);
+  }
+  if (longest) {
+    QWS_CHECK_PTR(k_caches);
+    QWS_CHECK_PTR(v_caches);
+  }
+  if (!aligned(k_prefix, 16) || !aligned(v_prefix, 16) || !aligned(k_caches, 16) ||
+      !aligned(v_caches, 16))
+    return fail(QWS_ERR_ALIGN, "%s: the caches must be 16-byte aligned", fn);
+  QWS_TRY(check_ws(fn, ws, ws_bytes,
+                   qws::prefix_attention_workspace_bytes(n_prefix, n_ctx, batch, n_q_heads,
+                                                         n_kv_heads, head_dim)));
+  const cudaError_t e = qws::launch_prefix_attention(
+      *q, k_prefix, v_prefix, max_prefix, n_prefix, k_caches, v_caches, max_seq, n_ctx, *out,
+      batch, n_q_heads, n_kv_heads, head_dim, scale, softcap, ws,
+      reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, fn, "");
+  return ok();
+}
+
 static qws_status check_ffn_shape(const char* fn, int64_t hidden, int64_t inter) {
   if (hidden <= 0 || hidden % 256 || hidden > kMaxHidden)
     return fail(QWS_ERR_SHAPE, "%s: hidden = %lld (need a multiple of 256 in (0, 20480])", fn,
@@ -596,7 +837,7 @@ qws_status qws_device_error(unsigned* code) {
   if (e != cudaSuccess) return cuda_fail(e, "qws_device_error", "");
   *code = qws::read_clear_matvec_errors() | qws::read_clear_chain_errors() |
           qws::read_clear_prefill_errors() | qws::read_clear_attention_errors() |
-          qws::read_clear_batchmv_errors();
+          qws::read_clear_batchmv_errors() | qws::read_clear_embed_errors();
   return *code ? fail(QWS_ERR_TIMEOUT, "device error code 0x%x", *code) : ok();
 }
 

@@ -1,0 +1,205 @@
+// attend_rows.cuh -- attention of a tile of query rows over a range of keys in
+// f32 on the CUDA cores, and the tables and partial results shared by the
+// prompt and shared-prefix attention (prompt.cu, prefix.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "launch.h"
+
+namespace qws {
+
+// Sequences of one launch: row (query token) and key offsets into the packed
+// arrays, and the first work item of each.  Passed as a kernel argument, so a
+// captured launch holds its own copy; longer lists take several launches.
+constexpr int kMaxSeqs = 128;
+struct SeqTab {
+  int n;
+  int q0[kMaxSeqs + 1];     // first query token of sequence s
+  int k0[kMaxSeqs + 1];     // first key of sequence s
+  int item[kMaxSeqs + 1];   // first work item of sequence s
+};
+
+// the sequence s with item[s] <= i < item[s + 1] (empty ones are skipped)
+__device__ __forceinline__ int find_seq(const int* first, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Column of value j of a lane's share of a row of 32 * kPL values, in groups
+// of up to four neighbours.
+template <int kPL>
+__device__ __forceinline__ int lane_col(int lane, int j) {
+  if constexpr (kPL >= 4) return (j / 4) * 128 + lane * 4 + j % 4;
+  else return lane * kPL + j;
+}
+
+template <int kPL>
+__device__ __forceinline__ void load_row(const float* p, int lane, float (&x)[kPL]) {
+  if constexpr (kPL >= 4) {
+#pragma unroll
+    for (int g = 0; g < kPL / 4; ++g) {
+      const float4 v = *reinterpret_cast<const float4*>(p + g * 128 + lane * 4);
+      x[4 * g] = v.x; x[4 * g + 1] = v.y; x[4 * g + 2] = v.z; x[4 * g + 3] = v.w;
+    }
+  } else if constexpr (kPL == 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p + lane * 2);
+    x[0] = v.x; x[1] = v.y;
+  } else {
+    x[0] = p[lane];
+  }
+}
+
+template <int kPL>
+__device__ __forceinline__ void store_row(float* p, int lane, const float (&x)[kPL]) {
+  if constexpr (kPL >= 4) {
+#pragma unroll
+    for (int g = 0; g < kPL / 4; ++g)
+      *reinterpret_cast<float4*>(p + g * 128 + lane * 4) =
+          make_float4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]);
+  } else if constexpr (kPL == 2) {
+    *reinterpret_cast<float2*>(p + lane * 2) = make_float2(x[0], x[1]);
+  } else {
+    p[lane] = x[0];
+  }
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+__device__ __forceinline__ float soft_cap(float s, float cap) {
+  return cap > 0.f ? cap * tanhf(s / cap) : s;
+}
+
+// A CTA of kRowWarps warps, kR query rows a warp.  Keys come in tiles of 32
+// through shared memory: a lane scores one key against the warp's rows (K row
+// and q by 16-byte loads, K rows padded by 16 bytes against bank conflicts),
+// the online softmax runs across the lanes, and for p * V a lane holds its
+// columns of the output.  Scores, statistics and output are f32.
+constexpr int kRowWarps = 8;
+constexpr int kRowThreads = kRowWarps * 32;
+
+template <int kPL, int kR>
+struct RowTile {
+  static constexpr int kHd = kPL * 32;
+  static constexpr int kPitch = kHd + 4;
+  static constexpr size_t kSmem =
+      sizeof(float) * (2 * 32 * kPitch + static_cast<size_t>(kRowWarps) * kR * kHd);
+  float m[kR], l[kR], acc[kR][kPL];
+
+  __device__ __forceinline__ void init() {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPL; ++j) acc[r][j] = 0.f;
+    }
+  }
+
+  // this warp's q rows in shared memory
+  __device__ __forceinline__ static float* q_rows(float* smem) {
+    return smem + 2 * 32 * kPitch + (threadIdx.x >> 5) * kR * kHd;
+  }
+
+  // keys [ka, kb) (relative to K and V); row r sees the keys below vis[r]
+  __device__ __forceinline__ void run(float* smem, const float* K, const float* V,
+                                      int64_t k_stride, int64_t v_stride, int ka, int kb,
+                                      const int (&vis)[kR], float scale, float cap) {
+    float* ks = smem;
+    float* vs = smem + 32 * kPitch;
+    const float* qs = q_rows(smem);
+    const int lane = threadIdx.x & 31;
+    int least = vis[0];
+#pragma unroll
+    for (int r = 1; r < kR; ++r) least = min(least, vis[r]);
+    for (int t = ka; t < kb; t += 32) {
+      const int n = min(32, kb - t);
+      __syncthreads();
+      for (int e = threadIdx.x; e < 32 * (kHd / 4); e += kRowThreads) {
+        const int row = e / (kHd / 4), c = (e - row * (kHd / 4)) * 4;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        if (row < n) {
+          a = *reinterpret_cast<const float4*>(K + (t + row) * k_stride + c);
+          b = *reinterpret_cast<const float4*>(V + (t + row) * v_stride + c);
+        }
+        *reinterpret_cast<float4*>(ks + row * kPitch + c) = a;
+        *reinterpret_cast<float4*>(vs + row * kPitch + c) = b;
+      }
+      __syncthreads();
+      float s[kR][2];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) s[r][0] = s[r][1] = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < kHd; c += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(ks + lane * kPitch + c);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const float4 q4 = *reinterpret_cast<const float4*>(qs + r * kHd + c);
+          s[r][0] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, s[r][0]));
+          s[r][1] = fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r][1]));
+        }
+      }
+      float p[kR];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        float x = soft_cap((s[r][0] + s[r][1]) * scale, cap);
+        if (t + lane >= vis[r]) x = -INFINITY;      // select: what is masked is not looked at
+        const float mn = fmaxf(m[r], warp_max(x));
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float alpha = expf(m[r] - base);
+        p[r] = expf(x - base);
+        l[r] = fmaf(l[r], alpha, warp_sum(p[r]));
+        m[r] = mn;
+#pragma unroll
+        for (int j = 0; j < kPL; ++j) acc[r][j] *= alpha;
+      }
+      const bool whole = t + n <= least;     // every row sees every key of the tile
+      for (int k = 0; k < n; ++k) {
+        float v[kPL];
+        load_row<kPL>(vs + k * kPitch, lane, v);
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+          const float pk = __shfl_sync(0xFFFFFFFFu, p[r], k);
+          // 0 * v of a masked key would let an infinity or NaN there through
+          if (whole || t + k < vis[r]) {
+#pragma unroll
+            for (int j = 0; j < kPL; ++j) acc[r][j] = fmaf(pk, v[j], acc[r][j]);
+          }
+        }
+      }
+    }
+  }
+};
+
+// One row's partial result: unnormalised output, then running max and sum.
+// Partials are [slot][row of the tile][head_dim + kPartPad].
+constexpr int kPartPad = 4;   // m, l, two unused: keeps rows 16-byte aligned
+
+template <int kPL>
+__device__ __forceinline__ void store_partial(float* dst, int lane, const float (&acc)[kPL],
+                                              float m, float l) {
+  store_row<kPL>(dst, lane, acc);
+  if (lane == 0) {
+    dst[32 * kPL] = m;
+    dst[32 * kPL + 1] = l;
+  }
+}
+
+// out = acc / l; a row that saw no key is zero
+template <int kPL>
+__device__ __forceinline__ void store_final(float* dst, int lane, float (&acc)[kPL], float l) {
+  const float r = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+  for (int j = 0; j < kPL; ++j) acc[j] *= r;
+  store_row<kPL>(dst, lane, acc);
+}
+
+}  // namespace qws

@@ -25,6 +25,8 @@ enum : unsigned {
   kErrEmptyWait = 2u,     // producer gave up waiting for a free stage
   kErrGridBarrier = 4u,   // a CTA gave up waiting at a grid barrier
   kErrDrain = 8u,         // producer gave up waiting for its own copies at exit
+  // 16 .. 256: prefill.cu
+  kErrTokenRange = 512u,  // an embedding row outside the table was asked for
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {

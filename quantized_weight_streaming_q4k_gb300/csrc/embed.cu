@@ -1,0 +1,132 @@
+// embed.cu -- rows of a quantised embedding table, scaled (the input of a
+// decode step or of a prompt; the table is the one the lm_head multiplies
+// when the two are tied):
+//   out[t][i] = scale * dequant(W)[token[t]][i].
+//
+// One thread writes four consecutive values with one 16-byte store and reads
+// the 2 to 4 bytes of codes behind them, the block's f16 scale(s) and its
+// sub-block scale; the reads of a block's scales hit L1 for all but the first
+// thread.  Bound by writing out: 4 bytes written per 0.56 to 1.06 read.
+//
+// Rounding: a Q4_0, Q8_0 or Q6_K weight d * sc * q is exact in f32 (11 + 7 + 6
+// bits at most); a Q4_K weight d * sc * q - dmin * m is one fma of two exact
+// products; the multiplication by scale rounds once.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch.h"
+
+namespace qws {
+
+__device__ unsigned g_err_embed;
+
+constexpr int kEmbThreads = 128;
+
+__device__ __forceinline__ uint32_t ld_u16(const uint8_t* p) {
+  return __ldg(reinterpret_cast<const unsigned short*>(p));
+}
+// four bytes at a 2-byte boundary
+__device__ __forceinline__ uint32_t ld_u32_at2(const uint8_t* p) {
+  return ld_u16(p) | (ld_u16(p + 2) << 16);
+}
+
+// values c .. c + 3 of a row (c % 4 == 0), before the scale
+template <int kFmt>
+__device__ __forceinline__ float4 embed_four(const uint8_t* row, int64_t c) {
+  float v[4];
+  if constexpr (kFmt == QWS_Q4_0) {
+    const uint8_t* b = row + c / 32 * 18;
+    const int j = static_cast<int>(c % 32);
+    const float d = half_bits_to_float(ld_u16(b));
+    const uint32_t q = ld_u32_at2(b + 2 + j % 16) >> (j >= 16 ? 4 : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = d * static_cast<float>(static_cast<int>((q >> (8 * i)) & 15u) - 8);
+  } else if constexpr (kFmt == QWS_Q8_0) {
+    const uint8_t* b = row + c / 32 * 34;
+    const float d = half_bits_to_float(ld_u16(b));
+    const uint32_t q = ld_u32_at2(b + 2 + c % 32);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = d * static_cast<float>(static_cast<signed char>((q >> (8 * i)) & 255u));
+  } else if constexpr (kFmt == QWS_Q4_K) {
+    const uint8_t* b = row + c / 256 * 144;
+    const int r = static_cast<int>(c % 256), s = r / 32;   // sub-block
+    const uint4 hd = __ldg(reinterpret_cast<const uint4*>(b));
+    const uint32_t sh = 8u * static_cast<uint32_t>(s & 3);
+    const uint32_t a = (hd.y >> sh) & 255u, m = (hd.z >> sh) & 255u, h = (hd.w >> sh) & 255u;
+    const uint32_t sc = s < 4 ? (a & 63u) : ((h & 15u) | ((a >> 6) << 4));
+    const uint32_t mn = s < 4 ? (m & 63u) : ((h >> 4) | ((m >> 6) << 4));
+    const float ds = half_bits_to_float(hd.x) * static_cast<float>(sc);
+    const float dm = half_bits_to_float(hd.x >> 16) * static_cast<float>(mn);
+    const uint32_t q = __ldg(reinterpret_cast<const uint32_t*>(b + 16 + r / 64 * 32 + r % 32)) >>
+                       ((s & 1) ? 4 : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(ds, static_cast<float>((q >> (8 * i)) & 15u), -dm);
+  } else {
+    const uint8_t* b = row + c / 256 * 210;
+    const int r = static_cast<int>(c % 256), h = r / 128, l = r % 32, qt = r % 128 / 32;
+    const float ds =
+        half_bits_to_float(ld_u16(b + 208)) *
+        static_cast<float>(static_cast<signed char>(__ldg(b + 192 + r / 16)));
+    const uint32_t lo = ld_u32_at2(b + 64 * h + 32 * (qt & 1) + l) >> (4 * (qt >> 1));
+    const uint32_t hi = ld_u32_at2(b + 128 + 32 * h + l) >> (2 * qt);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = static_cast<int>(((lo >> (8 * i)) & 15u) | (((hi >> (8 * i)) & 3u) << 4));
+      v[i] = ds * static_cast<float>(q - 32);
+    }
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// grid.x = n_tokens * segs; block b of a token covers values
+// [seg * 4 * kEmbThreads, ...) of its row
+template <int kFmt>
+__global__ void __launch_bounds__(kEmbThreads)
+    embed_kernel(const uint8_t* __restrict__ W, const int64_t* __restrict__ tokens,
+                 float* __restrict__ out, int64_t vocab, int64_t hidden, int64_t row_bytes,
+                 int segs, float scale) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x / static_cast<unsigned>(segs);
+  const int seg = static_cast<int>(blockIdx.x - t * segs);
+  const int64_t tok = __ldg(tokens + t);
+  const int64_t c = (static_cast<int64_t>(seg) * kEmbThreads + threadIdx.x) * 4;
+  if (c >= hidden) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (tok >= 0 && tok < vocab) {
+    v = embed_four<kFmt>(W + tok * row_bytes, c);
+    v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+  } else if (threadIdx.x == 0) {
+    atomicOr(&g_err_embed, kErrTokenRange);
+  }
+  *reinterpret_cast<float4*>(out + t * hidden + c) = v;
+}
+
+cudaError_t launch_embed(int fmt, const uint8_t* W, const int64_t* tokens, float* out,
+                         int64_t vocab, int64_t hidden, int64_t n_tokens, float scale,
+                         cudaStream_t st) {
+  const int segs = static_cast<int>((hidden / 4 + kEmbThreads - 1) / kEmbThreads);
+  const int64_t rb = row_bytes_of(fmt, hidden);
+  const dim3 grid(static_cast<unsigned>(n_tokens * segs));
+  switch (fmt) {
+#define QWS_EMB_CASE(F)                                                                       \
+  case F:                                                                                     \
+    return pdl_launch(embed_kernel<F>, grid, kEmbThreads, 0, st, W, tokens, out, vocab,       \
+                      hidden, rb, segs, scale);
+    QWS_EMB_CASE(QWS_Q4_0) QWS_EMB_CASE(QWS_Q8_0) QWS_EMB_CASE(QWS_Q4_K) QWS_EMB_CASE(QWS_Q6_K)
+#undef QWS_EMB_CASE
+  }
+  return cudaErrorInvalidValue;
+}
+
+unsigned read_clear_embed_errors() {
+  unsigned v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_embed, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_err_embed, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace qws

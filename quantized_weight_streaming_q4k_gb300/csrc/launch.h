@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <string>
+#include <utility>
 
 #include "../../include/qws.h"
 #include "engine.cuh"
@@ -168,6 +169,53 @@ cudaError_t launch_residual_rms_norm(float* h, const float* y, const float* w, f
 unsigned read_clear_matvec_errors();
 cudaError_t launch_selftest_mbar(long long limit, cudaStream_t st);
 cudaError_t launch_selftest_poll(void* word8, long long limit, cudaStream_t st);
+
+// rows of a quantised embedding table (embed.cu)
+cudaError_t launch_embed(int fmt, const uint8_t* W, const int64_t* tokens, float* out,
+                         int64_t vocab, int64_t hidden, int64_t n_tokens, float scale,
+                         cudaStream_t st);
+unsigned read_clear_embed_errors();
+// per-head norm + rotation of many tokens (qknorm.cu)
+cudaError_t launch_qk_norm_rope(const qws_heads& q, const qws_heads& k, const qws_heads& qo,
+                                const qws_heads& ko, const float* w_q, const float* w_k,
+                                const int64_t* positions, int64_t n_tokens, int n_q, int n_kv,
+                                int head_dim, int rot_dim, double base, float eps,
+                                cudaStream_t st);
+// causal attention over packed prompts (prompt.cu); cu_q, cu_k host arrays
+size_t prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k, int n_seqs,
+                                        int n_q, int n_kv, int head_dim);
+cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
+                                    const qws_heads& out, const int64_t* cu_q,
+                                    const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
+                                    int head_dim, float scale, float cap, void* ws,
+                                    cudaStream_t st);
+// decode attention of a batch over a shared prefix (prefix.cu); n_ctx a host array
+size_t prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_ctx, int batch,
+                                        int n_q, int n_kv, int head_dim);
+cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const float* vp,
+                                    int64_t max_prefix, int64_t n_prefix, const float* kc,
+                                    const float* vc, int64_t max_seq, const int64_t* n_ctx,
+                                    const qws_heads& out, int batch, int n_q, int n_kv,
+                                    int head_dim, float scale, float cap, void* ws,
+                                    cudaStream_t st);
+
+// A launch that may begin while the stream's previous kernel drains (the
+// kernel calls pdl_wait() before it touches global data).
+template <class... KArgs, class... Args>
+cudaError_t pdl_launch(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem,
+                       cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 // message returned by qws_last_error() on the calling thread (abi.cu)
 void set_last_error(const char* msg);

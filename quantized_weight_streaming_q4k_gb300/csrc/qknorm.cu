@@ -1,0 +1,135 @@
+// qknorm.cu -- the norm of every query and key head and the rotation at the
+// token's position, for many tokens in one pass (the prompt's form of
+// rope_at_pos, with the per-head RMS norm that some models put before it):
+//   y = x / sqrt(mean_i x_i^2 + eps) * w        (when w is given)
+//   (y_i, y_{i+r/2}) <- (y_i cos - y_{i+r/2} sin, y_i sin + y_{i+r/2} cos),
+//   angle pos * base^(-2i/r), i < r/2.
+//
+// Bound by memory: every head is read once and written once.  One CTA per
+// token: its threads compute the token's r/2 sines and cosines once into
+// shared memory while the warps' head rows are in flight, then one warp per
+// head (in turns) reduces, rotates and stores.
+//
+// The angle: FP64 arithmetic is slow on this GPU, and f32 loses the angle of
+// a far position.  The rotation per position in turns, f_i / 2 pi, is rounded
+// on the host to a 64-bit fixed-point fraction F_i (error 2^-53 relative);
+// pos * F_i modulo 2^64 by one integer product IS the fraction of a turn, exact
+// for any position.  Its top two bits (rounded) are the quadrant, the rest,
+// at most 1/8 turn either way, is rounded once to f32 for sinpi / cospi: an
+// angle error below 2^-24 * pi / 4.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attend_rows.cuh"
+#include "launch.h"
+
+namespace qws {
+
+constexpr int kQkMaxHalf = 128;   // rot_dim <= head_dim <= 256
+
+struct QkParams {
+  qws_heads q, k, qo, ko;
+  const float *w_q, *w_k;
+  const int64_t* positions;
+  int n_q, n_kv, rot;
+  float eps;
+  uint64_t turn[kQkMaxHalf];   // rotation per position, in 2^-64 turns
+};
+
+// cos and sin of the angle F * 2^-64 turns
+__device__ __forceinline__ void turn_cos_sin(uint64_t F, float& c, float& s) {
+  const uint64_t quad = (F + (uint64_t(1) << 61)) >> 62;
+  const int64_t rem = static_cast<int64_t>(F - (quad << 62));      // [-2^61, 2^61)
+  float s0, c0;
+  sincospif(static_cast<float>(rem) * 0x1p-63f, &s0, &c0);         // half turns
+  const int qd = static_cast<int>(quad & 3);
+  const float a = (qd & 1) ? s0 : c0, b = (qd & 1) ? c0 : s0;
+  c = (qd == 1 || qd == 2) ? -a : a;
+  s = qd >= 2 ? -b : b;
+}
+
+constexpr int kQkWarps = 8;
+
+template <int kPL>
+__global__ void __launch_bounds__(kQkWarps * 32)
+    qk_norm_rope_kernel(const __grid_constant__ QkParams p) {
+  constexpr int kHd = kPL * 32;
+  __shared__ float cs[kQkMaxHalf], sn[kQkMaxHalf];
+  __shared__ __align__(16) float row[kQkWarps][kHd];   // a head, for the partner of each element
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t t = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = p.rot / 2, heads = p.n_q + p.n_kv;
+  const uint64_t pos = static_cast<uint64_t>(__ldg(p.positions + t));
+  for (int i = threadIdx.x; i < half; i += kQkWarps * 32)
+    turn_cos_sin(pos * p.turn[i], cs[i], sn[i]);
+  float x[kPL];
+  auto fetch = [&](int h) {
+    const bool isq = h < p.n_q;
+    const qws_heads& in = isq ? p.q : p.k;
+    load_row<kPL>(in.data + t * in.token_stride + (isq ? h : h - p.n_q) * in.head_stride, lane,
+                  x);
+  };
+  if (warp < heads) fetch(warp);
+  __syncthreads();
+  for (int h = warp; h < heads; h += kQkWarps) {
+    if (h != warp) fetch(h);
+    const bool isq = h < p.n_q;
+    const float* w = isq ? p.w_q : p.w_k;
+    if (w) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPL; ++j) ss = fmaf(x[j], x[j], ss);
+      ss = warp_sum(ss);
+      const float r = 1.0f / sqrtf(ss * (1.0f / kHd) + p.eps);
+#pragma unroll
+      for (int j = 0; j < kPL; ++j) x[j] = x[j] * r * __ldg(w + lane_col<kPL>(lane, j));
+    }
+    __syncwarp();
+    store_row<kPL>(row[warp], lane, x);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kPL; ++j) {
+      const int i = lane_col<kPL>(lane, j);
+      if (i < half)
+        x[j] = fmaf(x[j], cs[i], -(row[warp][i + half] * sn[i]));
+      else if (i < p.rot)
+        x[j] = fmaf(row[warp][i - half], sn[i - half], x[j] * cs[i - half]);
+    }
+    const qws_heads& out = isq ? p.qo : p.ko;
+    store_row<kPL>(out.data + t * out.token_stride + (isq ? h : h - p.n_q) * out.head_stride,
+                   lane, x);
+  }
+}
+
+cudaError_t launch_qk_norm_rope(const qws_heads& q, const qws_heads& k, const qws_heads& qo,
+                                const qws_heads& ko, const float* w_q, const float* w_k,
+                                const int64_t* positions, int64_t n_tokens, int n_q, int n_kv,
+                                int head_dim, int rot_dim, double base, float eps,
+                                cudaStream_t st) {
+  QkParams p;
+  p.q = q; p.k = k; p.qo = qo; p.ko = ko;
+  p.w_q = w_q; p.w_k = w_k;
+  p.positions = positions;
+  p.n_q = n_q; p.n_kv = n_kv; p.rot = rot_dim;
+  p.eps = eps;
+  for (int i = 0; i < kQkMaxHalf; ++i) {
+    // base >= 1: at most 1 / 2 pi of a turn per position
+    const double turns =
+        i < rot_dim / 2 ? std::pow(base, -2.0 * i / rot_dim) / 6.283185307179586476925 : 0.0;
+    p.turn[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
+  }
+  const dim3 grid(static_cast<unsigned>(n_tokens));
+  switch (head_dim) {
+    case 32: return pdl_launch(qk_norm_rope_kernel<1>, grid, kQkWarps * 32, 0, st, p);
+    case 64: return pdl_launch(qk_norm_rope_kernel<2>, grid, kQkWarps * 32, 0, st, p);
+    case 128: return pdl_launch(qk_norm_rope_kernel<4>, grid, kQkWarps * 32, 0, st, p);
+    case 256: return pdl_launch(qk_norm_rope_kernel<8>, grid, kQkWarps * 32, 0, st, p);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace qws

@@ -22,6 +22,7 @@ __all__ = [
     "rope_at_pos", "kv_append", "kv_attention", "rms_norm_q8", "residual_rms_norm_q8",
     "q4k_qkv_proj", "q4k_ffn_gate_up_geglu", "q4k_ffn_gate_up_geglu_down", "rms_norm",
     "residual_add", "decode_chain", "decode_kv", "decode_kv_workspace_bytes", "workspace_bytes",
+    "embed_tokens", "qk_norm_rope", "prompt_attention", "prefix_attention",
     "device_error", "Layer", "Dims",
     "stream_handle",
 ]
@@ -216,6 +217,184 @@ def kv_attention(q, k_cache, v_cache, n_q_heads: int, n_kv_heads: int, head_dim:
         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         stream_handle(stream)))
     return y
+
+
+# ------------------------------------------------------------ prompts and batches
+def _here(t: torch.Tensor, name: str) -> None:
+    """Refuses a tensor of another device than the one the call launches on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _heads(t: torch.Tensor, name: str, heads: int | None = None, head_dim: int | None = None):
+    """qws_heads of a [tokens, heads, head_dim] f32 view; its last dimension is dense."""
+    _here(t, name)
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.dim() != 3 or (heads is not None and (t.shape[1] != heads or t.shape[2] != head_dim)):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {head_dim or 'head_dim'}], "
+                         f"got {tuple(t.shape)}")
+    a, b, c = t.stride()
+    if c != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+    return _lib.QwsHeads(t.data_ptr(), a if t.shape[0] > 1 else 0, b if t.shape[1] > 1 else 0)
+
+
+def _vec(t, name: str, dtype: torch.dtype, n: int) -> int:
+    _here(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _host_ints(v, name: str):
+    """A ctypes int64 array of a list, tuple or CPU tensor of whole numbers."""
+    if isinstance(v, torch.Tensor):
+        if v.is_cuda or v.dim() != 1 or v.is_floating_point():
+            raise TypeError(f"{name} must be a list or a 1-d CPU integer tensor: the lengths are "
+                            "read on the host")
+        v = v.tolist()
+    return (C.c_int64 * len(v))(*v)
+
+
+def _workspace(need: int, workspace, like: torch.Tensor, stream):
+    """(tensor, bytes) of the caller's workspace, or of a fresh one kept for the stream."""
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    else:
+        _here(workspace, "workspace")
+        _dev(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _new(shape, like: torch.Tensor, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=torch.float32, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def embed_tokens(fmt: int, W, tokens, vocab: int, hidden: int, scale: float = 1.0, out=None,
+                 stream=None):
+    """out [n, hidden] = scale * rows `tokens` (int64, [n]) of the quantised table W (uint8,
+    vocab rows).  A token outside the table gives zeros and sets device_error() bit 512."""
+    _here(W, "W")
+    n = tokens.numel()
+    block, size = {Q4_0: (32, 18), Q8_0: (32, 34), Q4_K: (256, 144), Q6_K: (256, 210)}.get(
+        fmt, (1, 0))
+    if W.numel() < vocab * (hidden // block) * size:
+        raise ValueError(f"W has {W.numel()} bytes, {vocab} rows of {hidden} need "
+                         f"{vocab * (hidden // block) * size}")
+    out = _new((n, hidden), W, stream) if out is None else out
+    check(lib().qws_embed_tokens(fmt, _dev(W, "W", torch.uint8),
+                                 _vec(tokens, "tokens", torch.int64, n),
+                                 _vec(out, "out", torch.float32, n * hidden), vocab, hidden, n,
+                                 float(scale), stream_handle(stream)) if n else 0)
+    return out
+
+
+def qk_norm_rope(q, k, positions, rot_dim: int, base: float, w_q=None, w_k=None,
+                 eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [T, n_q, hd] and k [T, n_kv, hd] (w_q, w_k [hd]; None: no
+    norm) and its rotation at positions [T] (int64).  Strided views welcome; q_out / k_out may
+    be q / k themselves, or for k a view of a cache.  Returns (q_out, k_out)."""
+    qh, kh = _heads(q, "q"), _heads(k, "k")
+    n, n_q, hd = q.shape
+    n_kv = k.shape[1]
+    if k.shape[0] != n or k.shape[2] != hd:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not match")
+    q_out = _new(q.shape, q, stream) if q_out is None else q_out
+    k_out = _new(k.shape, k, stream) if k_out is None else k_out
+    qo, ko = _heads(q_out, "q_out", n_q, hd), _heads(k_out, "k_out", n_kv, hd)
+    if q_out.shape[0] != n or k_out.shape[0] != n:
+        raise ValueError(f"q_out and k_out must have {n} tokens")
+    if n:
+        check(lib().qws_qk_norm_rope(
+            C.byref(qh), C.byref(kh), C.byref(qo), C.byref(ko),
+            None if w_q is None else _vec(w_q, "w_q", torch.float32, hd),
+            None if w_k is None else _vec(w_k, "w_k", torch.float32, hd),
+            _vec(positions, "positions", torch.int64, n), n, n_q, n_kv, hd, rot_dim, float(base),
+            float(eps), stream_handle(stream)))
+    return q_out, k_out
+
+
+def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu_seqlens_k=None,
+                     workspace=None, out=None, stream=None):
+    """Causal attention of packed sequences: q [T, n_q, hd], k and v [Tk, n_kv, hd], sequence s
+    at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (host integers) of q, and of k and v, or at
+    cu_seqlens_k there; its last query sees all of its keys.  Rows of out behind the last
+    sequence are left as they were."""
+    qh = _heads(q, "q")
+    n_q, hd = q.shape[1], q.shape[2]
+    n_kv = k.shape[1]
+    kh, vh = _heads(k, "k", n_kv, hd), _heads(v, "v", n_kv, hd)
+    cu = _host_ints(cu_seqlens, "cu_seqlens")
+    ck = cu if cu_seqlens_k is None else _host_ints(cu_seqlens_k, "cu_seqlens_k")
+    n = len(cu) - 1
+    if n < 0 or len(ck) != n + 1:
+        raise ValueError("cu_seqlens (and cu_seqlens_k) hold one offset more than sequences")
+    if max(cu) > q.shape[0] or max(ck) > min(k.shape[0], v.shape[0]):
+        raise ValueError("the offsets pass the end of q, k or v")
+    out = _new(q.shape, q, stream) if out is None else out
+    oh = _heads(out, "out", n_q, hd)
+    if max(cu) > out.shape[0]:
+        raise ValueError("the offsets pass the end of out")
+    if cu[0] == cu[n]:
+        return out
+    L = lib()
+    ws, nbytes = _workspace(
+        L.qws_prompt_attention_workspace_bytes(cu, ck, n, n_q, n_kv, hd), workspace, q, stream)
+    check(L.qws_prompt_attention(
+        C.byref(qh), C.byref(kh), C.byref(vh), C.byref(oh), cu, ck, n, n_q, n_kv, hd,
+        float(scale), float(softcap), None if ws is None else ws.data_ptr(), nbytes,
+        stream_handle(stream)))
+    return out
+
+
+def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n_ctx,
+                     scale: float, softcap: float = 0.0, workspace=None, out=None, stream=None):
+    """One decode step of a batch, q [B, n_q, hd]: row b attends to positions 0 .. n_prefix - 1
+    of the shared caches [n_kv, max_prefix, hd] and then to 0 .. n_ctx[b] - 1 (host integers)
+    of its own, k_caches and v_caches [B, n_kv, max_seq, hd]."""
+    qh = _heads(q, "q")
+    B, n_q, hd = q.shape
+    n_kv = k_prefix.shape[0]
+    for t, name, dims in ((k_prefix, "k_prefix", 3), (v_prefix, "v_prefix", 3),
+                          (k_caches, "k_caches", 4), (v_caches, "v_caches", 4)):
+        _here(t, name)
+        if t.dim() != dims or t.shape[-1] != hd or t.shape[-3] != n_kv:
+            raise ValueError(f"{name} {tuple(t.shape)} does not match {n_kv} heads of {hd}")
+    if v_prefix.shape != k_prefix.shape or v_caches.shape != k_caches.shape:
+        raise ValueError("key and value caches must have the same shape")
+    lens = _host_ints(n_ctx, "n_ctx")
+    if len(lens) != B or k_caches.shape[0] != B:
+        raise ValueError(f"q has {B} rows, n_ctx {len(lens)}, the caches {k_caches.shape[0]}")
+    out = _new(q.shape, q, stream) if out is None else out
+    oh = _heads(out, "out", n_q, hd)
+    if out.shape[0] != B:
+        raise ValueError(f"out must have {B} rows")
+    if B == 0:
+        return out
+    L = lib()
+    ws, nbytes = _workspace(
+        L.qws_prefix_attention_workspace_bytes(n_prefix, lens, B, n_q, n_kv, hd), workspace, q,
+        stream)
+    check(L.qws_prefix_attention(
+        C.byref(qh), _dev(k_prefix, "k_prefix", torch.float32),
+        _dev(v_prefix, "v_prefix", torch.float32), k_prefix.shape[1], n_prefix,
+        _dev(k_caches, "k_caches", torch.float32), _dev(v_caches, "v_caches", torch.float32),
+        k_caches.shape[2], lens, C.byref(oh), B, n_q, n_kv, hd, float(scale), float(softcap),
+        None if ws is None else ws.data_ptr(), nbytes, stream_handle(stream)))
+    return out
 
 
 def q4k_ffn_gate_up_geglu(Wg, Wu, x, hidden: int, inter: int, out=None, stream=None):
