@@ -837,7 +837,8 @@ qws_status qws_device_error(unsigned* code) {
   if (e != cudaSuccess) return cuda_fail(e, "qws_device_error", "");
   *code = qws::read_clear_matvec_errors() | qws::read_clear_chain_errors() |
           qws::read_clear_prefill_errors() | qws::read_clear_attention_errors() |
-          qws::read_clear_batchmv_errors() | qws::read_clear_embed_errors();
+          qws::read_clear_batchmv_errors() | qws::read_clear_embed_errors() |
+          qws::read_clear_prompt_errors();
   return *code ? fail(QWS_ERR_TIMEOUT, "device error code 0x%x", *code) : ok();
 }
 

@@ -18,6 +18,7 @@ struct SeqTab {
   int q0[kMaxSeqs + 1];     // first query token of sequence s
   int k0[kMaxSeqs + 1];     // first key of sequence s
   int item[kMaxSeqs + 1];   // first work item of sequence s
+  int ktile[kMaxSeqs + 1];  // first 64-key tile of sequence s
 };
 
 // the sequence s with item[s] <= i < item[s + 1] (empty ones are skipped)
@@ -73,6 +74,10 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
+
+// Scores are kept in units of log 2 (times log2 e), so that weights are powers of
+// two of differences; running maxima of partial results too.
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float soft_cap(float s, float cap) {
   return cap > 0.f ? cap * tanhf(s / cap) : s;
@@ -150,12 +155,12 @@ struct RowTile {
       float p[kR];
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
-        float x = soft_cap((s[r][0] + s[r][1]) * scale, cap);
+        float x = soft_cap((s[r][0] + s[r][1]) * scale, cap) * kLog2e;
         if (t + lane >= vis[r]) x = -INFINITY;      // select: what is masked is not looked at
         const float mn = fmaxf(m[r], warp_max(x));
         const float base = mn == -INFINITY ? 0.f : mn;
-        const float alpha = expf(m[r] - base);
-        p[r] = expf(x - base);
+        const float alpha = exp2f(m[r] - base);
+        p[r] = exp2f(x - base);
         l[r] = fmaf(l[r], alpha, warp_sum(p[r]));
         m[r] = mn;
 #pragma unroll

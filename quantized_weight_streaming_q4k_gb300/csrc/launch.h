@@ -189,6 +189,7 @@ cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, cons
                                     const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
                                     int head_dim, float scale, float cap, void* ws,
                                     cudaStream_t st);
+unsigned read_clear_prompt_errors();
 // decode attention of a batch over a shared prefix (prefix.cu); n_ctx a host array
 size_t prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_ctx, int batch,
                                         int n_q, int n_kv, int head_dim);

@@ -134,16 +134,16 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
         float d = 0.f;
 #pragma unroll
         for (int j = 0; j < kPL; ++j) d = fmaf(q[h][j], k[i][j], d);
-        s[i] = t + i < kb ? soft_cap(warp_sum(d) * p.scale, p.cap) : -INFINITY;
+        s[i] = t + i < kb ? soft_cap(warp_sum(d) * p.scale, p.cap) * kLog2e : -INFINITY;
         mn = fmaxf(mn, s[i]);
       }
       const float base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = expf(m[h] - base);
+      const float alpha = exp2f(m[h] - base);
       float pr[kOwnKeys];
       l[h] *= alpha;
 #pragma unroll
       for (int i = 0; i < kOwnKeys; ++i) {
-        pr[i] = expf(s[i] - base);
+        pr[i] = exp2f(s[i] - base);
         l[h] += pr[i];
       }
 #pragma unroll
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
     const float base = M == -INFINITY ? 0.f : M;
     float a = 0.f, L = 0.f;
     for (int w = 0; w < kOwnWarps; ++w) {
-      const float f = expf(sm[w][h] - base);
+      const float f = exp2f(sm[w][h] - base);
       a = fmaf(sacc[w][h][c], f, a);
       L = fmaf(sl[w][h], f, L);
     }
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(128)
     const float mc = src[kHd], lc = src[kHd + 1];
     const float mn = fmaxf(m, mc);
     const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = expf(m - base), c = expf(mc - base);
+    const float a = exp2f(m - base), c = exp2f(mc - base);
     l = fmaf(l, a, lc * c);
 #pragma unroll
     for (int j = 0; j < kPL; ++j) acc[j] = fmaf(acc[j], a, x[j] * c);

@@ -7,10 +7,13 @@
 
 #include <algorithm>
 
+#include "attend_mma.cuh"
 #include "attend_rows.cuh"
 #include "launch.h"
 
 namespace qws {
+
+__device__ unsigned g_err_prompt;
 
 // ------------------------------------------------------------ work items
 // A tile is `rows` query rows of one kv head: tok = rows / group tokens with
@@ -22,6 +25,8 @@ namespace qws {
 struct PromptParams {
   qws_heads q, k, v, out;
   float* part;
+  uint8_t* packed;      // tensor-core form: packed key tiles [tile][kv head]
+  TileMeta* meta;
   int n_q, n_kv, group, tok, rows, chunk;
   float scale, cap;
   SeqTab seqs;
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(256)
     const float mc = src[kHd], lc = src[kHd + 1];
     const float mn = fmaxf(m, mc);
     const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = expf(m - base), b = expf(mc - base);
+    const float a = exp2f(m - base), b = exp2f(mc - base);
     l = fmaf(l, a, lc * b);
 #pragma unroll
     for (int j = 0; j < kPL; ++j) acc[j] = fmaf(acc[j], a, x[j] * b);
@@ -163,47 +168,246 @@ __global__ void __launch_bounds__(256)
                    lane, acc, l);
 }
 
+// ------------------------------------------------------------ tensor cores
+// Key tiles of every sequence and kv head, split and laid out once (they are
+// read by all of the sequence's query tiles).  grid (key tiles, n_kv).
+template <int kHd>
+__global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant__ PromptParams p) {
+  using Cfg = MmaCfg<kHd>;
+  extern __shared__ __align__(16) float smem[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tile = blockIdx.x, g = blockIdx.y;
+  const int s = find_seq(p.seqs.ktile, p.seqs.n, tile);
+  const int64_t key = p.seqs.k0[s] + static_cast<int64_t>(tile - p.seqs.ktile[s]) * kTileKeys;
+  const int n = static_cast<int>(min(static_cast<int64_t>(kTileKeys), p.seqs.k0[s + 1] - key));
+  const int64_t at = static_cast<int64_t>(tile) * p.n_kv + g;
+  pack_tile<Cfg>(p.k.data + key * p.k.token_stride + g * p.k.head_stride,
+                 p.v.data + key * p.v.token_stride + g * p.v.head_stride, p.k.token_stride,
+                 p.v.token_stride, n, p.packed + at * Cfg::kTile, p.meta + at, smem);
+}
+
+// One item per CTA: 128 rows of one kv head against its piece of the keys.
+template <int kHd>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    prompt_mma_kernel(const __grid_constant__ PromptParams p) {
+  using Cfg = MmaCfg<kHd>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  auto& sh = *reinterpret_cast<MmaShared<Cfg::kStages>*>(stages + Cfg::kStages * Cfg::kStage);
+  const PromptItem it = prompt_item(p, blockIdx.x);
+  pdl_launch_dependents();
+  if (it.piece >= it.pieces) return;
+  const int g = blockIdx.y;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
+  const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
+  const int64_t tile0 = p.seqs.ktile[it.s] + ka / kTileKeys;    // its packed tiles
+  if (threadIdx.x == 0) mma_init_barriers(sh, 1);
+  if (warp == 9) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  pdl_wait();
+  if (warp >= 8) {
+    regs_few();
+    if (warp == 8 && lane == 0) {
+      const uint64_t pol = l2_policy_evict_first();
+      int unit = 0;
+      bool ok = true;
+      auto load = [&](int j, int v, int h) {     // v: 0 K, 1 V half h of tile j
+        const int s = unit % Cfg::kStages;
+        const uint32_t ph = static_cast<uint32_t>(unit / Cfg::kStages) & 1u;
+        ok = ok && mbar_wait(&sh.empty[s], ph ^ 1u);
+        if (!ok) return;
+        const uint8_t* src = p.packed + ((tile0 + j) * p.n_kv + g) * Cfg::kTile +
+                             (v ? Cfg::kNH * Cfg::kKUnit + h * Cfg::kVUnit : h * Cfg::kKUnit);
+        const uint32_t bytes = v ? Cfg::kVUnit : Cfg::kKUnit;
+        mbar_arrive_expect_tx(&sh.full[s], bytes);
+        bulk_copy_g2s(stages + s * Cfg::kStage, src, bytes, &sh.full[s], pol);
+        ++unit;
+      };
+      auto load_meta = [&](int j) {
+        const int s = j & 1;
+        ok = ok && mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta));
+        bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g, sizeof(TileMeta),
+                      &sh.meta_full[s], pol);
+      };
+      int metas = 0;
+      if (n > 0) {
+        load_meta(metas++);
+        for (int h = 0; h < Cfg::kNH; ++h) load(0, 0, h);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n) load_meta(metas++);
+        for (int h = 0; h < Cfg::kNH; ++h) {
+          if (j + 1 < n) load(j + 1, 0, h);
+          load(j, 1, h);
+        }
+      }
+      if (!ok) atomicOr(&g_err_prompt, kErrAttLoad);
+      // do not leave with copies into shared memory in flight
+      for (int u = max(0, unit - Cfg::kStages); u < unit; ++u)
+        if (!mbar_wait(&sh.full[u % Cfg::kStages], static_cast<uint32_t>(u / Cfg::kStages) & 1u))
+          atomicOr(&g_err_prompt, kErrAttLoad);
+    }
+    if (warp == 9 && lane == 0) mma_issue<Cfg>(sh, stages, tmem, n, &g_err_prompt);
+  } else {
+    regs_many();
+    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    const int live = it.n_tok * p.group;
+    const bool alive = row < live;
+    const int r = min(row, live - 1);
+    const int i = it.i0 + r / p.group, h = g * p.group + r % p.group;
+    const int64_t token = p.seqs.q0[it.s] + i;
+    const float* q = p.q.data + token * p.q.token_stride + h * p.q.head_stride;
+    const int vis = visible(i, it.n_q, it.n_k) - ka;
+    RowState<Cfg> st;
+    bool dead;
+    mma_rows<Cfg>(sh, tmem, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
+                  p.scale, p.cap, st, dead);
+    if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
+    if (st.any_left_out && alive) {
+      for (int j = 0; j < n; ++j) {
+        const TileMeta& m = p.meta[(tile0 + j) * p.n_kv + g];
+        for (int t = 0; t < kTileKeys; ++t) {
+          if (!((m.left_out[t >> 5] >> (t & 31)) & 1u) || j * kTileKeys + t >= vis) continue;
+          const int64_t key = p.seqs.k0[it.s] + ka + j * kTileKeys + t;
+          add_left_out<Cfg>(st, q, p.k.data + key * p.k.token_stride + g * p.k.head_stride,
+                            p.v.data + key * p.v.token_stride + g * p.v.head_stride, half,
+                            p.scale, p.cap);
+        }
+      }
+    }
+    if (alive && !dead) {
+      constexpr float kUnshift = 1.0f / (1 << kPShift);
+      if (it.pieces > 1) {
+        float* dst =
+            p.part + (part_slot(p, it, it.piece, g) * p.rows + row) * (kHd + kPartPad);
+        store_columns<Cfg>(st, dst, half, kUnshift);
+        if (half == 0) {
+          dst[kHd] = st.m;
+          dst[kHd + 1] = st.l * kUnshift;
+        }
+      } else {
+        store_columns<Cfg>(st, p.out.data + token * p.out.token_stride + h * p.out.head_stride,
+                           half, st.l == 0.f ? 0.f : 1.0f / st.l);
+      }
+    }
+  }
+  // every MMA has completed before tensor memory is freed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    if (lane == 0 && !mbar_wait(&sh.done, 0)) atomicOr(&g_err_prompt, kErrAttMma);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------ host side
 namespace {
 
+constexpr int64_t kMmaFrom = 1 << 18;
+
 struct PromptPlan {
+  bool mma;             // on the tensor cores
   int rows, tok, chunk;
-  int64_t items;        // work items per kv head of the largest launch
   bool split;           // some tile has several pieces
+  int64_t items, ktiles;        // per kv head, of the largest launch
+  size_t packed_bytes, meta_bytes, part_bytes;
 };
 
-// The tile and piece lengths of a call, and the workspace of its partials.
-PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int group) {
-  PromptPlan pl;
-  pl.rows = 4 * kRowWarps;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The form, tile and piece lengths of a call, and the sizes of its workspace.
+PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
+                       int head_dim) {
+  PromptPlan pl = {};
+  const int group = n_q / n_kv;
+  // (row, key) pairs that are scored, per kv head, counted in whole rows
+  int64_t pairs = 0;
+  for (int s = 0; s < n_seqs; ++s) {
+    const int64_t nq = cu_q[s + 1] - cu_q[s], nk = cu_k[s + 1] - cu_k[s];
+    pairs += nq * group * std::max<int64_t>(1, nk - std::min(nq, nk) / 2);
+  }
+  pl.mma = pairs * n_kv > kMmaFrom;
+  pl.rows = pl.mma ? kTileRows : 4 * kRowWarps;
   pl.tok = pl.rows / group;
   pl.chunk = 512;
-  pl.items = 0;
-  pl.split = false;
+  if (pl.mma) {
+    // about eight pieces an SM, of at least 8 tiles
+    const int64_t tiles = pairs / (kTileRows * kTileKeys) * n_kv;
+    pl.chunk = static_cast<int>(std::max<int64_t>(8, ceil_div(tiles, 8 * 152))) * kTileKeys;
+  }
   for (int s0 = 0; s0 < n_seqs; s0 += kMaxSeqs) {
-    int64_t items = 0;
+    int64_t items = 0, ktiles = 0;
     for (int s = s0; s < std::min(n_seqs, s0 + kMaxSeqs); ++s) {
       const int64_t nq = cu_q[s + 1] - cu_q[s], nk = cu_k[s + 1] - cu_k[s];
       if (nq == 0) continue;
-      const int64_t pieces = std::max<int64_t>(1, (nk + pl.chunk - 1) / pl.chunk);
-      items += (nq + pl.tok - 1) / pl.tok * pieces;
+      const int64_t pieces = std::max<int64_t>(1, ceil_div(nk, pl.chunk));
+      items += ceil_div(nq, pl.tok) * pieces;
+      ktiles += ceil_div(nk, kTileKeys);
       pl.split = pl.split || pieces > 1;
     }
     pl.items = std::max(pl.items, items);
+    pl.ktiles = std::max(pl.ktiles, ktiles);
   }
+  const auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
+  if (pl.mma) {
+    const size_t tile = head_dim == 32   ? MmaCfg<32>::kTile
+                        : head_dim == 64 ? MmaCfg<64>::kTile
+                        : head_dim == 128 ? MmaCfg<128>::kTile
+                                          : MmaCfg<256>::kTile;
+    pl.packed_bytes = pad(static_cast<size_t>(pl.ktiles) * n_kv * tile);
+    pl.meta_bytes = pad(static_cast<size_t>(pl.ktiles) * n_kv * sizeof(TileMeta));
+  }
+  if (pl.split)
+    pl.part_bytes = pad(static_cast<size_t>(pl.items) * n_kv * pl.rows *
+                        (head_dim + kPartPad) * sizeof(float));
   return pl;
 }
 
 template <int kPL>
-cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, cudaStream_t st) {
-  using Tile = RowTile<kPL, 4>;
-  cudaError_t e = cudaFuncSetAttribute(prompt_rows_kernel<kPL, 4>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(Tile::kSmem));
-  if (e != cudaSuccess) return e;
-  e = pdl_launch(prompt_rows_kernel<kPL, 4>,
-                 dim3(static_cast<unsigned>(items), static_cast<unsigned>(p.n_kv)), kRowThreads,
-                 Tile::kSmem, st, p);
+cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int64_t ktiles,
+                       cudaStream_t st) {
+  constexpr int kHd = kPL * 32;
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(p.n_kv));
+  cudaError_t e;
+  if (pl.mma) {
+    using Cfg = MmaCfg<kHd>;
+    constexpr size_t kPackSmem = sizeof(float) * kTileKeys * (kHd + 1);
+    constexpr size_t kSmem = 1024 + Cfg::kStages * Cfg::kStage + sizeof(MmaShared<Cfg::kStages>);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    if (ktiles > 0) {
+      e = cudaFuncSetAttribute(prompt_pack_kernel<kHd>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kPackSmem));
+      if (e != cudaSuccess) return e;
+      e = pdl_launch(prompt_pack_kernel<kHd>,
+                     dim3(static_cast<unsigned>(ktiles), static_cast<unsigned>(p.n_kv)), 256,
+                     kPackSmem, st, p);
+      if (e != cudaSuccess) return e;
+    }
+    e = cudaFuncSetAttribute(prompt_mma_kernel<kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(prompt_mma_kernel<kHd>, grid, kMmaThreads, kSmem, st, p);
+  } else {
+    using Tile = RowTile<kPL, 4>;
+    e = cudaFuncSetAttribute(prompt_rows_kernel<kPL, 4>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(Tile::kSmem));
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(prompt_rows_kernel<kPL, 4>, grid, kRowThreads, Tile::kSmem, st, p);
+  }
   if (e != cudaSuccess || !pl.split) return e;
   const int64_t rows = static_cast<int64_t>(p.seqs.q0[p.seqs.n] - p.seqs.q0[0]) * p.n_q;
   return pdl_launch(prompt_merge_kernel<kPL>, dim3(static_cast<unsigned>((rows + 7) / 8)), 256,
@@ -214,9 +418,8 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, cud
 
 size_t prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k, int n_seqs,
                                         int n_q, int n_kv, int head_dim) {
-  const PromptPlan pl = plan_prompt(cu_q, cu_k, n_seqs, n_q / n_kv);
-  if (!pl.split) return 0;
-  return static_cast<size_t>(pl.items) * n_kv * pl.rows * (head_dim + kPartPad) * sizeof(float);
+  const PromptPlan pl = plan_prompt(cu_q, cu_k, n_seqs, n_q, n_kv, head_dim);
+  return pl.packed_bytes + pl.meta_bytes + pl.part_bytes;
 }
 
 cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
@@ -224,37 +427,48 @@ cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, cons
                                     const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
                                     int head_dim, float scale, float cap, void* ws,
                                     cudaStream_t st) {
-  const PromptPlan pl = plan_prompt(cu_q, cu_k, n_seqs, n_q / n_kv);
+  const PromptPlan pl = plan_prompt(cu_q, cu_k, n_seqs, n_q, n_kv, head_dim);
   PromptParams p;
   p.q = q; p.k = k; p.v = v; p.out = out;
-  p.part = static_cast<float*>(ws);
+  p.packed = static_cast<uint8_t*>(ws);
+  p.meta = reinterpret_cast<TileMeta*>(p.packed + pl.packed_bytes);
+  p.part = reinterpret_cast<float*>(p.packed + pl.packed_bytes + pl.meta_bytes);
   p.n_q = n_q; p.n_kv = n_kv; p.group = n_q / n_kv;
   p.tok = pl.tok; p.rows = pl.rows; p.chunk = pl.chunk;
   p.scale = scale; p.cap = cap;
   for (int s0 = 0; s0 < n_seqs; s0 += kMaxSeqs) {
     SeqTab& t = p.seqs;
     t.n = std::min(n_seqs - s0, kMaxSeqs);
-    int64_t items = 0;
+    int64_t items = 0, ktiles = 0;
     for (int s = 0; s <= t.n; ++s) {
       t.q0[s] = static_cast<int>(cu_q[s0 + s]);
       t.k0[s] = static_cast<int>(cu_k[s0 + s]);
       t.item[s] = static_cast<int>(items);
+      t.ktile[s] = static_cast<int>(ktiles);
       if (s == t.n) break;
       const int64_t nq = cu_q[s0 + s + 1] - cu_q[s0 + s], nk = cu_k[s0 + s + 1] - cu_k[s0 + s];
-      if (nq)
-        items += (nq + pl.tok - 1) / pl.tok * std::max<int64_t>(1, (nk + pl.chunk - 1) / pl.chunk);
+      if (nq == 0) continue;
+      items += ceil_div(nq, pl.tok) * std::max<int64_t>(1, ceil_div(nk, pl.chunk));
+      ktiles += ceil_div(nk, kTileKeys);
     }
     if (items == 0) continue;
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 32: e = run_prompt<1>(p, pl, items, st); break;
-      case 64: e = run_prompt<2>(p, pl, items, st); break;
-      case 128: e = run_prompt<4>(p, pl, items, st); break;
-      case 256: e = run_prompt<8>(p, pl, items, st); break;
+      case 32: e = run_prompt<1>(p, pl, items, ktiles, st); break;
+      case 64: e = run_prompt<2>(p, pl, items, ktiles, st); break;
+      case 128: e = run_prompt<4>(p, pl, items, ktiles, st); break;
+      case 256: e = run_prompt<8>(p, pl, items, ktiles, st); break;
     }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+unsigned read_clear_prompt_errors() {
+  unsigned v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_prompt, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_err_prompt, &z, sizeof(z));
+  return v;
 }
 
 }  // namespace qws
