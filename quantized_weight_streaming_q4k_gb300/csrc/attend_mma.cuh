@@ -22,7 +22,7 @@
 // products per value leave time for (256 of about 3000 cycles a tile at head_dim
 // 256).  This also spares the correction pass over tensor memory.
 //
-// TMEM columns (of 512): Q hi 0.., Q lo 128.., S 256.., P hi 320.., P lo 352..,
+// TMEM columns (all 512 are allocated, so they start at 0): Q hi 0.., Q lo 128.., S 256.., P hi 320.., P lo 352..,
 // O_tile 384.. (128 columns: at head_dim 256 the two halves of O_tile take turns).
 //
 // Roles (12 warps, two idle): warps 0..7 softmax and output (thread = row 32 (w % 4) + lane,
@@ -158,73 +158,85 @@ __device__ __forceinline__ void mma_init_barriers(MmaShared<kStages>& sh, uint32
 }
 
 // ------------------------------------------------------------ the MMA issuer
-// One thread.  Units arrive in the order they are used: K halves of tile 0, then
+// A whole warp.  Units arrive in the order they are used: K halves of tile 0, then
 // for every tile j and half h: K half h of tile j + 1, V half h of tile j.
 template <class Cfg>
-__device__ __forceinline__ void mma_issue(MmaShared<Cfg::kStages>& sh, uint8_t* stages,
-                                          uint32_t tmem, int n, unsigned* err) {
+__device__ __forceinline__ void mma_issue(MmaShared<Cfg::kStages>& sh, uint8_t* stages, int n,
+                                          unsigned* err) {
   constexpr uint32_t kIdescQk = tc_idesc_f16(kTileRows, kTileKeys);
   constexpr uint32_t kIdescPv = tc_idesc_f16(kTileRows, Cfg::kHC);
-  int unit = 0;
-  bool ok = n == 0 || mbar_wait(&sh.q_ready, 0);
-  tc_fence_after();
-  auto stage_of = [&](int u) { return u % Cfg::kStages; };
-  auto wait_unit = [&]() {
-    ok = ok && mbar_wait(&sh.full[stage_of(unit)],
-                         static_cast<uint32_t>(unit / Cfg::kStages) & 1u);
-    tc_fence_after();
+  const uint32_t one = elect_one();
+  const uint32_t base = sw128_lo(smem_addr(stages));   // units of 16 bytes
+  int unit = 0, stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  auto next = [&]() {
+    ++unit;
+    if (++stage == Cfg::kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
   };
   auto qk = [&](int j, int h) {
-    if (h == 0 && j > 0)
-      ok = ok && mbar_wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
-    wait_unit();
+    if (h == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
+    wait(&sh.full[stage], phase);
+    tc_fence_after();
     if (!ok) return;
-    const uint32_t b = smem_addr(stages + stage_of(unit) * Cfg::kStage);
+    const uint32_t b = base + static_cast<uint32_t>(stage) * (Cfg::kStage >> 4);
     // the small cross terms first: what is rounded off them is smaller still
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
 #pragma unroll
       for (int k = 0; k < Cfg::kQkSteps; ++k) {
-        const uint32_t a = tmem + (t == 1 ? kTmQlo : kTmQhi) +
-                           static_cast<uint32_t>(h * Cfg::kQkSteps + k) * 8u;
-        const uint32_t bk = b + (t == 0 ? Cfg::kKPart : 0u) +
-                            static_cast<uint32_t>(k / 4) * 8192u + static_cast<uint32_t>(k % 4) * 32u;
-        tc_mma_f16_ts(tmem + kTmS, a, sw128_desc(bk), kIdescQk, (h | t | k) != 0 ? 1u : 0u);
+        const uint32_t a =
+            (t == 1 ? kTmQlo : kTmQhi) + static_cast<uint32_t>(h * Cfg::kQkSteps + k) * 8u;
+        const uint32_t off = (t == 0 ? Cfg::kKPart : 0u) + static_cast<uint32_t>(k / 4) * 8192u +
+                             static_cast<uint32_t>(k % 4) * 32u;
+        tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdescQk, (h | t | k) != 0 ? 1u : 0u, one);
       }
     }
-    tc_commit(&sh.empty[stage_of(unit)]);
-    if (h == Cfg::kNH - 1) tc_commit(&sh.s_full);
-    ++unit;
+    tc_commit(&sh.empty[stage], one);
+    if (h == Cfg::kNH - 1) tc_commit(&sh.s_full, one);
+    next();
   };
   auto pv = [&](int j, int h) {
     const int use = j * Cfg::kNH + h;
-    if (h == 0) ok = ok && mbar_wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);
-    if (use > 0) ok = ok && mbar_wait(&sh.o_free, static_cast<uint32_t>(use - 1) & 1u);
-    wait_unit();
+    if (h == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);
+    if (use > 0) wait(&sh.o_free, static_cast<uint32_t>(use - 1) & 1u);
+    wait(&sh.full[stage], phase);
+    tc_fence_after();
     if (!ok) return;
-    const uint32_t b = smem_addr(stages + stage_of(unit) * Cfg::kStage);
+    const uint32_t b = base + static_cast<uint32_t>(stage) * (Cfg::kStage >> 4);
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
 #pragma unroll
       for (int k = 0; k < kTileKeys / 16; ++k) {
-        const uint32_t a = tmem + (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
-        const uint32_t bk = b + (t == 0 ? Cfg::kVPart : 0u) + static_cast<uint32_t>(k) * 32u;
-        tc_mma_f16_ts(tmem + kTmO, a, sw128_desc(bk), kIdescPv, (t | k) != 0 ? 1u : 0u);
+        const uint32_t a = (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
+        const uint32_t off = (t == 0 ? Cfg::kVPart : 0u) + static_cast<uint32_t>(k) * 32u;
+        tc_mma_f16_ts(kTmO, a, b + (off >> 4), kIdescPv, (t | k) != 0 ? 1u : 0u, one);
       }
     }
-    tc_commit(&sh.empty[stage_of(unit)]);
-    tc_commit(&sh.o_full);
-    ++unit;
+    tc_commit(&sh.empty[stage], one);
+    tc_commit(&sh.o_full, one);
+    next();
   };
-  if (n > 0)
+  if (n > 0) {
+    wait(&sh.q_ready, 0);
+#pragma unroll
     for (int h = 0; h < Cfg::kNH; ++h) qk(0, h);
-  for (int j = 0; j < n && ok; ++j)
+  }
+  for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
     for (int h = 0; h < Cfg::kNH; ++h) {
       if (j + 1 < n) qk(j + 1, h);
       pv(j, h);
     }
-  if (!ok) atomicOr(err, kErrAttMma);
-  tc_commit(&sh.done);     // arrives when every MMA above has completed
+  }
+  if (!ok && one) atomicOr(err, kErrAttMma);
+  tc_commit(&sh.done, one);     // arrives when every MMA above has completed
 }
 
 // ------------------------------------------------------------ softmax and output
@@ -264,13 +276,12 @@ __device__ __forceinline__ void drain_o(MmaShared<Cfg::kStages>& sh, uint32_t t_
 // below vis (relative to the first key of tile 0 of the run); all_vis: a bound
 // below which every row of the CTA sees every key.
 template <class Cfg>
-__device__ __forceinline__ void mma_rows(MmaShared<Cfg::kStages>& sh, uint32_t tmem,
-                                         const float* q, int n, int vis, int all_vis, float scale,
+__device__ __forceinline__ void mma_rows(MmaShared<Cfg::kStages>& sh, const float* q, int n, int vis, int all_vis, float scale,
                                          float cap, RowState<Cfg>& st, bool& dead) {
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int quad = warp & 3, half = warp >> 2;
   const int row = 32 * quad + lane;
-  const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quad) << 16);
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
   dead = false;
   st.m = -INFINITY;
   st.l = 0.f;

@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   pdl_wait();
   if (warp >= 8) {
     regs_few();
@@ -257,7 +256,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         if (!mbar_wait(&sh.full[u % Cfg::kStages], static_cast<uint32_t>(u / Cfg::kStages) & 1u))
           atomicOr(&g_err_prompt, kErrAttLoad);
     }
-    if (warp == 9 && lane == 0) mma_issue<Cfg>(sh, stages, tmem, n, &g_err_prompt);
+    if (warp == 9) mma_issue<Cfg>(sh, stages, n, &g_err_prompt);
   } else {
     regs_many();
     const int row = 32 * (warp & 3) + lane, half = warp >> 2;
@@ -270,7 +269,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const int vis = visible(i, it.n_q, it.n_k) - ka;
     RowState<Cfg> st;
     bool dead;
-    mma_rows<Cfg>(sh, tmem, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
+    mma_rows<Cfg>(sh, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
                   p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
     if (st.any_left_out && alive) {
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     if (lane == 0 && !mbar_wait(&sh.done, 0)) atomicOr(&g_err_prompt, kErrAttMma);
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(sh.tmem, 512);
   }
 }
 
