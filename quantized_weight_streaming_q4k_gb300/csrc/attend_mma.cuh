@@ -22,14 +22,18 @@
 // products per value leave time for (256 of about 3000 cycles a tile at head_dim
 // 256).  This also spares the correction pass over tensor memory.
 //
-// TMEM columns (all 512 are allocated, so they start at 0): Q hi 0.., Q lo 128.., S 256.., P hi 320.., P lo 352..,
-// O_tile 384.. (128 columns: at head_dim 256 the two halves of O_tile take turns).
+// TMEM columns (all 512 are allocated, so they start at 0): Q hi 0.., Q lo 128..,
+// S 256.., P hi 320.., P lo 352.., O_tile 384.. and 448.. (64 columns each: the 64-column
+// chunks of O_tile take turns).
 //
-// Roles (12 warps, two idle): warps 0..7 softmax and output (thread = row 32 (w % 4) + lane,
-// w / 4 = which half of the tile's keys and of the output columns), warp 8 loads, warp 9
-// issues the MMAs in the order QK_a(j+1), PV_0(j), QK_b(j+1), PV_1(j), (a, b and
-// 0, 1: halves of head_dim), so that the softmax of a tile and both drains of
-// O_tile each have a segment of other MMAs to hide behind.
+// Roles: 4 * kSplit softmax warps (thread = row 32 (w % 4) + lane, w / 4 = which part of
+// the tile's keys and of the output columns) and four helper warps: two load K and V
+// chunks into their rings, two issue the MMAs of Q K^T and of P V.  One issuing warp
+// would do, but a commit holds the issuing warp until its MMAs are done, and the tensor
+// cores then idle for the next wait; with two, one's MMAs are queued behind the other's.
+// A softmax warp turns S(j+1) into weights before it drains O_tile(j), so that Q K(j+2)^T
+// and P V(j) run behind it; the chunks of O_tile alternate between two accumulators, so
+// that a chunk is drained while the next is multiplied.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -48,14 +52,6 @@ enum : unsigned {
 
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
-constexpr int kConsumers = 256;
-constexpr int kMmaThreads = kConsumers + 128;   // whole warpgroups, for the register split
-// Registers a thread: the launch gives 168 x 384 = 64512; the last warpgroup keeps 56, the
-// softmax warpgroups take 224 (2 x 128 x 224 + 128 x 56 = 64512, no more than launched).
-__device__ __forceinline__ void regs_few() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
-__device__ __forceinline__ void regs_many() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-}
 constexpr int kPShift = 14;            // weights are 2^14 exp2(s - max)
 
 // what a key tile carries beside its values
@@ -67,33 +63,57 @@ struct __align__(16) TileMeta {
 };
 static_assert(sizeof(TileMeta) == 272, "copied in 16-byte units");
 
-template <int kHdT>
+// A unit: 64 keys x 64 columns of K, or 64 channels x 64 keys of V^T, hi then lo,
+// rows of 128 bytes.
+template <int kHdT, int kSplitT>
 struct MmaCfg {
   static constexpr int kHd = kHdT;
-  static constexpr int kNH = kHd > 128 ? 2 : 1;         // halves of head_dim
-  static constexpr int kHC = kHd / kNH;                 // columns of a half
-  static constexpr int kOC = kHC / 2;                   // of these, a thread's
-  static constexpr int kChunks = (kHC + 63) / 64;       // 64-column runs of a K unit
-  static constexpr int kQkSteps = kHC / 16;
-  static constexpr uint32_t kKPart = kChunks * 8192u;   // hi or lo of a K unit
-  static constexpr uint32_t kVPart = kHC * 128u;        // hi or lo of a V unit
+  static constexpr int kSplit = kSplitT;                // threads of a query row
+  static constexpr int kNC = kHd > 64 ? kHd / 64 : 1;   // chunks of head_dim
+  static constexpr int kHC = kHd / kNC;                 // columns of a chunk
+  static constexpr int kKeys = kTileKeys / kSplit;      // of a tile, a thread's
+  static constexpr int kOC = kHC / kSplit;              // of a chunk, a thread's
+  static constexpr uint32_t kKPart = 64 * 128;          // hi or lo of a K unit
+  static constexpr uint32_t kVPart = kHC * 128;         // hi or lo of a V unit
   static constexpr uint32_t kKUnit = 2 * kKPart, kVUnit = 2 * kVPart;
-  static constexpr uint32_t kTile = kNH * (kKUnit + kVUnit);   // a packed key tile
-  static constexpr uint32_t kStage = kKUnit > kVUnit ? kKUnit : kVUnit;
-  static constexpr int kStages = 6;
+  static constexpr uint32_t kTile = kNC * (kKUnit + kVUnit);   // a packed key tile
+  static constexpr int kStages = 6;                     // of each ring
+  static constexpr uint32_t kRing = kStages * (kKUnit + kVUnit);
+  // softmax warps, then the helpers
+  static constexpr int kRowsWarps = 4 * kSplit;
+  static constexpr int kLoadK = kRowsWarps, kLoadV = kRowsWarps + 1;
+  static constexpr int kMmaQk = kRowsWarps + 2, kMmaPv = kRowsWarps + 3;
+  static constexpr int kThreads = 32 * (kRowsWarps + 4);
+  // Registers: a scheduler's quarter of the file (16384) holds 3 (5 for kSplit = 4)
+  // warps, 168 (96) a thread at launch; the helpers keep few and the softmax warps
+  // take what that frees: 2 x 224 + 56 = 3 x 168, 4 x 112 + 32 = 5 x 96.
+  static_assert(kSplit == 2 || kSplit == 4, "register split");
 };
+
+template <class Cfg>
+__device__ __forceinline__ void regs_few() {
+  if constexpr (Cfg::kSplit == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+}
+template <class Cfg>
+__device__ __forceinline__ void regs_many() {
+  if constexpr (Cfg::kSplit == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+}
 
 constexpr uint32_t kTmQhi = 0, kTmQlo = 128, kTmS = 256, kTmPhi = 320, kTmPlo = 352, kTmO = 384;
 
 // barriers and small exchanges of one CTA
-template <int kStages>
+template <class Cfg>
 struct MmaShared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t k_full[Cfg::kStages], k_empty[Cfg::kStages];
+  uint64_t v_full[Cfg::kStages], v_empty[Cfg::kStages];
   uint64_t meta_full[2], meta_free[2];
-  uint64_t q_ready, s_full, s_free, p_ready, o_full, o_free, done;
+  uint64_t o_full[2], o_free[2];
+  uint64_t q_ready, s_full, s_free, p_ready, done[2];
   uint32_t tmem;
   uint32_t pad;
-  float xmax[2][2][kTileRows];
+  float xmax[2][Cfg::kSplit][kTileRows];
   TileMeta meta[2];
 };
 
@@ -137,213 +157,261 @@ __device__ __forceinline__ bool finite_bits(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
 }
 
-template <int kStages>
-__device__ __forceinline__ void mma_init_barriers(MmaShared<kStages>& sh, uint32_t full_count) {
-  for (int s = 0; s < kStages; ++s) {
-    mbar_init(&sh.full[s], full_count);
-    mbar_init(&sh.empty[s], 1);
+template <class Cfg>
+__device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh) {
+  for (int s = 0; s < Cfg::kStages; ++s) {
+    mbar_init(&sh.k_full[s], 1);
+    mbar_init(&sh.k_empty[s], 1);
+    mbar_init(&sh.v_full[s], 1);
+    mbar_init(&sh.v_empty[s], 1);
   }
   for (int s = 0; s < 2; ++s) {
     mbar_init(&sh.meta_full[s], 1);
-    mbar_init(&sh.meta_free[s], kConsumers / 32);
+    mbar_init(&sh.meta_free[s], Cfg::kRowsWarps);
+    mbar_init(&sh.o_full[s], 1);
+    mbar_init(&sh.o_free[s], Cfg::kRowsWarps);
+    mbar_init(&sh.done[s], 1);
   }
-  mbar_init(&sh.q_ready, kConsumers / 32);
+  mbar_init(&sh.q_ready, Cfg::kRowsWarps);
   mbar_init(&sh.s_full, 1);
-  mbar_init(&sh.s_free, kConsumers / 32);
-  mbar_init(&sh.p_ready, kConsumers / 32);
-  mbar_init(&sh.o_full, 1);
-  mbar_init(&sh.o_free, kConsumers / 32);
-  mbar_init(&sh.done, 1);
+  mbar_init(&sh.s_free, Cfg::kRowsWarps);
+  mbar_init(&sh.p_ready, Cfg::kRowsWarps);
   fence_barrier_init();
 }
 
-// ------------------------------------------------------------ the MMA issuer
-// A whole warp.  Units arrive in the order they are used: K halves of tile 0, then
-// for every tile j and half h: K half h of tile j + 1, V half h of tile j.
-template <class Cfg>
-__device__ __forceinline__ void mma_issue(MmaShared<Cfg::kStages>& sh, uint8_t* stages, int n,
-                                          unsigned* err) {
-  constexpr uint32_t kIdescQk = tc_idesc_f16(kTileRows, kTileKeys);
-  constexpr uint32_t kIdescPv = tc_idesc_f16(kTileRows, Cfg::kHC);
-  const uint32_t one = elect_one();
-  const uint32_t base = sw128_lo(smem_addr(stages));   // units of 16 bytes
-  int unit = 0, stage = 0;
+// A place in a ring of kStages: stage and the parity of its current phase.
+template <int kStages>
+struct RingAt {
+  int stage = 0;
   uint32_t phase = 0;
-  bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-  };
-  auto next = [&]() {
-    ++unit;
-    if (++stage == Cfg::kStages) {
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
-  };
-  auto qk = [&](int j, int h) {
-    if (h == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
-    wait(&sh.full[stage], phase);
-    tc_fence_after();
-    if (!ok) return;
-    const uint32_t b = base + static_cast<uint32_t>(stage) * (Cfg::kStage >> 4);
-    // the small cross terms first: what is rounded off them is smaller still
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-#pragma unroll
-      for (int k = 0; k < Cfg::kQkSteps; ++k) {
-        const uint32_t a =
-            (t == 1 ? kTmQlo : kTmQhi) + static_cast<uint32_t>(h * Cfg::kQkSteps + k) * 8u;
-        const uint32_t off = (t == 0 ? Cfg::kKPart : 0u) + static_cast<uint32_t>(k / 4) * 8192u +
-                             static_cast<uint32_t>(k % 4) * 32u;
-        tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdescQk, (h | t | k) != 0 ? 1u : 0u, one);
-      }
-    }
-    tc_commit(&sh.empty[stage], one);
-    if (h == Cfg::kNH - 1) tc_commit(&sh.s_full, one);
-    next();
-  };
-  auto pv = [&](int j, int h) {
-    const int use = j * Cfg::kNH + h;
-    if (h == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);
-    if (use > 0) wait(&sh.o_free, static_cast<uint32_t>(use - 1) & 1u);
-    wait(&sh.full[stage], phase);
-    tc_fence_after();
-    if (!ok) return;
-    const uint32_t b = base + static_cast<uint32_t>(stage) * (Cfg::kStage >> 4);
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-#pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k) {
-        const uint32_t a = (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
-        const uint32_t off = (t == 0 ? Cfg::kVPart : 0u) + static_cast<uint32_t>(k) * 32u;
-        tc_mma_f16_ts(kTmO, a, b + (off >> 4), kIdescPv, (t | k) != 0 ? 1u : 0u, one);
-      }
-    }
-    tc_commit(&sh.empty[stage], one);
-    tc_commit(&sh.o_full, one);
-    next();
-  };
-  if (n > 0) {
-    wait(&sh.q_ready, 0);
-#pragma unroll
-    for (int h = 0; h < Cfg::kNH; ++h) qk(0, h);
   }
+};
+
+// ------------------------------------------------------------ the MMA issuers
+// Each a whole warp.  S(j) = Q K(j)^T, chunk after chunk of head_dim, once S(j-1) has
+// been read; of each chunk the small cross terms first.
+template <class Cfg>
+__device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring, int n,
+                                             unsigned* err) {
+  constexpr uint32_t kIdesc = tc_idesc_f16(kTileRows, kTileKeys);
+  constexpr int kSteps = Cfg::kHC / 16;
+  const uint32_t one = elect_one();
+  const uint32_t base = sw128_lo(smem_addr(k_ring));   // units of 16 bytes
+  RingAt<Cfg::kStages> at;
+  bool ok = true, there = false;       // there: this chunk's unit has been seen to land
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  if (n > 0) wait(&sh.q_ready, 0);
   for (int j = 0; j < n && ok; ++j) {
+#pragma unroll 1
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      if (!there) wait(&sh.k_full[at.stage], at.phase);
+      if (c == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
+      tc_fence_after();
+      if (!ok) break;
+      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kKUnit >> 4);
+      uint64_t* empty = &sh.k_empty[at.stage];
+      at.next();
+      const bool next = mbar_test(&sh.k_full[at.stage], at.phase);
 #pragma unroll
-    for (int h = 0; h < Cfg::kNH; ++h) {
-      if (j + 1 < n) qk(j + 1, h);
-      pv(j, h);
+      for (int t = 0; t < 3; ++t) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          const uint32_t a = (t == 1 ? kTmQlo : kTmQhi) + static_cast<uint32_t>(c * kSteps + k) * 8u;
+          const uint32_t off = (t == 0 ? Cfg::kKPart : 0u) + static_cast<uint32_t>(k) * 32u;
+          tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdesc, (c | t | k) != 0 ? 1u : 0u, one);
+        }
+      }
+      tc_commit(empty, one);
+      if (c == Cfg::kNC - 1) tc_commit(&sh.s_full, one);
+      there = __all_sync(0xFFFFFFFFu, next);
     }
   }
   if (!ok && one) atomicOr(err, kErrAttMma);
-  tc_commit(&sh.done, one);     // arrives when every MMA above has completed
+  tc_commit(&sh.done[0], one);     // arrives when every MMA above has completed
+}
+
+// O_tile(j) = P(j) V(j), a 64-column chunk at a time in one of two accumulators.
+template <class Cfg>
+__device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring, int n,
+                                             unsigned* err) {
+  constexpr uint32_t kIdesc = tc_idesc_f16(kTileRows, Cfg::kHC);
+  const uint32_t one = elect_one();
+  const uint32_t base = sw128_lo(smem_addr(v_ring));
+  RingAt<Cfg::kStages> at;
+  RingAt<2> buf;
+  bool ok = true, there = false;       // there: unit and accumulator seen to be ready
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  for (int j = 0; j < n && ok; ++j) {
+#pragma unroll 1
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      if (!there) {
+        wait(&sh.v_full[at.stage], at.phase);
+        wait(&sh.o_free[buf.stage], buf.phase ^ 1u);   // the first use of each passes
+      }
+      if (c == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);   // the last to come
+      tc_fence_after();
+      if (!ok) break;
+      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kVUnit >> 4);
+      const uint32_t d = kTmO + static_cast<uint32_t>(buf.stage) * 64u;
+      uint64_t *full = &sh.o_full[buf.stage], *empty = &sh.v_empty[at.stage];
+      at.next();
+      buf.next();
+      const bool next = mbar_test(&sh.v_full[at.stage], at.phase) &
+                        mbar_test(&sh.o_free[buf.stage], buf.phase ^ 1u);
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k) {
+          const uint32_t a = (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
+          const uint32_t off = (t == 0 ? Cfg::kVPart : 0u) + static_cast<uint32_t>(k) * 32u;
+          tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, (t | k) != 0 ? 1u : 0u, one);
+        }
+      }
+      tc_commit(full, one);
+      tc_commit(empty, one);
+      there = __all_sync(0xFFFFFFFFu, next);
+    }
+  }
+  if (!ok && one) atomicOr(err, kErrAttMma);
+  tc_commit(&sh.done[1], one);
+}
+
+// A loader: one thread.  Waits for a free stage before each of the n * kNC units;
+// copy(stage, j, c) starts the copy of chunk c of tile j; before(j) comes before a
+// tile's first, and returns false when it gave up.  Ends when its copies have landed.
+template <class Cfg, class Before, class Copy>
+__device__ __forceinline__ void mma_load(uint64_t* full, uint64_t* empty, int n, Before&& before,
+                                         Copy&& copy, unsigned* err) {
+  RingAt<Cfg::kStages> at;
+  bool ok = true;
+  int units = 0;
+  for (int j = 0; j < n && ok; ++j) {
+    ok = before(j);
+    for (int c = 0; c < Cfg::kNC && ok; ++c) {
+      ok = mbar_wait(&empty[at.stage], at.phase ^ 1u);
+      if (!ok) break;
+      copy(at.stage, j, c);
+      at.next();
+      ++units;
+    }
+  }
+  for (int u = max(0, units - Cfg::kStages); u < units; ++u)
+    ok = mbar_wait(&full[u % Cfg::kStages], static_cast<uint32_t>(u / Cfg::kStages) & 1u) && ok;
+  if (!ok) atomicOr(err, kErrAttLoad);
 }
 
 // ------------------------------------------------------------ softmax and output
-// One query row per pair of threads.
+// kSplit threads share a query row: each has its part of a tile's keys and, of
+// each chunk of head_dim, its part of the output columns.
 template <class Cfg>
 struct RowState {
-  float o[Cfg::kNH][Cfg::kOC];
-  float m, l;              // of the whole row; l of this thread's keys until finish()
-  float qscale;            // 2^-e of the row
+  float o[Cfg::kNC][Cfg::kOC];
+  float m, l;              // of the whole row; l of this thread's keys until the end
   bool any_left_out;
 };
-
-template <class Cfg>
-__device__ __forceinline__ void drain_o(MmaShared<Cfg::kStages>& sh, uint32_t t_o, int use,
-                                        float alpha, float vs, float (&o)[Cfg::kOC],
-                                        bool& dead) {
-  if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.o_full, static_cast<uint32_t>(use) & 1u));
-  tc_fence_after();
-#pragma unroll
-  for (int c = 0; c < Cfg::kOC; c += 16) {
-    uint32_t v[16];
-    tc_ld16(t_o + static_cast<uint32_t>(c), v);
-    tc_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float a, b;
-      mul2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), vs, vs);
-      scale_add2(o[c + i], o[c + i + 1], alpha, a, b);
-    }
-  }
-  tc_fence_before();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.o_free);
-}
 
 // q: the row's head_dim values, or null (a row of zeros); vis: it sees the keys
 // below vis (relative to the first key of tile 0 of the run); all_vis: a bound
 // below which every row of the CTA sees every key.
-template <class Cfg>
-__device__ __forceinline__ void mma_rows(MmaShared<Cfg::kStages>& sh, const float* q, int n, int vis, int all_vis, float scale,
-                                         float cap, RowState<Cfg>& st, bool& dead) {
+template <class Cfg, bool kCap>
+__device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int n, int vis, int all_vis, float scale, float cap,
+                                         RowState<Cfg>& st, bool& dead) {
+  constexpr int kKeys = Cfg::kKeys, kSplit = Cfg::kSplit;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int quad = warp & 3, half = warp >> 2;
+  const int quad = warp & 3, part = warp >> 2;
   const int row = 32 * quad + lane;
   const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+  auto row_sync = [&]() { bar_sync(1 + quad, 32 * kSplit); };
   dead = false;
   st.m = -INFINITY;
   st.l = 0.f;
   st.any_left_out = false;
-#pragma unroll
-  for (int h = 0; h < Cfg::kNH; ++h)
-#pragma unroll
-    for (int i = 0; i < Cfg::kOC; ++i) st.o[h][i] = 0.f;
-  // ---- Q: this thread's half of the row, scaled and split into tensor memory
+  float qscale;
+  // ---- Q: this thread's part of the row, scaled and split into tensor memory
   {
-    constexpr int kQC = Cfg::kHd / 2;
+    constexpr int kQC = Cfg::kHd / kSplit;
     float x[kQC];
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < kQC; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (q) v = *reinterpret_cast<const float4*>(q + half * kQC + i);
+      if (q) v = *reinterpret_cast<const float4*>(q + part * kQC + i);
       x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (finite_bits(x[i + c])) a = fmaxf(a, fabsf(x[i + c]));
     }
-    sh.xmax[1][half][row] = a;
-    bar_sync(1 + quad, 64);
-    a = fmaxf(a, sh.xmax[1][half ^ 1][row]);
+    sh.xmax[1][part][row] = a;
+    row_sync();
+#pragma unroll
+    for (int c = 0; c < kSplit; ++c) a = fmaxf(a, sh.xmax[1][c][row]);
     const int e = split_exp(a);
     const float sc = exp2i(e);
-    st.qscale = exp2i(-e);
+    qscale = exp2i(-e);
+    constexpr int kStep = kQC < 16 ? kQC : 16;
 #pragma unroll
-    for (int i = 0; i < kQC; i += 16) {
+    for (int i = 0; i < kQC; i += kStep) {
       uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) split_f16x2(x[i + 2 * c] * sc, x[i + 2 * c + 1] * sc, hi[c], lo[c]);
-      const uint32_t col = static_cast<uint32_t>((half * kQC + i) / 2);
-      tc_st8(lanes + kTmQhi + col, hi);
-      tc_st8(lanes + kTmQlo + col, lo);
+      for (int c = 0; c < kStep / 2; ++c)
+        split_f16x2(x[i + 2 * c] * sc, x[i + 2 * c + 1] * sc, hi[c], lo[c]);
+      const uint32_t col = static_cast<uint32_t>((part * kQC + i) / 2);
+      if constexpr (kStep == 16) {
+        tc_st8(lanes + kTmQhi + col, hi);
+        tc_st8(lanes + kTmQlo + col, lo);
+      } else {
+        tc_st4(lanes + kTmQhi + col, hi[0], hi[1], hi[2], hi[3]);
+        tc_st4(lanes + kTmQlo + col, lo[0], lo[1], lo[2], lo[3]);
+      }
     }
     tc_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_ready);
   }
-  const float rowf = st.qscale * scale * (cap > 0.f ? 1.f : kLog2e);
-  const uint32_t t_o = lanes + kTmO + static_cast<uint32_t>(half * Cfg::kOC);
-  float alpha_prev = 1.f, vs_prev = 1.f;
-  for (int j = 0; j < n; ++j) {
+#pragma unroll
+  for (int c = 0; c < Cfg::kNC; ++c)
+#pragma unroll
+    for (int i = 0; i < Cfg::kOC; ++i) st.o[c][i] = 0.f;
+  const float rowf = qscale * scale * (kCap ? 1.f : kLog2e);
+  const uint32_t t_o = lanes + kTmO + static_cast<uint32_t>(part * Cfg::kOC);
+  float alpha = 1.f, vs = 1.f, alpha_next = 1.f, vs_next = 1.f;
+  uint32_t hi[kKeys / 2], lo[kKeys / 2];
+  // waits unless an earlier mbar_test saw the phase over
+  auto wait = [&](uint64_t* bar, uint32_t parity, bool seen) {
+    if (!__all_sync(0xFFFFFFFFu, seen) && !dead)
+      dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  RingAt<2> buf;
+  bool s_seen = false, o_seen = false;
+  // S(j) -> the weights of tile j, split, in registers
+  auto weights = [&](int j) {
     const uint32_t ph = static_cast<uint32_t>(j) & 1u;
     const uint32_t mph = static_cast<uint32_t>(j >> 1) & 1u;
-    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.meta_full[ph], mph));
-    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.s_full, ph));
+    if (!__all_sync(0xFFFFFFFFu, s_seen) && !dead)
+      dead = !__all_sync(0xFFFFFFFFu,
+                         mbar_wait(&sh.meta_full[ph], mph) && mbar_wait(&sh.s_full, ph));
     tc_fence_after();
-    float x[32];
+    float x[kKeys];
     {
-      uint32_t v[32];
-      tc_ld32(lanes + kTmS + static_cast<uint32_t>(32 * half), v);
+      uint32_t v[kKeys];
+      tc_ld<kKeys>(lanes + kTmS + static_cast<uint32_t>(kKeys * part), v);
       tc_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.s_free);
-      const float4* ks = reinterpret_cast<const float4*>(sh.meta[ph].kscale + 32 * half);
+      const float4* ks = reinterpret_cast<const float4*>(sh.meta[ph].kscale + kKeys * part);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kKeys / 4; ++i) {
         const float4 f = ks[i];
         x[4 * i] = __uint_as_float(v[4 * i]) * (f.x * rowf);
         x[4 * i + 1] = __uint_as_float(v[4 * i + 1]) * (f.y * rowf);
@@ -351,68 +419,100 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg::kStages>& sh, const floa
         x[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * (f.w * rowf);
       }
     }
-    const float vs = sh.meta[ph].vscale;
+    vs_next = sh.meta[ph].vscale;
     st.any_left_out = st.any_left_out || (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
-    if (cap > 0.f) {
+    if constexpr (kCap) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = cap * tanhf(x[i] / cap) * kLog2e;
+      for (int i = 0; i < kKeys; ++i) x[i] = cap * tanhf(x[i] / cap) * kLog2e;
     }
     if ((j + 1) * kTileKeys > all_vis) {
-      const int left = vis - j * kTileKeys - 32 * half;     // of this thread's keys, how many
+      const int left = vis - j * kTileKeys - kKeys * part;    // of this thread's keys, how many
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i >= left) x[i] = -INFINITY;                     // a select: nothing is multiplied
+      for (int i = 0; i < kKeys; ++i)
+        if (i >= left) x[i] = -INFINITY;                      // a select: nothing is multiplied
     }
     float mx = x[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
-    sh.xmax[ph][half][row] = mx;
-    bar_sync(1 + quad, 64);
-    mx = fmaxf(mx, sh.xmax[ph][half ^ 1][row]);
+    for (int i = 1; i < kKeys; ++i) mx = fmaxf(mx, x[i]);
+    sh.xmax[ph][part][row] = mx;
+    row_sync();
+#pragma unroll
+    for (int c = 0; c < kSplit; ++c) mx = fmaxf(mx, sh.xmax[ph][c][row]);
     const float mn = fmaxf(st.m, mx);
     const float base = mn == -INFINITY ? 0.f : mn;
-    const float alpha = ex2(st.m - base);
+    alpha_next = ex2(st.m - base);
     st.m = mn;
     const float sub = base - static_cast<float>(kPShift);
+    o_seen = mbar_test(&sh.o_full[buf.stage], buf.phase);   // the chunk drained next
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t hi[16], lo[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < kKeys / 2; ++i) {
       const float a = ex2(x[2 * i] - sub), b = ex2(x[2 * i + 1] - sub);
       sum[i & 3] += a + b;
       split_f16x2(a, b, hi[i], lo[i]);
     }
-    st.l = fmaf(st.l, alpha, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-    // the last half of the tile before: after it P may be overwritten
-    if (j > 0)
-      drain_o<Cfg>(sh, t_o, j * Cfg::kNH - 1, alpha_prev, vs_prev, st.o[Cfg::kNH - 1], dead);
-    tc_st16(lanes + kTmPhi + static_cast<uint32_t>(16 * half), hi);
-    tc_st16(lanes + kTmPlo + static_cast<uint32_t>(16 * half), lo);
+    st.l = fmaf(st.l, alpha_next, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+  };
+  auto store_p = [&](int j) {
+    // S of the tile after next, meanwhile
+    const uint32_t ph = static_cast<uint32_t>(j + 1) & 1u;
+    s_seen = mbar_test(&sh.meta_full[ph], static_cast<uint32_t>((j + 1) >> 1) & 1u) &
+             mbar_test(&sh.s_full, ph);
+    tc_st<kKeys / 2>(lanes + kTmPhi + static_cast<uint32_t>(kKeys / 2 * part), hi);
+    tc_st<kKeys / 2>(lanes + kTmPlo + static_cast<uint32_t>(kKeys / 2 * part), lo);
     tc_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.p_ready);
-    if constexpr (Cfg::kNH == 2)
-      drain_o<Cfg>(sh, t_o, 2 * j, alpha, vs, st.o[0], dead);
-    alpha_prev = alpha;
-    vs_prev = vs;
+  };
+  // one copy of each step: the code of a tile is read anew for every tile, and two
+  // copies of it do not stay in the instruction caches
+#pragma unroll 1
+  for (int j = -1; j < n; ++j) {
+    alpha = alpha_next;
+    vs = vs_next;
+    if (j + 1 < n) weights(j + 1);
+    if (j >= 0) {
+#pragma unroll
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      wait(&sh.o_full[buf.stage], buf.phase, o_seen);
+      tc_fence_after();
+      uint32_t v[Cfg::kOC];
+      tc_ld<Cfg::kOC>(t_o + static_cast<uint32_t>(buf.stage) * 64u, v);
+      uint64_t* free_bar = &sh.o_free[buf.stage];
+      buf.next();
+      o_seen = c + 1 < Cfg::kNC && mbar_test(&sh.o_full[buf.stage], buf.phase);
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(free_bar);
+#pragma unroll
+      for (int i = 0; i < Cfg::kOC; i += 2) {
+        float a, b;
+        mul2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), vs, vs);
+        scale_add2(st.o[c][i], st.o[c][i + 1], alpha, a, b);
+      }
+    }
+    }
+    if (j + 1 < n) store_p(j + 1);      // P(j) has been multiplied by now
   }
-  if (n > 0)
-    drain_o<Cfg>(sh, t_o, n * Cfg::kNH - 1, alpha_prev, vs_prev, st.o[Cfg::kNH - 1], dead);
   // the row's whole sum
-  bar_sync(1 + quad, 64);
-  sh.xmax[0][half][row] = st.l;
-  bar_sync(1 + quad, 64);
-  st.l += sh.xmax[0][half ^ 1][row];
+  row_sync();
+  sh.xmax[0][part][row] = st.l;
+  row_sync();
+  float l = 0.f;
+#pragma unroll
+  for (int c = 0; c < kSplit; ++c) l += sh.xmax[0][c][row];
+  st.l = l;
 }
 
 // A key left out of its tile (see the head of this file): its weight from the
 // row's final maximum, and its values, in f32.
 template <class Cfg>
 __device__ __forceinline__ void add_left_out(RowState<Cfg>& st, const float* q, const float* k,
-                                          const float* v, int half, float scale, float cap) {
+                                          const float* v, int part, float scale, float cap) {
   float s = 0.f;
   for (int i = 0; i < Cfg::kHd; i += 4) {
     const float4 a = *reinterpret_cast<const float4*>(q + i);
@@ -422,29 +522,28 @@ __device__ __forceinline__ void add_left_out(RowState<Cfg>& st, const float* q, 
   const float base = st.m == -INFINITY ? 0.f : st.m;
   const float p = ex2(soft_cap(s * scale, cap) * kLog2e - (base - static_cast<float>(kPShift)));
 #pragma unroll
-  for (int h = 0; h < Cfg::kNH; ++h)
+  for (int c = 0; c < Cfg::kNC; ++c)
 #pragma unroll
     for (int i = 0; i < Cfg::kOC; ++i)
-      st.o[h][i] = fmaf(p, v[h * Cfg::kHC + half * Cfg::kOC + i], st.o[h][i]);
+      st.o[c][i] = fmaf(p, v[c * Cfg::kHC + part * Cfg::kOC + i], st.o[c][i]);
 }
 
 // this thread's columns of a row: f * o
 template <class Cfg>
-__device__ __forceinline__ void store_columns(const RowState<Cfg>& st, float* dst, int half,
+__device__ __forceinline__ void store_columns(const RowState<Cfg>& st, float* dst, int part,
                                               float f) {
 #pragma unroll
-  for (int h = 0; h < Cfg::kNH; ++h)
+  for (int c = 0; c < Cfg::kNC; ++c)
 #pragma unroll
     for (int i = 0; i < Cfg::kOC; i += 4)
-      *reinterpret_cast<float4*>(dst + h * Cfg::kHC + half * Cfg::kOC + i) =
-          make_float4(st.o[h][i] * f, st.o[h][i + 1] * f, st.o[h][i + 2] * f, st.o[h][i + 3] * f);
+      *reinterpret_cast<float4*>(dst + c * Cfg::kHC + part * Cfg::kOC + i) =
+          make_float4(st.o[c][i] * f, st.o[c][i + 1] * f, st.o[c][i + 2] * f, st.o[c][i + 3] * f);
 }
 
 // ------------------------------------------------------------ packing a key tile
 // 64 keys of one kv head, n of them there (the rest zero), by a CTA of 256
-// threads: K rows as units of [hi, lo][64-column run] x 64 rows of 128 bytes, V
-// transposed as units of [hi, lo] x head_dim rows of 64 keys, into dst (the
-// order K half 0, K half 1, V half 0, V half 1), and the meta record.
+// threads, into dst: the units of K, then those of V^T (see MmaCfg), and the meta
+// record.
 // smem: kTileKeys * (hd + 1) floats.
 template <class Cfg>
 __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_t k_stride,
@@ -485,10 +584,9 @@ __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_
 #pragma unroll
       for (int i = 0; i < kPL; i += (kPL >= 4 ? 4 : 2)) {
         const int c = lane_col<kPL>(lane, i);
-        const int h = c / Cfg::kHC, ch = c - h * Cfg::kHC;
-        uint8_t* u = dst + h * Cfg::kKUnit + (ch / 64) * 8192;
-        const uint32_t off = sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(ch % 64) / 8u) +
-                             static_cast<uint32_t>(ch % 8) * 2u;
+        uint8_t* u = dst + (c / 64) * Cfg::kKUnit;
+        const uint32_t off = sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(c % 64) / 8u) +
+                             static_cast<uint32_t>(c % 8) * 2u;
         uint32_t h0, l0;
         split_f16x2(x[i] * sc, x[i + 1] * sc, h0, l0);
         if constexpr (kPL >= 4) {
@@ -553,7 +651,7 @@ __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_
     split_f16x2(y[4], y[5], hi.z, lo.z);
     split_f16x2(y[6], y[7], hi.w, lo.w);
     const int h = d / Cfg::kHC, dh = d - h * Cfg::kHC;
-    uint8_t* u = dst + Cfg::kNH * Cfg::kKUnit + h * Cfg::kVUnit;
+    uint8_t* u = dst + Cfg::kNC * Cfg::kKUnit + h * Cfg::kVUnit;
     const uint32_t off = sw128_off(static_cast<uint32_t>(dh), static_cast<uint32_t>(kg));
     *reinterpret_cast<uint4*>(u + off) = hi;
     *reinterpret_cast<uint4*>(u + Cfg::kVPart + off) = lo;

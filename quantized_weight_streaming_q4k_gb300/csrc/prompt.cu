@@ -169,11 +169,14 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ tensor cores
+template <int kHd>
+using PromptCfg = MmaCfg<kHd, 2>;
+
 // Key tiles of every sequence and kv head, split and laid out once (they are
 // read by all of the sequence's query tiles).  grid (key tiles, n_kv).
 template <int kHd>
 __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant__ PromptParams p) {
-  using Cfg = MmaCfg<kHd>;
+  using Cfg = PromptCfg<kHd>;
   extern __shared__ __align__(16) float smem[];
   pdl_launch_dependents();
   pdl_wait();
@@ -188,13 +191,13 @@ __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant_
 }
 
 // One item per CTA: 128 rows of one kv head against its piece of the keys.
-template <int kHd>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+template <int kHd, bool kCap>
+__global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
     prompt_mma_kernel(const __grid_constant__ PromptParams p) {
-  using Cfg = MmaCfg<kHd>;
+  using Cfg = PromptCfg<kHd>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  auto& sh = *reinterpret_cast<MmaShared<Cfg::kStages>*>(stages + Cfg::kStages * Cfg::kStage);
+  auto& sh = *reinterpret_cast<MmaShared<Cfg>*>(stages + Cfg::kRing);
   const PromptItem it = prompt_item(p, blockIdx.x);
   pdl_launch_dependents();
   if (it.piece >= it.pieces) return;
@@ -203,8 +206,8 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
   const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
   const int64_t tile0 = p.seqs.ktile[it.s] + ka / kTileKeys;    // its packed tiles
-  if (threadIdx.x == 0) mma_init_barriers(sh, 1);
-  if (warp == 9) {
+  if (threadIdx.x == 0) mma_init_barriers<Cfg>(sh);
+  if (warp == Cfg::kMmaQk) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
@@ -212,54 +215,47 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  if (warp >= 8) {
-    regs_few();
-    if (warp == 8 && lane == 0) {
-      const uint64_t pol = l2_policy_evict_first();
-      int unit = 0;
-      bool ok = true;
-      auto load = [&](int j, int v, int h) {     // v: 0 K, 1 V half h of tile j
-        const int s = unit % Cfg::kStages;
-        const uint32_t ph = static_cast<uint32_t>(unit / Cfg::kStages) & 1u;
-        ok = ok && mbar_wait(&sh.empty[s], ph ^ 1u);
-        if (!ok) return;
-        const uint8_t* src = p.packed + ((tile0 + j) * p.n_kv + g) * Cfg::kTile +
-                             (v ? Cfg::kNH * Cfg::kKUnit + h * Cfg::kVUnit : h * Cfg::kKUnit);
-        const uint32_t bytes = v ? Cfg::kVUnit : Cfg::kKUnit;
-        mbar_arrive_expect_tx(&sh.full[s], bytes);
-        bulk_copy_g2s(stages + s * Cfg::kStage, src, bytes, &sh.full[s], pol);
-        ++unit;
-      };
-      auto load_meta = [&](int j) {
-        const int s = j & 1;
-        ok = ok && mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta));
-        bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g, sizeof(TileMeta),
-                      &sh.meta_full[s], pol);
-      };
-      int metas = 0;
-      if (n > 0) {
-        load_meta(metas++);
-        for (int h = 0; h < Cfg::kNH; ++h) load(0, 0, h);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) load_meta(metas++);
-        for (int h = 0; h < Cfg::kNH; ++h) {
-          if (j + 1 < n) load(j + 1, 0, h);
-          load(j, 1, h);
-        }
-      }
-      if (!ok) atomicOr(&g_err_prompt, kErrAttLoad);
-      // do not leave with copies into shared memory in flight
-      for (int u = max(0, unit - Cfg::kStages); u < unit; ++u)
-        if (!mbar_wait(&sh.full[u % Cfg::kStages], static_cast<uint32_t>(u / Cfg::kStages) & 1u))
-          atomicOr(&g_err_prompt, kErrAttLoad);
+  uint8_t* k_ring = stages;
+  uint8_t* v_ring = stages + Cfg::kStages * Cfg::kKUnit;
+  if (warp >= Cfg::kRowsWarps) {
+    regs_few<Cfg>();
+    const auto packed = [&](int j) { return p.packed + ((tile0 + j) * p.n_kv + g) * Cfg::kTile; };
+    if (warp == Cfg::kLoadK && lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      mma_load<Cfg>(
+          sh.k_full, sh.k_empty, n,
+          [&](int j) {
+            const int s = j & 1;
+            if (!mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
+            mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta));
+            bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g, sizeof(TileMeta),
+                          &sh.meta_full[s], pol);
+            return true;
+          },
+          [&](int s, int j, int c) {
+            mbar_arrive_expect_tx(&sh.k_full[s], Cfg::kKUnit);
+            bulk_copy_g2s(k_ring + s * Cfg::kKUnit, packed(j) + c * Cfg::kKUnit, Cfg::kKUnit,
+                          &sh.k_full[s], pol);
+          },
+          &g_err_prompt);
     }
-    if (warp == 9) mma_issue<Cfg>(sh, stages, n, &g_err_prompt);
+    if (warp == Cfg::kLoadV && lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      mma_load<Cfg>(
+          sh.v_full, sh.v_empty, n, [&](int) { return true; },
+          [&](int s, int j, int c) {
+            mbar_arrive_expect_tx(&sh.v_full[s], Cfg::kVUnit);
+            bulk_copy_g2s(v_ring + s * Cfg::kVUnit,
+                          packed(j) + Cfg::kNC * Cfg::kKUnit + c * Cfg::kVUnit, Cfg::kVUnit,
+                          &sh.v_full[s], pol);
+          },
+          &g_err_prompt);
+    }
+    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh, k_ring, n, &g_err_prompt);
+    if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh, v_ring, n, &g_err_prompt);
   } else {
-    regs_many();
-    const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+    regs_many<Cfg>();
+    const int row = 32 * (warp & 3) + lane, part = warp >> 2;
     const int live = it.n_tok * p.group;
     const bool alive = row < live;
     const int r = min(row, live - 1);
@@ -269,7 +265,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     const int vis = visible(i, it.n_q, it.n_k) - ka;
     RowState<Cfg> st;
     bool dead;
-    mma_rows<Cfg>(sh, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
+    mma_rows<Cfg, kCap>(sh, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
                   p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
     if (st.any_left_out && alive) {
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           if (!((m.left_out[t >> 5] >> (t & 31)) & 1u) || j * kTileKeys + t >= vis) continue;
           const int64_t key = p.seqs.k0[it.s] + ka + j * kTileKeys + t;
           add_left_out<Cfg>(st, q, p.k.data + key * p.k.token_stride + g * p.k.head_stride,
-                            p.v.data + key * p.v.token_stride + g * p.v.head_stride, half,
+                            p.v.data + key * p.v.token_stride + g * p.v.head_stride, part,
                             p.scale, p.cap);
         }
       }
@@ -289,22 +285,23 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       if (it.pieces > 1) {
         float* dst =
             p.part + (part_slot(p, it, it.piece, g) * p.rows + row) * (kHd + kPartPad);
-        store_columns<Cfg>(st, dst, half, kUnshift);
-        if (half == 0) {
+        store_columns<Cfg>(st, dst, part, kUnshift);
+        if (part == 0) {
           dst[kHd] = st.m;
           dst[kHd + 1] = st.l * kUnshift;
         }
       } else {
         store_columns<Cfg>(st, p.out.data + token * p.out.token_stride + h * p.out.head_stride,
-                           half, st.l == 0.f ? 0.f : 1.0f / st.l);
+                           part, st.l == 0.f ? 0.f : 1.0f / st.l);
       }
     }
   }
   // every MMA has completed before tensor memory is freed
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
-    if (lane == 0 && !mbar_wait(&sh.done, 0)) atomicOr(&g_err_prompt, kErrAttMma);
+  if (warp == Cfg::kMmaQk) {
+    for (int i = 0; i < 2; ++i)
+      if (lane == 0 && !mbar_wait(&sh.done[i], 0)) atomicOr(&g_err_prompt, kErrAttMma);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(sh.tmem, 512);
@@ -361,10 +358,10 @@ PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int
   }
   const auto pad = [](size_t v) { return (v + 255) / 256 * 256; };
   if (pl.mma) {
-    const size_t tile = head_dim == 32   ? MmaCfg<32>::kTile
-                        : head_dim == 64 ? MmaCfg<64>::kTile
-                        : head_dim == 128 ? MmaCfg<128>::kTile
-                                          : MmaCfg<256>::kTile;
+    const size_t tile = head_dim == 32   ? PromptCfg<32>::kTile
+                        : head_dim == 64 ? PromptCfg<64>::kTile
+                        : head_dim == 128 ? PromptCfg<128>::kTile
+                                          : PromptCfg<256>::kTile;
     pl.packed_bytes = pad(static_cast<size_t>(pl.ktiles) * n_kv * tile);
     pl.meta_bytes = pad(static_cast<size_t>(pl.ktiles) * n_kv * sizeof(TileMeta));
   }
@@ -381,9 +378,9 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(p.n_kv));
   cudaError_t e;
   if (pl.mma) {
-    using Cfg = MmaCfg<kHd>;
+    using Cfg = PromptCfg<kHd>;
     constexpr size_t kPackSmem = sizeof(float) * kTileKeys * (kHd + 1);
-    constexpr size_t kSmem = 1024 + Cfg::kStages * Cfg::kStage + sizeof(MmaShared<Cfg::kStages>);
+    constexpr size_t kSmem = 1024 + Cfg::kRing + sizeof(MmaShared<Cfg>);
     static_assert(kSmem <= 227 * 1024, "shared memory");
     if (ktiles > 0) {
       e = cudaFuncSetAttribute(prompt_pack_kernel<kHd>,
@@ -395,10 +392,11 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
                      kPackSmem, st, p);
       if (e != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(prompt_mma_kernel<kHd>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const auto kernel = p.cap > 0.f ? prompt_mma_kernel<kHd, true> : prompt_mma_kernel<kHd, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
-    e = pdl_launch(prompt_mma_kernel<kHd>, grid, kMmaThreads, kSmem, st, p);
+    e = pdl_launch(kernel, grid, Cfg::kThreads, kSmem, st, p);
   } else {
     using Tile = RowTile<kPL, 4>;
     e = cudaFuncSetAttribute(prompt_rows_kernel<kPL, 4>,
