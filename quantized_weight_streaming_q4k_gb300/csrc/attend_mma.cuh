@@ -13,8 +13,9 @@
 // in f32, by the rows that see it.
 //
 // Per tile of 64 keys, S = Q K^T (128 x 64) and O_tile = P V (128 x head_dim).
-// Q hi / lo and P hi / lo are A operands in tensor memory, K and V^T come
-// through a shared-memory ring in the 128-byte-swizzled K-major image.  O_tile is
+// Q hi / lo and P hi / lo are A operands in tensor memory; K and V come through
+// rings in shared memory, both as rows (a key) of 128 bytes (64 columns), swizzled: K
+// as a K-major B operand, V as an MN-major one, so neither is transposed.  O_tile is
 // NOT accumulated in tensor memory: the tensor cores' f32 accumulation does
 // not round to nearest, and its bias grows with the number of steps.  Each
 // tile's O_tile (12 accumulation steps) is added to f32 registers with the
@@ -63,9 +64,8 @@ struct __align__(16) TileMeta {
 };
 static_assert(sizeof(TileMeta) == 272, "copied in 16-byte units");
 
-// A unit: 64 keys x 64 columns of K, or 64 channels x 64 keys of V^T, hi then lo,
-// rows of 128 bytes.
-template <int kHdT, int kSplitT>
+// A unit: 64 keys x 64 columns of K or V, hi then lo.
+template <int kHdT, int kSplitT, int kDepthT = 0>
 struct MmaCfg {
   static constexpr int kHd = kHdT;
   static constexpr int kSplit = kSplitT;                // threads of a query row
@@ -73,12 +73,13 @@ struct MmaCfg {
   static constexpr int kHC = kHd / kNC;                 // columns of a chunk
   static constexpr int kKeys = kTileKeys / kSplit;      // of a tile, a thread's
   static constexpr int kOC = kHC / kSplit;              // of a chunk, a thread's
-  static constexpr uint32_t kKPart = 64 * 128;          // hi or lo of a K unit
-  static constexpr uint32_t kVPart = kHC * 128;         // hi or lo of a V unit
-  static constexpr uint32_t kKUnit = 2 * kKPart, kVUnit = 2 * kVPart;
-  static constexpr uint32_t kTile = kNC * (kKUnit + kVUnit);   // a packed key tile
-  static constexpr int kStages = 6;                     // of each ring
-  static constexpr uint32_t kRing = kStages * (kKUnit + kVUnit);
+  static constexpr uint32_t kPart = kTileKeys * 128;    // hi or lo of a unit
+  static constexpr uint32_t kUnit = 2 * kPart;
+  static constexpr uint32_t kHalfTile = kNC * kUnit;    // K, or V, of a tile
+  static constexpr uint32_t kTile = 2 * kHalfTile;      // a packed key tile
+  // units of each of the two rings: 6, or kDepth whole tiles
+  static constexpr int kStages = kDepthT ? kDepthT * kNC : 6;
+  static constexpr uint32_t kRing = 2 * kStages * kUnit;
   // softmax warps, then the helpers
   static constexpr int kRowsWarps = 4 * kSplit;
   static constexpr int kLoadK = kRowsWarps, kLoadV = kRowsWarps + 1;
@@ -108,7 +109,8 @@ template <class Cfg>
 struct MmaShared {
   uint64_t k_full[Cfg::kStages], k_empty[Cfg::kStages];
   uint64_t v_full[Cfg::kStages], v_empty[Cfg::kStages];
-  uint64_t meta_full[2], meta_free[2];
+  uint64_t meta_full[2], meta_free[2];      // kscale
+  uint64_t vmeta_full[2], vmeta_free[2];    // vscale, left_out
   uint64_t o_full[2], o_free[2];
   uint64_t q_ready, s_full, s_free, p_ready, done[2];
   uint32_t tmem;
@@ -158,16 +160,18 @@ __device__ __forceinline__ bool finite_bits(float x) {
 }
 
 template <class Cfg>
-__device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh) {
+__device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh, uint32_t full_count) {
   for (int s = 0; s < Cfg::kStages; ++s) {
-    mbar_init(&sh.k_full[s], 1);
+    mbar_init(&sh.k_full[s], full_count);
     mbar_init(&sh.k_empty[s], 1);
-    mbar_init(&sh.v_full[s], 1);
+    mbar_init(&sh.v_full[s], full_count);
     mbar_init(&sh.v_empty[s], 1);
   }
   for (int s = 0; s < 2; ++s) {
-    mbar_init(&sh.meta_full[s], 1);
+    mbar_init(&sh.meta_full[s], full_count);
     mbar_init(&sh.meta_free[s], Cfg::kRowsWarps);
+    mbar_init(&sh.vmeta_full[s], full_count);
+    mbar_init(&sh.vmeta_free[s], Cfg::kRowsWarps);
     mbar_init(&sh.o_full[s], 1);
     mbar_init(&sh.o_free[s], Cfg::kRowsWarps);
     mbar_init(&sh.done[s], 1);
@@ -215,7 +219,7 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
       if (c == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
       tc_fence_after();
       if (!ok) break;
-      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kKUnit >> 4);
+      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
       uint64_t* empty = &sh.k_empty[at.stage];
       at.next();
       const bool next = mbar_test(&sh.k_full[at.stage], at.phase);
@@ -224,7 +228,7 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           const uint32_t a = (t == 1 ? kTmQlo : kTmQhi) + static_cast<uint32_t>(c * kSteps + k) * 8u;
-          const uint32_t off = (t == 0 ? Cfg::kKPart : 0u) + static_cast<uint32_t>(k) * 32u;
+          const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 32u;
           tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdesc, (c | t | k) != 0 ? 1u : 0u, one);
         }
       }
@@ -241,7 +245,7 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
 template <class Cfg>
 __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring, int n,
                                              unsigned* err) {
-  constexpr uint32_t kIdesc = tc_idesc_f16(kTileRows, Cfg::kHC);
+  constexpr uint32_t kIdesc = tc_idesc_f16(kTileRows, Cfg::kHC) | kIdescBMn;
   const uint32_t one = elect_one();
   const uint32_t base = sw128_lo(smem_addr(v_ring));
   RingAt<Cfg::kStages> at;
@@ -260,7 +264,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
       if (c == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);   // the last to come
       tc_fence_after();
       if (!ok) break;
-      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kVUnit >> 4);
+      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
       const uint32_t d = kTmO + static_cast<uint32_t>(buf.stage) * 64u;
       uint64_t *full = &sh.o_full[buf.stage], *empty = &sh.v_empty[at.stage];
       at.next();
@@ -272,7 +276,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k) {
           const uint32_t a = (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
-          const uint32_t off = (t == 0 ? Cfg::kVPart : 0u) + static_cast<uint32_t>(k) * 32u;
+          const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 2048u;
           tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, (t | k) != 0 ? 1u : 0u, one);
         }
       }
@@ -384,7 +388,7 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
     for (int i = 0; i < Cfg::kOC; ++i) st.o[c][i] = 0.f;
   const float rowf = qscale * scale * (kCap ? 1.f : kLog2e);
   const uint32_t t_o = lanes + kTmO + static_cast<uint32_t>(part * Cfg::kOC);
-  float alpha = 1.f, vs = 1.f, alpha_next = 1.f, vs_next = 1.f;
+  float alpha = 1.f, vs = 1.f, alpha_next = 1.f;
   uint32_t hi[kKeys / 2], lo[kKeys / 2];
   // waits unless an earlier mbar_test saw the phase over
   auto wait = [&](uint64_t* bar, uint32_t parity, bool seen) {
@@ -419,8 +423,6 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
         x[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * (f.w * rowf);
       }
     }
-    vs_next = sh.meta[ph].vscale;
-    st.any_left_out = st.any_left_out || (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
     if constexpr (kCap) {
@@ -472,9 +474,16 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
 #pragma unroll 1
   for (int j = -1; j < n; ++j) {
     alpha = alpha_next;
-    vs = vs_next;
     if (j + 1 < n) weights(j + 1);
     if (j >= 0) {
+      const uint32_t ph = static_cast<uint32_t>(j) & 1u;
+      if (!dead)
+        dead = !__all_sync(0xFFFFFFFFu,
+                           mbar_wait(&sh.vmeta_full[ph], static_cast<uint32_t>(j >> 1) & 1u));
+      vs = sh.meta[ph].vscale;
+      st.any_left_out = st.any_left_out || (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.vmeta_free[ph]);
 #pragma unroll
     for (int c = 0; c < Cfg::kNC; ++c) {
       wait(&sh.o_full[buf.stage], buf.phase, o_seen);
@@ -540,121 +549,110 @@ __device__ __forceinline__ void store_columns(const RowState<Cfg>& st, float* ds
           make_float4(st.o[c][i] * f, st.o[c][i + 1] * f, st.o[c][i + 2] * f, st.o[c][i + 3] * f);
 }
 
-// ------------------------------------------------------------ packing a key tile
+// ------------------------------------------------------------ key tiles
+// One key row (a lane's kPL = head_dim / 32 columns of it, times sc) as hi and lo f16
+// into row r of the units at dst.
+template <class Cfg>
+__device__ __forceinline__ void store_split_row(const float (&x)[Cfg::kHd / 32], float sc, int r,
+                                                int lane, uint8_t* dst) {
+  constexpr int kPL = Cfg::kHd / 32;
+  if constexpr (kPL >= 2) {
+#pragma unroll
+    for (int i = 0; i < kPL; i += (kPL >= 4 ? 4 : 2)) {
+      const int c = lane_col<kPL>(lane, i);
+      uint8_t* u = dst + (c / 64) * Cfg::kUnit +
+                   sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(c % 64) / 8u) + (c % 8) * 2;
+      uint32_t h0, l0;
+      split_f16x2(x[i] * sc, x[i + 1] * sc, h0, l0);
+      if constexpr (kPL >= 4) {
+        uint32_t h1, l1;
+        split_f16x2(x[i + 2] * sc, x[i + 3] * sc, h1, l1);
+        *reinterpret_cast<uint2*>(u) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(u + Cfg::kPart) = make_uint2(l0, l1);
+      } else {
+        *reinterpret_cast<uint32_t*>(u) = h0;
+        *reinterpret_cast<uint32_t*>(u + Cfg::kPart) = l0;
+      }
+    }
+  } else {
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
+    if (!(lane & 1)) {
+      uint32_t h0, l0;
+      split_f16x2(x[0] * sc, other * sc, h0, l0);
+      uint8_t* u = dst + sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(lane) / 8u) +
+                   (lane % 8) * 2;
+      *reinterpret_cast<uint32_t*>(u) = h0;
+      *reinterpret_cast<uint32_t*>(u + Cfg::kPart) = l0;
+    }
+  }
+}
+
+// largest finite magnitude of a row over the warp; `all`: every value is finite
+template <int kPL>
+__device__ __forceinline__ float row_amax(const float (&x)[kPL], bool& all) {
+  float a = 0.f;
+  bool fin = true;
+#pragma unroll
+  for (int i = 0; i < kPL; ++i) {
+    const bool f = finite_bits(x[i]);
+    fin = fin && f;
+    a = fmaxf(a, f ? fabsf(x[i]) : 0.f);
+  }
+  all = __all_sync(0xFFFFFFFFu, fin);
+  return warp_max(a);
+}
+
 // 64 keys of one kv head, n of them there (the rest zero), by a CTA of 256
-// threads, into dst: the units of K, then those of V^T (see MmaCfg), and the meta
-// record.
-// smem: kTileKeys * (hd + 1) floats.
+// threads, into dst: the units of K, then those of V, and the meta record.
 template <class Cfg>
 __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_t k_stride,
-                                          int64_t v_stride, int n, uint8_t* dst, TileMeta* meta,
-                                          float* vt) {
-  constexpr int kHd = Cfg::kHd, kPL = kHd / 32, kPitch = kHd + 1;
+                                          int64_t v_stride, int n, uint8_t* dst, TileMeta* meta) {
+  constexpr int kPL = Cfg::kHd / 32, kRows = kTileKeys / 8;
   __shared__ float vmax[kTileKeys];
-  __shared__ uint32_t bad[2];
-  __shared__ float vsc;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  for (int r = warp; r < kTileKeys; r += 8) {
-    float x[kPL], y[kPL];
+  float y[kRows][kPL];
 #pragma unroll
-    for (int i = 0; i < kPL; ++i) x[i] = y[i] = 0.f;
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + 8 * i;
+    float x[kPL];
+#pragma unroll
+    for (int c = 0; c < kPL; ++c) x[c] = y[i][c] = 0.f;
     if (r < n) {
       load_row<kPL>(K + r * k_stride, lane, x);
-      load_row<kPL>(V + r * v_stride, lane, y);
+      load_row<kPL>(V + r * v_stride, lane, y[i]);
     }
-    float a = 0.f, b = 0.f;
-    bool fin = true;
-#pragma unroll
-    for (int i = 0; i < kPL; ++i) {
-      if (finite_bits(x[i])) a = fmaxf(a, fabsf(x[i]));
-      fin = fin && finite_bits(y[i]);
-      b = fmaxf(b, fabsf(y[i]));
-    }
-    a = warp_max(a);
-    b = warp_max(b);
-    fin = __all_sync(0xFFFFFFFFu, fin);
-    const int e = split_exp(a);
-    const float sc = exp2i(e);
+    bool fin;
+    const int e = split_exp(row_amax<kPL>(x, fin));
+    store_split_row<Cfg>(x, exp2i(e), r, lane, dst);
+    const float b = row_amax<kPL>(y[i], fin);
     if (lane == 0) {
       meta->kscale[r] = exp2i(-e);
       vmax[r] = fin ? b : INFINITY;
     }
-    // K: neighbours in pairs (one value at head_dim 32 and 64: exchange below)
-    if constexpr (kPL >= 2) {
-#pragma unroll
-      for (int i = 0; i < kPL; i += (kPL >= 4 ? 4 : 2)) {
-        const int c = lane_col<kPL>(lane, i);
-        uint8_t* u = dst + (c / 64) * Cfg::kKUnit;
-        const uint32_t off = sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(c % 64) / 8u) +
-                             static_cast<uint32_t>(c % 8) * 2u;
-        uint32_t h0, l0;
-        split_f16x2(x[i] * sc, x[i + 1] * sc, h0, l0);
-        if constexpr (kPL >= 4) {
-          uint32_t h1, l1;
-          split_f16x2(x[i + 2] * sc, x[i + 3] * sc, h1, l1);
-          *reinterpret_cast<uint2*>(u + off) = make_uint2(h0, h1);
-          *reinterpret_cast<uint2*>(u + Cfg::kKPart + off) = make_uint2(l0, l1);
-        } else {
-          *reinterpret_cast<uint32_t*>(u + off) = h0;
-          *reinterpret_cast<uint32_t*>(u + Cfg::kKPart + off) = l0;
-        }
-      }
-    } else {
-      const float other = __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
-      if (!(lane & 1)) {
-        uint32_t h0, l0;
-        split_f16x2(x[0] * sc, other * sc, h0, l0);
-        const uint32_t off = sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(lane) / 8u) +
-                             static_cast<uint32_t>(lane % 8) * 2u;
-        *reinterpret_cast<uint32_t*>(dst + off) = h0;
-        *reinterpret_cast<uint32_t*>(dst + Cfg::kKPart + off) = l0;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kPL; ++i) vt[r * kPitch + lane_col<kPL>(lane, i)] = y[i];
   }
   __syncthreads();
-  if (warp == 0) {
-    // the smallest finite non-zero row maximum; rows above 2^16 times it stay out
-    const float a = vmax[lane], b = vmax[lane + 32];
-    float lo = fminf(a > 0.f ? a : INFINITY, b > 0.f ? b : INFINITY);
+  // the smallest non-zero row maximum; rows above 2^16 times it stay out
+  const float a = vmax[lane], b = vmax[lane + 32];
+  float lo = fminf(a > 0.f ? a : INFINITY, b > 0.f ? b : INFINITY);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    const float top = lo * 65536.0f;                 // infinity: only what is not finite
-    const bool out_a = !(a <= top) || a == INFINITY, out_b = !(b <= top) || b == INFINITY;
-    const uint32_t ma = __ballot_sync(0xFFFFFFFFu, out_a), mb = __ballot_sync(0xFFFFFFFFu, out_b);
-    const float big = warp_max(fmaxf(out_a ? 0.f : a, out_b ? 0.f : b));
-    if (lane == 0) {
-      const int e = split_exp(big);
-      bad[0] = ma;
-      bad[1] = mb;
-      vsc = exp2i(e);
-      meta->vscale = exp2i(-e);
-      meta->left_out[0] = ma;
-      meta->left_out[1] = mb;
-      meta->pad = 0;
-    }
+  for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+  const float top = lo * 65536.0f;                 // infinity: only what is not finite
+  const bool out_a = !(a <= top) || a == INFINITY, out_b = !(b <= top) || b == INFINITY;
+  const uint32_t ma = __ballot_sync(0xFFFFFFFFu, out_a), mb = __ballot_sync(0xFFFFFFFFu, out_b);
+  const int e = split_exp(warp_max(fmaxf(out_a ? 0.f : a, out_b ? 0.f : b)));
+  if (threadIdx.x == 0) {
+    meta->vscale = exp2i(-e);
+    meta->left_out[0] = ma;
+    meta->left_out[1] = mb;
+    meta->pad = 0;
   }
-  __syncthreads();
-  const float sc = vsc;
-  // a warp: 4 channels x 8 groups of 8 keys, each 16 bytes of hi and of lo
-  for (int d0 = warp * 4; d0 < kHd; d0 += 32) {
-    const int d = d0 + (lane >> 3), kg = lane & 7;
-    const uint32_t out8 = (bad[kg >> 2] >> (8 * (kg & 3))) & 255u;
-    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      y[i] = (out8 >> i) & 1u ? 0.f : vt[(kg * 8 + i) * kPitch + d] * sc;
-    uint4 hi, lo;
-    split_f16x2(y[0], y[1], hi.x, lo.x);
-    split_f16x2(y[2], y[3], hi.y, lo.y);
-    split_f16x2(y[4], y[5], hi.z, lo.z);
-    split_f16x2(y[6], y[7], hi.w, lo.w);
-    const int h = d / Cfg::kHC, dh = d - h * Cfg::kHC;
-    uint8_t* u = dst + Cfg::kNC * Cfg::kKUnit + h * Cfg::kVUnit;
-    const uint32_t off = sw128_off(static_cast<uint32_t>(dh), static_cast<uint32_t>(kg));
-    *reinterpret_cast<uint4*>(u + off) = hi;
-    *reinterpret_cast<uint4*>(u + Cfg::kVPart + off) = lo;
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + 8 * i;
+    const bool out = ((r < 32 ? ma : mb) >> (r & 31)) & 1u;
+#pragma unroll
+    for (int c = 0; c < kPL; ++c) y[i][c] = out ? 0.f : y[i][c];
+    store_split_row<Cfg>(y[i], exp2i(e), r, lane, dst + Cfg::kHalfTile);
   }
 }
 

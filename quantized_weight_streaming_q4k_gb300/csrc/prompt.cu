@@ -177,7 +177,6 @@ using PromptCfg = MmaCfg<kHd, 2>;
 template <int kHd>
 __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant__ PromptParams p) {
   using Cfg = PromptCfg<kHd>;
-  extern __shared__ __align__(16) float smem[];
   pdl_launch_dependents();
   pdl_wait();
   const int tile = blockIdx.x, g = blockIdx.y;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant_
   const int64_t at = static_cast<int64_t>(tile) * p.n_kv + g;
   pack_tile<Cfg>(p.k.data + key * p.k.token_stride + g * p.k.head_stride,
                  p.v.data + key * p.v.token_stride + g * p.v.head_stride, p.k.token_stride,
-                 p.v.token_stride, n, p.packed + at * Cfg::kTile, p.meta + at, smem);
+                 p.v.token_stride, n, p.packed + at * Cfg::kTile, p.meta + at);
 }
 
 // One item per CTA: 128 rows of one kv head against its piece of the keys.
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
   const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
   const int64_t tile0 = p.seqs.ktile[it.s] + ka / kTileKeys;    // its packed tiles
-  if (threadIdx.x == 0) mma_init_barriers<Cfg>(sh);
+  if (threadIdx.x == 0) mma_init_barriers<Cfg>(sh, 1);
   if (warp == Cfg::kMmaQk) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   tc_fence_after();
   pdl_wait();
   uint8_t* k_ring = stages;
-  uint8_t* v_ring = stages + Cfg::kStages * Cfg::kKUnit;
+  uint8_t* v_ring = stages + Cfg::kStages * Cfg::kUnit;
   if (warp >= Cfg::kRowsWarps) {
     regs_few<Cfg>();
     const auto packed = [&](int j) { return p.packed + ((tile0 + j) * p.n_kv + g) * Cfg::kTile; };
@@ -227,14 +226,14 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
           [&](int j) {
             const int s = j & 1;
             if (!mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
-            mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta));
-            bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g, sizeof(TileMeta),
-                          &sh.meta_full[s], pol);
+            mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta::kscale));
+            bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g,
+                          sizeof(TileMeta::kscale), &sh.meta_full[s], pol);
             return true;
           },
           [&](int s, int j, int c) {
-            mbar_arrive_expect_tx(&sh.k_full[s], Cfg::kKUnit);
-            bulk_copy_g2s(k_ring + s * Cfg::kKUnit, packed(j) + c * Cfg::kKUnit, Cfg::kKUnit,
+            mbar_arrive_expect_tx(&sh.k_full[s], Cfg::kUnit);
+            bulk_copy_g2s(k_ring + s * Cfg::kUnit, packed(j) + c * Cfg::kUnit, Cfg::kUnit,
                           &sh.k_full[s], pol);
           },
           &g_err_prompt);
@@ -242,12 +241,19 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
     if (warp == Cfg::kLoadV && lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
       mma_load<Cfg>(
-          sh.v_full, sh.v_empty, n, [&](int) { return true; },
+          sh.v_full, sh.v_empty, n,
+          [&](int j) {
+            const int s = j & 1;
+            if (!mbar_wait(&sh.vmeta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
+            mbar_arrive_expect_tx(&sh.vmeta_full[s], 16);
+            bulk_copy_g2s(&sh.meta[s].vscale, &p.meta[(tile0 + j) * p.n_kv + g].vscale, 16,
+                          &sh.vmeta_full[s], pol);
+            return true;
+          },
           [&](int s, int j, int c) {
-            mbar_arrive_expect_tx(&sh.v_full[s], Cfg::kVUnit);
-            bulk_copy_g2s(v_ring + s * Cfg::kVUnit,
-                          packed(j) + Cfg::kNC * Cfg::kKUnit + c * Cfg::kVUnit, Cfg::kVUnit,
-                          &sh.v_full[s], pol);
+            mbar_arrive_expect_tx(&sh.v_full[s], Cfg::kUnit);
+            bulk_copy_g2s(v_ring + s * Cfg::kUnit, packed(j) + Cfg::kHalfTile + c * Cfg::kUnit,
+                          Cfg::kUnit, &sh.v_full[s], pol);
           },
           &g_err_prompt);
     }
@@ -379,17 +385,12 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
   cudaError_t e;
   if (pl.mma) {
     using Cfg = PromptCfg<kHd>;
-    constexpr size_t kPackSmem = sizeof(float) * kTileKeys * (kHd + 1);
     constexpr size_t kSmem = 1024 + Cfg::kRing + sizeof(MmaShared<Cfg>);
     static_assert(kSmem <= 227 * 1024, "shared memory");
     if (ktiles > 0) {
-      e = cudaFuncSetAttribute(prompt_pack_kernel<kHd>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(kPackSmem));
-      if (e != cudaSuccess) return e;
       e = pdl_launch(prompt_pack_kernel<kHd>,
-                     dim3(static_cast<unsigned>(ktiles), static_cast<unsigned>(p.n_kv)), 256,
-                     kPackSmem, st, p);
+                     dim3(static_cast<unsigned>(ktiles), static_cast<unsigned>(p.n_kv)), 256, 0,
+                     st, p);
       if (e != cudaSuccess) return e;
     }
     const auto kernel = p.cap > 0.f ? prompt_mma_kernel<kHd, true> : prompt_mma_kernel<kHd, false>;

@@ -159,6 +159,7 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t one) {
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int m, int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
+constexpr uint32_t kIdescBMn = 1u << 16;   // B as K rows of 64 N values (MN-major)
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
