@@ -838,7 +838,7 @@ qws_status qws_device_error(unsigned* code) {
   *code = qws::read_clear_matvec_errors() | qws::read_clear_chain_errors() |
           qws::read_clear_prefill_errors() | qws::read_clear_attention_errors() |
           qws::read_clear_batchmv_errors() | qws::read_clear_embed_errors() |
-          qws::read_clear_prompt_errors();
+          qws::read_clear_prompt_errors() | qws::read_clear_prefix_errors();
   return *code ? fail(QWS_ERR_TIMEOUT, "device error code 0x%x", *code) : ok();
 }
 

@@ -199,6 +199,7 @@ cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const f
                                     const qws_heads& out, int batch, int n_q, int n_kv,
                                     int head_dim, float scale, float cap, void* ws,
                                     cudaStream_t st);
+unsigned read_clear_prefix_errors();
 
 // A launch that may begin while the stream's previous kernel drains (the
 // kernel calls pdl_wait() before it touches global data).

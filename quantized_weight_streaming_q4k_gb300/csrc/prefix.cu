@@ -14,10 +14,13 @@
 
 #include <algorithm>
 
+#include "attend_mma.cuh"
 #include "attend_rows.cuh"
 #include "launch.h"
 
 namespace qws {
+
+__device__ unsigned g_err_prefix;
 
 constexpr int kOwnChunk = 128;      // keys of an own-cache item
 constexpr int kMaxBatch = 256;      // sequences of one launch
@@ -84,6 +87,264 @@ __global__ void __launch_bounds__(kRowThreads)
     if (row < rows)
       store_partial<kPL>(p.part + prefix_part<kPL>(p, piece, g, row), lane, tile.acc[r],
                          tile.m[r], tile.l[r]);
+  }
+}
+
+// ------------------------------------------------------------ tensor cores
+// The shared part of 128 rows of one kv head against one piece of the prefix, on
+// the core of attend_mma.cuh.  The prefix is read once, as f32, straight from the cache:
+// a loader copies runs of rows into a staging ring, four converter warps scale, split
+// and lay them out for the tensor cores.  Bound by that read (8 * head_dim bytes a key
+// and kv head; at head_dim 256 a tile of 64 keys is 128 KB, about 5800 cycles of an
+// SM's share of the memory, against 3072 cycles of MMAs).
+//
+// The values of a tile have one scale, taken from its first run of rows before the
+// others are there: that run's largest value at [2^12, 2^13).  A row whose largest
+// scaled value is not in [2^-3, 65504] would overflow or lose bits; it is left out of
+// the tile and added at the end in f32.
+template <int kHd>
+struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : 2)> {
+  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : 2)>;
+  static constexpr int kDepth = kHd > 128 ? 1 : 2;          // tiles of a ring
+  static constexpr int kConvWarps = 4;
+  static constexpr int kConv = Base::kRowsWarps + 4;        // first converter warp
+  static constexpr int kThreads = 32 * (kConv + kConvWarps);
+  static constexpr int kRun = kHd >= 64 ? 4096 / kHd : 64;  // rows of a staging stage
+  static constexpr int kRuns = kTileKeys / kRun;            // stages of K or V of a tile
+  static constexpr int kRunRows = kRun / kConvWarps;        // of a stage, a warp's
+  static constexpr uint32_t kRunBytes = kRun * kHd * 4;
+  static constexpr int kStaging = 5;
+};
+constexpr int kMaxPieceTiles = 64;
+
+template <int kHd>
+struct PrefixShared {
+  uint64_t stg_full[PrefixCfg<kHd>::kStaging], stg_empty[PrefixCfg<kHd>::kStaging];
+  uint32_t left_out[kMaxPieceTiles][2];
+  float vmax[4];
+  MmaShared<PrefixCfg<kHd>> mma;
+};
+
+// 512 threads, 128 registers each at launch; per scheduler 2 softmax warps at 176, a
+// helper at 56 and a converter at 104: 2 x 176 + 56 + 104 = 4 x 128.
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int kHd>
+__device__ __forceinline__ void prefix_load(PrefixShared<kHd>& sh, uint8_t* staging,
+                                            const float* K, const float* V, int keys, int n) {
+  using Cfg = PrefixCfg<kHd>;
+  const uint64_t pol = l2_policy_evict_first();
+  RingAt<Cfg::kStaging> at;
+  int units = 0;
+  bool ok = true;
+  for (int j = 0; j < n && ok; ++j)
+    for (int half = 0; half < 2 && ok; ++half)
+      for (int r = 0; r < Cfg::kRuns && ok; ++r) {
+        const int key = j * kTileKeys + r * Cfg::kRun, rows = min(Cfg::kRun, keys - key);
+        if (rows <= 0) continue;
+        ok = mbar_wait(&sh.stg_empty[at.stage], at.phase ^ 1u);
+        if (!ok) break;
+        const uint32_t bytes = static_cast<uint32_t>(rows) * kHd * 4u;
+        mbar_arrive_expect_tx(&sh.stg_full[at.stage], bytes);
+        bulk_copy_g2s(staging + at.stage * Cfg::kRunBytes,
+                      (half ? V : K) + static_cast<int64_t>(key) * kHd, bytes,
+                      &sh.stg_full[at.stage], pol);
+        at.next();
+        ++units;
+      }
+  // do not leave with copies into shared memory in flight
+  for (int u = max(0, units - Cfg::kStaging); u < units; ++u)
+    ok = mbar_wait(&sh.stg_full[u % Cfg::kStaging],
+                   static_cast<uint32_t>(u / Cfg::kStaging) & 1u) && ok;
+  if (!ok) atomicOr(&g_err_prefix, kErrAttLoad);
+}
+
+template <int kHd>
+__device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint8_t* staging,
+                                               uint8_t* k_ring, uint8_t* v_ring, int keys, int n) {
+  using Cfg = PrefixCfg<kHd>;
+  constexpr int kPL = kHd / 32, kNC = Cfg::kNC;
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  const int cw = static_cast<int>(threadIdx.x >> 5) - Cfg::kConv;
+  RingAt<Cfg::kStaging> at;
+  bool dead = false;           // a wait gave up: no more waits, the barriers go on
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+#pragma unroll 1
+  for (int jh = 0; jh < 2 * n; ++jh) {
+    const int j = jh >> 1, slot = j & 1;
+    const bool is_v = jh & 1;
+    const uint32_t free_par = (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u;
+    const int stage = (j % Cfg::kDepth) * kNC;
+    uint64_t* empty = is_v ? sh.mma.v_empty : sh.mma.k_empty;
+    wait(is_v ? &sh.mma.vmeta_free[slot] : &sh.mma.meta_free[slot], free_par);
+    // the last chunk of the tile that was there: commits come in order
+    wait(&empty[stage + kNC - 1], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
+    uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
+    TileMeta& meta = sh.mma.meta[slot];
+    float vsc = 1.f;
+#pragma unroll 1
+    for (int r = 0; r < Cfg::kRuns; ++r) {
+      const int rows = min(Cfg::kRun, keys - j * kTileKeys - r * Cfg::kRun);
+      float x[Cfg::kRunRows][kPL];
+      if (rows > 0) wait(&sh.stg_full[at.stage], at.phase);
+#pragma unroll
+      for (int i = 0; i < Cfg::kRunRows; ++i) {
+        const int row = cw + Cfg::kConvWarps * i;
+#pragma unroll
+        for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
+        if (row < rows)
+          load_row<kPL>(reinterpret_cast<const float*>(staging + at.stage * Cfg::kRunBytes) +
+                            row * kHd,
+                        lane, x[i]);
+      }
+      if (rows > 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.stg_empty[at.stage]);
+        at.next();
+      }
+      float am[Cfg::kRunRows];
+      uint32_t fin = 0;
+#pragma unroll
+      for (int i = 0; i < Cfg::kRunRows; ++i) {
+        bool f;
+        am[i] = row_amax<kPL>(x[i], f);
+        fin |= static_cast<uint32_t>(f) << i;
+      }
+      if (is_v && r == 0) {
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < Cfg::kRunRows; ++i) a = fmaxf(a, (fin >> i) & 1u ? am[i] : 0.f);
+        if (lane == 0) sh.vmax[cw] = a;
+        if (cw == 0 && lane < 2) sh.left_out[j][lane] = 0;
+        bar_sync(5, 32 * Cfg::kConvWarps);
+        a = fmaxf(fmaxf(sh.vmax[0], sh.vmax[1]), fmaxf(sh.vmax[2], sh.vmax[3]));
+        const int e = a > 0.f ? max(split_exp(a) - 2, -126) : 0;
+        vsc = exp2i(e);
+        if (cw == 0 && lane == 0) meta.vscale = exp2i(-e);
+      }
+#pragma unroll
+      for (int i = 0; i < Cfg::kRunRows; ++i) {
+        const int row = r * Cfg::kRun + cw + Cfg::kConvWarps * i;
+        float sc;
+        if (is_v) {
+          sc = vsc;
+          const float top = am[i] * vsc;
+          const bool in = ((fin >> i) & 1u) && (am[i] == 0.f || (top >= 0.125f && top <= 65504.f));
+          if (!in) {
+#pragma unroll
+            for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
+            if (lane == 0) atomicOr(&sh.left_out[j][row >> 5], 1u << (row & 31));
+          }
+        } else {
+          const int e = split_exp(am[i]);
+          sc = exp2i(e);
+          if (lane == 0) meta.kscale[row] = exp2i(-e);
+        }
+        store_split_row<typename Cfg::Base>(x[i], sc, row, lane, dst);
+      }
+    }
+    if (is_v) {
+      bar_sync(5, 32 * Cfg::kConvWarps);          // every warp's left_out is in
+      if (cw == 0 && lane < 2) meta.left_out[lane] = sh.left_out[j][lane];
+    }
+    fence_proxy_async_smem();                     // generic stores -> visible to the MMAs
+    __syncwarp();
+    if (lane == 0) {
+      uint64_t* full = is_v ? sh.mma.v_full : sh.mma.k_full;
+      for (int c = 0; c < kNC; ++c) mbar_arrive(&full[stage + c]);
+      mbar_arrive(is_v ? &sh.mma.vmeta_full[slot] : &sh.mma.meta_full[slot]);
+    }
+  }
+  if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttLoad);
+}
+
+// grid (pieces * row tiles, n_kv)
+template <int kHd, bool kCap>
+__global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
+    prefix_mma_kernel(const __grid_constant__ PrefixParams p) {
+  using Cfg = PrefixCfg<kHd>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* k_ring = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  uint8_t* v_ring = k_ring + Cfg::kStages * Cfg::kUnit;
+  uint8_t* staging = v_ring + Cfg::kStages * Cfg::kUnit;
+  auto& sh = *reinterpret_cast<PrefixShared<kHd>*>(staging + Cfg::kStaging * Cfg::kRunBytes);
+  pdl_launch_dependents();
+  const int piece = blockIdx.x / p.row_tiles, rt = blockIdx.x - piece * p.row_tiles;
+  const int g = blockIdx.y;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int ka = piece * p.chunk, keys = min(p.n_prefix, ka + p.chunk) - ka;
+  const int n = (keys + kTileKeys - 1) / kTileKeys;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::kStaging; ++s) {
+      mbar_init(&sh.stg_full[s], 1);
+      mbar_init(&sh.stg_empty[s], Cfg::kConvWarps);
+    }
+    mma_init_barriers<Cfg>(sh.mma, Cfg::kConvWarps);
+  }
+  if (warp == Cfg::kMmaQk) {
+    tmem_alloc(&sh.mma.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  const int64_t at = (static_cast<int64_t>(g) * p.max_prefix + ka) * kHd;
+  if (warp >= Cfg::kConv) {
+    regs_dec<104>();
+    prefix_convert<kHd>(sh, staging, k_ring, v_ring, keys, n);
+  } else if (warp >= Cfg::kRowsWarps) {
+    regs_dec<56>();
+    if (warp == Cfg::kLoadK && lane == 0)
+      prefix_load<kHd>(sh, staging, p.kp + at, p.vp + at, keys, n);
+    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh.mma, k_ring, n, &g_err_prefix);
+    if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh.mma, v_ring, n, &g_err_prefix);
+  } else {
+    regs_inc<176>();
+    const int row = 32 * (warp & 3) + lane, part = warp >> 2;
+    const int r = rt * kTileRows + row, live = p.batch * p.group;
+    const bool alive = r < live;
+    const int rc = min(r, live - 1);
+    const float* q = p.q.data + static_cast<int64_t>(p.b0 + rc / p.group) * p.q.token_stride +
+                     (g * p.group + rc % p.group) * p.q.head_stride;
+    RowState<Cfg> st;
+    bool dead;
+    mma_rows<Cfg, kCap>(sh.mma, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
+    if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttRows);
+    if (st.any_left_out && alive) {
+      for (int t = 0; t < keys; ++t)
+        if ((sh.left_out[t / kTileKeys][(t % kTileKeys) >> 5] >> (t & 31)) & 1u)
+          add_left_out<Cfg>(st, q, p.kp + at + static_cast<int64_t>(t) * kHd,
+                            p.vp + at + static_cast<int64_t>(t) * kHd, part, p.scale, p.cap);
+    }
+    if (alive && !dead) {
+      constexpr float kUnshift = 1.0f / (1 << kPShift);
+      float* dst = p.part + prefix_part<kHd / 32>(p, piece, g, r);
+      store_columns<Cfg>(st, dst, part, kUnshift);
+      if (part == 0) {
+        dst[kHd] = st.m;
+        dst[kHd + 1] = st.l * kUnshift;
+      }
+    }
+  }
+  // every MMA has completed before tensor memory is freed
+  tc_fence_before();
+  __syncthreads();
+  if (warp == Cfg::kMmaQk) {
+    for (int i = 0; i < 2; ++i)
+      if (lane == 0 && !mbar_wait(&sh.mma.done[i], 0)) atomicOr(&g_err_prefix, kErrAttMma);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(sh.mma.tmem, 512);
   }
 }
 
@@ -229,7 +490,11 @@ namespace {
 constexpr int kPrefixR = 4;
 constexpr int kPrefixRows = kRowWarps * kPrefixR;
 
+constexpr int64_t kPrefixMmaFrom = 1;
+
 struct PrefixPlan {
+  bool mma;              // the shared part on the tensor cores
+  int rows;              // of a row tile
   int chunk, pieces;
   size_t part_floats, own_floats;    // of the largest launch
 };
@@ -238,11 +503,20 @@ PrefixPlan plan_prefix(int64_t n_prefix, const int64_t* n_ctx, int batch, int n_
                        int head_dim) {
   PrefixPlan pl;
   const int group = n_q / n_kv, some = std::min(batch, kMaxBatch);
-  const int64_t tiles = (static_cast<int64_t>(some) * group + kPrefixRows - 1) / kPrefixRows;
-  // about two items an SM
-  const int64_t want = std::max<int64_t>(1, 304 / (tiles * n_kv));
-  int64_t chunk = (n_prefix + want - 1) / want;
-  chunk = std::max<int64_t>(64, (chunk + 31) / 32 * 32);
+  pl.mma = n_prefix >= kPrefixMmaFrom;
+  pl.rows = pl.mma ? kTileRows : kPrefixRows;
+  const int64_t tiles = (static_cast<int64_t>(some) * group + pl.rows - 1) / pl.rows;
+  int64_t chunk;
+  if (pl.mma) {
+    // one item an SM
+    const int64_t want = std::max<int64_t>(1, 152 / (tiles * n_kv));
+    const int64_t key_tiles = (n_prefix + kTileKeys - 1) / kTileKeys;
+    chunk = std::min<int64_t>((key_tiles + want - 1) / want, kMaxPieceTiles) * kTileKeys;
+  } else {
+    // about two items an SM
+    const int64_t want = std::max<int64_t>(1, 304 / (tiles * n_kv));
+    chunk = std::max<int64_t>(64, ((n_prefix + want - 1) / want + 31) / 32 * 32);
+  }
   pl.chunk = static_cast<int>(chunk);
   pl.pieces = static_cast<int>((n_prefix + chunk - 1) / chunk);
   const size_t row = static_cast<size_t>(head_dim) + kPartPad;
@@ -259,11 +533,24 @@ PrefixPlan plan_prefix(int64_t n_prefix, const int64_t* n_ctx, int batch, int n_
 }
 
 template <int kPL>
-cudaError_t run_prefix(const PrefixParams& p, cudaStream_t st) {
+cudaError_t run_prefix(const PrefixParams& p, const PrefixPlan& pl, cudaStream_t st) {
   using Tile = RowTile<kPL, kPrefixR>;
   cudaError_t e = cudaSuccess;
   const unsigned nkv = static_cast<unsigned>(p.n_kv);
-  if (p.pieces > 0) {
+  if (p.pieces > 0 && pl.mma) {
+    constexpr int kHd = kPL * 32;
+    using Cfg = PrefixCfg<kHd>;
+    constexpr size_t kSmem =
+        1024 + Cfg::kRing + Cfg::kStaging * Cfg::kRunBytes + sizeof(PrefixShared<kHd>);
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    const auto kernel = p.cap > 0.f ? prefix_mma_kernel<kHd, true> : prefix_mma_kernel<kHd, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmem));
+    if (e != cudaSuccess) return e;
+    e = pdl_launch(kernel, dim3(static_cast<unsigned>(p.pieces * p.row_tiles), nkv), Cfg::kThreads,
+                   kSmem, st, p);
+    if (e != cudaSuccess) return e;
+  } else if (p.pieces > 0) {
     e = cudaFuncSetAttribute(prefix_rows_kernel<kPL, kPrefixR>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Tile::kSmem));
@@ -317,7 +604,7 @@ cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const f
   for (int b0 = 0; b0 < batch; b0 += kMaxBatch) {
     p.b0 = b0;
     p.batch = std::min(batch - b0, kMaxBatch);
-    p.row_tiles = (p.batch * p.group + kPrefixRows - 1) / kPrefixRows;
+    p.row_tiles = (p.batch * p.group + pl.rows - 1) / pl.rows;
     p.first[0] = 0;
     for (int b = 0; b < p.batch; ++b) {
       p.n_ctx[b] = static_cast<int>(n_ctx[b0 + b]);
@@ -325,14 +612,21 @@ cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const f
     }
     cudaError_t e = cudaErrorInvalidValue;
     switch (head_dim) {
-      case 32: e = run_prefix<1>(p, st); break;
-      case 64: e = run_prefix<2>(p, st); break;
-      case 128: e = run_prefix<4>(p, st); break;
-      case 256: e = run_prefix<8>(p, st); break;
+      case 32: e = run_prefix<1>(p, pl, st); break;
+      case 64: e = run_prefix<2>(p, pl, st); break;
+      case 128: e = run_prefix<4>(p, pl, st); break;
+      case 256: e = run_prefix<8>(p, pl, st); break;
     }
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+unsigned read_clear_prefix_errors() {
+  unsigned v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_prefix, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_err_prefix, &z, sizeof(z));
+  return v;
 }
 
 }  // namespace qws
