@@ -148,12 +148,11 @@ __device__ __forceinline__ void scale_add2(float& d0, float& d1, float a, float 
       : "f"(a), "f"(b0), "f"(b1));
 }
 
-// The power of two 2^e that puts a into [2^14, 2^15) (1 for zero), e in +-126.
+// e with a 2^e in [2^14, 2^15) for a finite a >= 0 (0 for zero), within +-126 (a
+// subnormal a stays below).
 __device__ __forceinline__ int split_exp(float a) {
-  if (!(a > 0.f)) return 0;
-  int E;
-  frexpf(a, &E);
-  return min(126, max(-126, 15 - E));
+  const int e = 141 - static_cast<int>(__float_as_uint(a) >> 23);
+  return a > 0.f ? min(126, e) : 0;
 }
 __device__ __forceinline__ bool finite_bits(float x) {
   return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u;
@@ -423,8 +422,6 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
         x[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * (f.w * rowf);
       }
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
     if constexpr (kCap) {
 #pragma unroll
       for (int i = 0; i < kKeys; ++i) x[i] = cap * tanhf(x[i] / cap) * kLog2e;
@@ -440,6 +437,8 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
     for (int i = 1; i < kKeys; ++i) mx = fmaxf(mx, x[i]);
     sh.xmax[ph][part][row] = mx;
     row_sync();
+    // what was stored came of the scales: they have been read
+    if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
 #pragma unroll
     for (int c = 0; c < kSplit; ++c) mx = fmaxf(mx, sh.xmax[ph][c][row]);
     const float mn = fmaxf(st.m, mx);
@@ -481,9 +480,12 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
         dead = !__all_sync(0xFFFFFFFFu,
                            mbar_wait(&sh.vmeta_full[ph], static_cast<uint32_t>(j >> 1) & 1u));
       vs = sh.meta[ph].vscale;
-      st.any_left_out = st.any_left_out || (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.vmeta_free[ph]);
+      const bool left = (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]) != 0;
+      // the arrival hangs on the values read: loads that nothing has used yet may be
+      // scheduled behind it (vs is a power of two; left is the same in all lanes)
+      const uint32_t lefts = __ballot_sync(0xFFFFFFFFu, left && vs > 0.f);
+      st.any_left_out = st.any_left_out || lefts;
+      if (lane == 0 && (vs > 0.f || lefts)) mbar_arrive(&sh.vmeta_free[ph]);
 #pragma unroll
     for (int c = 0; c < Cfg::kNC; ++c) {
       wait(&sh.o_full[buf.stage], buf.phase, o_seen);
@@ -587,19 +589,23 @@ __device__ __forceinline__ void store_split_row(const float (&x)[Cfg::kHd / 32],
   }
 }
 
-// largest finite magnitude of a row over the warp; `all`: every value is finite
+// largest finite magnitude of a row over the warp; `all`: every value is finite.  The
+// bits of a magnitude compare as unsigned numbers, infinities and NaN on top.
 template <int kPL>
 __device__ __forceinline__ float row_amax(const float (&x)[kPL], bool& all) {
-  float a = 0.f;
-  bool fin = true;
+  uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < kPL; ++i) {
-    const bool f = finite_bits(x[i]);
-    fin = fin && f;
-    a = fmaxf(a, f ? fabsf(x[i]) : 0.f);
+  for (int i = 0; i < kPL; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  a = __reduce_max_sync(0xFFFFFFFFu, a);
+  all = a < 0x7F800000u;
+  if (!all) {
+    a = 0;
+#pragma unroll
+    for (int i = 0; i < kPL; ++i)
+      a = max(a, finite_bits(x[i]) ? __float_as_uint(x[i]) & 0x7FFFFFFFu : 0u);
+    a = __reduce_max_sync(0xFFFFFFFFu, a);
   }
-  all = __all_sync(0xFFFFFFFFu, fin);
-  return warp_max(a);
+  return __uint_as_float(a);
 }
 
 // 64 keys of one kv head, n of them there (the rest zero), by a CTA of 256

@@ -198,6 +198,46 @@ __device__ __forceinline__ void store_partial(float* dst, int lane, const float 
   }
 }
 
+// Joins the n partial results of a row in order, by one warp: the weights of all pieces
+// first (a lane a piece), then the weighted sum of this warp's columns, kV neighbours
+// a lane from column col on.  part(c) is piece c's row.  Returns the row's sum.
+template <int kHd, int kV, class Part>
+__device__ __forceinline__ float join_parts(int n, int lane, int col, Part&& part,
+                                            float (&acc)[kV]) {
+  float M = -INFINITY;
+  for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c)[kHd]);
+  M = warp_max(M);
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    float w = 0.f;
+    if (c0 + lane < n) {
+      const float* p = part(c0 + lane);
+      w = exp2f(p[kHd] - base);
+      L = fmaf(p[kHd + 1], w, L);
+    }
+    const int m = min(32, n - c0);
+#pragma unroll 8
+    for (int c = 0; c < m; ++c) {
+      const float f = __shfl_sync(0xFFFFFFFFu, w, c);
+      const float* p = part(c0 + c) + col;
+      if constexpr (kV == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
+        acc[2] = fmaf(v.z, f, acc[2]); acc[3] = fmaf(v.w, f, acc[3]);
+      } else if constexpr (kV == 2) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
+      } else {
+        acc[0] = fmaf(p[0], f, acc[0]);
+      }
+    }
+  }
+  return warp_sum(L);
+}
+
 // out = acc / l; a row that saw no key is zero
 template <int kPL>
 __device__ __forceinline__ void store_final(float* dst, int lane, float (&acc)[kPL], float l) {

@@ -178,6 +178,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
   };
+  bool seen = false;           // the next run of rows was seen to be there
 #pragma unroll 1
   for (int jh = 0; jh < 2 * n; ++jh) {
     const int j = jh >> 1, slot = j & 1;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     for (int r = 0; r < Cfg::kRuns; ++r) {
       const int rows = min(Cfg::kRun, keys - j * kTileKeys - r * Cfg::kRun);
       float x[Cfg::kRunRows][kPL];
-      if (rows > 0) wait(&sh.stg_full[at.stage], at.phase);
+      if (rows > 0 && !__all_sync(0xFFFFFFFFu, seen)) wait(&sh.stg_full[at.stage], at.phase);
 #pragma unroll
       for (int i = 0; i < Cfg::kRunRows; ++i) {
         const int row = cw + Cfg::kConvWarps * i;
@@ -206,11 +207,6 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
                             row * kHd,
                         lane, x[i]);
       }
-      if (rows > 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.stg_empty[at.stage]);
-        at.next();
-      }
       float am[Cfg::kRunRows];
       uint32_t fin = 0;
 #pragma unroll
@@ -218,6 +214,16 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
         bool f;
         am[i] = row_amax<kPL>(x[i], f);
         fin |= static_cast<uint32_t>(f) << i;
+      }
+      if (rows > 0) {
+        // the stage may be overwritten once every lane HAS its values: loads that nothing
+        // has used yet may be scheduled behind the arrival, so it hangs on the maxima
+        uint32_t had = 0;
+#pragma unroll
+        for (int i = 0; i < Cfg::kRunRows; ++i) had |= __float_as_uint(am[i]);
+        if (lane == 0 && had != 0xFFFFFFFFu) mbar_arrive(&sh.stg_empty[at.stage]);
+        at.next();
+        seen = mbar_test(&sh.stg_full[at.stage], at.phase);
       }
       if (is_v && r == 0) {
         float a = 0.f;
@@ -448,40 +454,31 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
   }
 }
 
-// One warp per (sequence, query head): the prefix pieces, then the own ones.
+// One warp per (sequence, query head, 64 columns): the prefix pieces, then the own ones.
 template <int kPL>
 __global__ void __launch_bounds__(128)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p) {
-  constexpr int kHd = kPL * 32;
+  constexpr int kHd = kPL * 32, kV = kPL >= 2 ? 2 : 1, kWide = kHd / (32 * kV);
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
   const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int b = w / p.n_q, h = w - b * p.n_q, g = h / p.group;
+  const int rh = w / kWide, c0 = (w - rh * kWide) * 32 * kV;
+  const int b = rh / p.n_q, h = rh - b * p.n_q, g = h / p.group;
   if (b >= p.batch) return;
   const int row = b * p.group + (h - g * p.group);
-  float m = -INFINITY, l = 0.f, acc[kPL];
-#pragma unroll
-  for (int j = 0; j < kPL; ++j) acc[j] = 0.f;
-  auto join = [&](const float* src) {
-    float x[kPL];
-    load_row<kPL>(src, lane, x);
-    const float mc = src[kHd], lc = src[kHd + 1];
-    const float mn = fmaxf(m, mc);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(m - base), c = exp2f(mc - base);
-    l = fmaf(l, a, lc * c);
-#pragma unroll
-    for (int j = 0; j < kPL; ++j) acc[j] = fmaf(acc[j], a, x[j] * c);
-    m = mn;
+  const auto part = [&](int c) {
+    return c < p.pieces
+               ? p.part + prefix_part<kPL>(p, c, g, row)
+               : p.own + ((static_cast<int64_t>(p.first[b] + c - p.pieces) * p.n_kv + g) * p.group +
+                          (h - g * p.group)) * (kHd + kPartPad);
   };
-  for (int c = 0; c < p.pieces; ++c) join(p.part + prefix_part<kPL>(p, c, g, row));
-  for (int c = p.first[b]; c < p.first[b + 1]; ++c)
-    join(p.own + ((static_cast<int64_t>(c) * p.n_kv + g) * p.group + (h - g * p.group)) *
-                     (kHd + kPartPad));
-  store_final<kPL>(p.out.data + static_cast<int64_t>(p.b0 + b) * p.out.token_stride +
-                       h * p.out.head_stride,
-                   lane, acc, l);
+  float acc[kV];
+  const float l = join_parts<kHd, kV>(p.pieces + p.first[b + 1] - p.first[b], lane,
+                                      c0 + lane * kV, part, acc);
+  store_final<kV>(p.out.data + static_cast<int64_t>(p.b0 + b) * p.out.token_stride +
+                      h * p.out.head_stride + c0,
+                  lane, acc, l);
 }
 
 // ------------------------------------------------------------ host side
@@ -571,8 +568,9 @@ cudaError_t run_prefix(const PrefixParams& p, const PrefixPlan& pl, cudaStream_t
     }
     if (e != cudaSuccess) return e;
   }
-  const int rows = p.batch * p.n_q;
-  return pdl_launch(prefix_merge_kernel<kPL>, dim3(static_cast<unsigned>((rows + 3) / 4)), 128,
+  constexpr int kWide = kPL > 2 ? kPL / 2 : 1;          // warps of a row
+  const int warps = p.batch * p.n_q * kWide;
+  return pdl_launch(prefix_merge_kernel<kPL>, dim3(static_cast<unsigned>((warps + 3) / 4)), 128,
                     0, st, p);
 }
 

@@ -147,25 +147,18 @@ __global__ void __launch_bounds__(256)
   tile_span(p, it);
   if (it.pieces < 2) return;
   const int row = (i - it.i0) * p.group + (h - g * p.group);
-  float m = -INFINITY, l = 0.f, acc[kPL];
+  const auto part = [&](int c) {
+    return p.part + (part_slot(p, it, c, g) * p.rows + row) * (kHd + kPartPad);
+  };
+  constexpr int kV = kPL >= 4 ? 4 : kPL;
+  float* dst = p.out.data + static_cast<int64_t>(token) * p.out.token_stride +
+               h * p.out.head_stride;
 #pragma unroll
-  for (int j = 0; j < kPL; ++j) acc[j] = 0.f;
-  for (int c = 0; c < it.pieces; ++c) {
-    const float* src = p.part + (part_slot(p, it, c, g) * p.rows + row) * (kHd + kPartPad);
-    float x[kPL];
-    load_row<kPL>(src, lane, x);
-    const float mc = src[kHd], lc = src[kHd + 1];
-    const float mn = fmaxf(m, mc);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(m - base), b = exp2f(mc - base);
-    l = fmaf(l, a, lc * b);
-#pragma unroll
-    for (int j = 0; j < kPL; ++j) acc[j] = fmaf(acc[j], a, x[j] * b);
-    m = mn;
+  for (int c = 0; c < kHd; c += 32 * kV) {
+    float acc[kV];
+    const float l = join_parts<kHd, kV>(it.pieces, lane, c + lane * kV, part, acc);
+    store_final<kV>(dst + c, lane, acc, l);
   }
-  store_final<kPL>(p.out.data + static_cast<int64_t>(token) * p.out.token_stride +
-                       h * p.out.head_stride,
-                   lane, acc, l);
 }
 
 // ------------------------------------------------------------ tensor cores
