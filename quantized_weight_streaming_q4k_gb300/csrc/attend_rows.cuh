@@ -198,44 +198,68 @@ __device__ __forceinline__ void store_partial(float* dst, int lane, const float 
   }
 }
 
-// Joins the n partial results of a row in order, by one warp: the weights of all pieces
-// first (a lane a piece), then the weighted sum of this warp's columns, kV neighbours
-// a lane from column col on.  part(c) is piece c's row.  Returns the row's sum.
-template <int kHd, int kV, class Part>
-__device__ __forceinline__ float join_parts(int n, int lane, int col, Part&& part,
+// Joins the n partial results of a row in order, by one warp, for its columns, kV
+// neighbours a lane from column col on.  part(c) is piece c's row, called by the whole
+// warp with one c; mine(c) the same, called by some lanes, lane i with c = i modulo 32
+// (so neither may exchange values between lanes there).  The columns of a
+// batch of pieces are fetched together with, not after, the maxima that weigh them: one
+// trip to memory and not three.  Returns the row's sum.
+template <int kHd, int kV, class Mine, class Part>
+__device__ __forceinline__ float join_parts(int n, int lane, int col, Mine&& mine, Part&& part,
                                             float (&acc)[kV]) {
-  float M = -INFINITY;
-  for (int c = lane; c < n; c += 32) M = fmaxf(M, part(c)[kHd]);
-  M = warp_max(M);
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
+  constexpr int kBatch = 32 / kV;
+  float M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
   for (int c0 = 0; c0 < n; c0 += 32) {
-    float w = 0.f;
-    if (c0 + lane < n) {
-      const float* p = part(c0 + lane);
-      w = exp2f(p[kHd] - base);
-      L = fmaf(p[kHd + 1], w, L);
-    }
     const int m = min(32, n - c0);
-#pragma unroll 8
-    for (int c = 0; c < m; ++c) {
-      const float f = __shfl_sync(0xFFFFFFFFu, w, c);
-      const float* p = part(c0 + c) + col;
-      if constexpr (kV == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
-        acc[2] = fmaf(v.z, f, acc[2]); acc[3] = fmaf(v.w, f, acc[3]);
-      } else if constexpr (kV == 2) {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        acc[0] = fmaf(v.x, f, acc[0]); acc[1] = fmaf(v.y, f, acc[1]);
-      } else {
-        acc[0] = fmaf(p[0], f, acc[0]);
+    float mc = -INFINITY, lc = 0.f;
+    if (lane < m) {
+      const float2 ml = *reinterpret_cast<const float2*>(mine(c0 + lane) + kHd);
+      mc = ml.x;
+      lc = ml.y;
+    }
+    for (int b0 = 0; b0 < m; b0 += kBatch) {
+      float v[kBatch][kV];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[c][i] = 0.f;
+        if (b0 + c < m) {
+          const float* p = part(c0 + b0 + c) + col;
+          if constexpr (kV == 4) {
+            const float4 q = *reinterpret_cast<const float4*>(p);
+            v[c][0] = q.x; v[c][1] = q.y; v[c][2] = q.z; v[c][3] = q.w;
+          } else if constexpr (kV == 2) {
+            const float2 q = *reinterpret_cast<const float2*>(p);
+            v[c][0] = q.x; v[c][1] = q.y;
+          } else {
+            v[c][0] = p[0];
+          }
+        }
+      }
+      if (b0 == 0) {
+        // this group's maximum joins the running one
+        const float Mn = fmaxf(M, warp_max(mc));
+        const float base = Mn == -INFINITY ? 0.f : Mn;
+        const float old = exp2f(M - base);
+        lc *= mc = exp2f(mc - base);                  // mc: from here on the weight
+        L = fmaf(L, old, warp_sum(lc));
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] *= old;
+        M = Mn;
+      }
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float f = __shfl_sync(0xFFFFFFFFu, mc, (b0 + c) & 31);
+        if (b0 + c < m) {
+#pragma unroll
+          for (int i = 0; i < kV; ++i) acc[i] = fmaf(v[c][i], f, acc[i]);
+        }
       }
     }
   }
-  return warp_sum(L);
+  return L;
 }
 
 // out = acc / l; a row that saw no key is zero

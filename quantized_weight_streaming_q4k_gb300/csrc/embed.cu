@@ -3,10 +3,12 @@
 // when the two are tied):
 //   out[t][i] = scale * dequant(W)[token[t]][i].
 //
-// One thread writes four consecutive values with one 16-byte store and reads
-// the 2 to 4 bytes of codes behind them, the block's f16 scale(s) and its
+// One thread writes runs of four consecutive values with 16-byte stores and reads
+// the 2 to 4 bytes of codes behind each, the block's f16 scale(s) and its
 // sub-block scale; the reads of a block's scales hit L1 for all but the first
-// thread.  Bound by writing out: 4 bytes written per 0.56 to 1.06 read.
+// thread.  Bound by writing out (4 bytes written per 0.56 to 1.06 read) for many
+// tokens: five runs a thread (a row of 2560 is one CTA) keep enough bytes in flight
+// behind the two dependent reads, the token and its row.
 //
 // Rounding: a Q4_0, Q8_0 or Q6_K weight d * sc * q is exact in f32 (11 + 7 + 6
 // bits at most); a Q4_K weight d * sc * q - dmin * m is one fma of two exact
@@ -22,6 +24,7 @@ namespace qws {
 __device__ unsigned g_err_embed;
 
 constexpr int kEmbThreads = 128;
+constexpr int kEmbRuns = 5;
 
 __device__ __forceinline__ uint32_t ld_u16(const uint8_t* p) {
   return __ldg(reinterpret_cast<const unsigned short*>(p));
@@ -81,8 +84,7 @@ __device__ __forceinline__ float4 embed_four(const uint8_t* row, int64_t c) {
   return make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// grid.x = n_tokens * segs; block b of a token covers values
-// [seg * 4 * kEmbThreads, ...) of its row
+// grid.x = n_tokens * segs: a CTA covers 4 * kEmbThreads * kEmbRuns values of a row
 template <int kFmt>
 __global__ void __launch_bounds__(kEmbThreads)
     embed_kernel(const uint8_t* __restrict__ W, const int64_t* __restrict__ tokens,
@@ -93,22 +95,30 @@ __global__ void __launch_bounds__(kEmbThreads)
   const int64_t t = blockIdx.x / static_cast<unsigned>(segs);
   const int seg = static_cast<int>(blockIdx.x - t * segs);
   const int64_t tok = __ldg(tokens + t);
-  const int64_t c = (static_cast<int64_t>(seg) * kEmbThreads + threadIdx.x) * 4;
-  if (c >= hidden) return;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (tok >= 0 && tok < vocab) {
-    v = embed_four<kFmt>(W + tok * row_bytes, c);
-    v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
-  } else if (threadIdx.x == 0) {
-    atomicOr(&g_err_embed, kErrTokenRange);
+  const int64_t c0 = (static_cast<int64_t>(seg) * kEmbRuns * kEmbThreads + threadIdx.x) * 4;
+  const bool known = tok >= 0 && tok < vocab;
+  if (!known && threadIdx.x == 0) atomicOr(&g_err_embed, kErrTokenRange);
+  float4 v[kEmbRuns];
+#pragma unroll
+  for (int r = 0; r < kEmbRuns; ++r) {
+    const int64_t c = c0 + r * kEmbThreads * 4;
+    v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (known && c < hidden) v[r] = embed_four<kFmt>(W + tok * row_bytes, c);
   }
-  *reinterpret_cast<float4*>(out + t * hidden + c) = v;
+#pragma unroll
+  for (int r = 0; r < kEmbRuns; ++r) {
+    const int64_t c = c0 + r * kEmbThreads * 4;
+    if (c < hidden)
+      *reinterpret_cast<float4*>(out + t * hidden + c) =
+          make_float4(v[r].x * scale, v[r].y * scale, v[r].z * scale, v[r].w * scale);
+  }
 }
 
 cudaError_t launch_embed(int fmt, const uint8_t* W, const int64_t* tokens, float* out,
                          int64_t vocab, int64_t hidden, int64_t n_tokens, float scale,
                          cudaStream_t st) {
-  const int segs = static_cast<int>((hidden / 4 + kEmbThreads - 1) / kEmbThreads);
+  const int segs = static_cast<int>((hidden / 4 + kEmbThreads * kEmbRuns - 1) /
+                                    (kEmbThreads * kEmbRuns));
   const int64_t rb = row_bytes_of(fmt, hidden);
   const dim3 grid(static_cast<unsigned>(n_tokens * segs));
   switch (fmt) {

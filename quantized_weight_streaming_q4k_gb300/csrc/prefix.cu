@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(128)
   };
   float acc[kV];
   const float l = join_parts<kHd, kV>(p.pieces + p.first[b + 1] - p.first[b], lane,
-                                      c0 + lane * kV, part, acc);
+                                      c0 + lane * kV, part, part, acc);
   store_final<kV>(p.out.data + static_cast<int64_t>(p.b0 + b) * p.out.token_stride +
                       h * p.out.head_stride + c0,
                   lane, acc, l);

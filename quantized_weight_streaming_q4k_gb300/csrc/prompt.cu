@@ -19,9 +19,9 @@ __device__ unsigned g_err_prompt;
 // A tile is `rows` query rows of one kv head: tok = rows / group tokens with
 // the group's heads side by side, row r = token r / group, head r % group.  Its
 // keys are cut into pieces of `chunk`; an item is one piece.  A sequence's
-// items are a rectangle (pieces of its last tile x tiles): pieces beyond a
-// tile's visible keys do nothing.  A tile of one piece writes out, the others
-// leave partials that prompt_merge_kernel joins.
+// items come by piece, first every tile's piece 0, the longest tile first, then
+// piece 1 of the tiles that have one, and so on.  A tile of one piece writes out, the
+// others leave partials that prompt_merge_kernel joins.
 struct PromptParams {
   qws_heads q, k, v, out;
   float* part;
@@ -51,23 +51,40 @@ __device__ __forceinline__ void tile_span(const PromptParams& p, PromptItem& it)
   it.pieces = max(1, (it.vis + p.chunk - 1) / p.chunk);
 }
 
+// Tiles from this one on have a piece `piece` (they see more than piece * chunk keys).
+__host__ __device__ __forceinline__ int first_tile(int piece, int chunk, int tok, int n_q,
+                                                   int n_k) {
+  const int64_t need = static_cast<int64_t>(piece) * chunk - (static_cast<int64_t>(n_k) - n_q);
+  return piece == 0 || need <= 0 ? 0 : static_cast<int>(need / tok);
+}
+
 __device__ __forceinline__ PromptItem prompt_item(const PromptParams& p, int item) {
   PromptItem it;
   it.s = find_seq(p.seqs.item, p.seqs.n, item);
   it.n_q = p.seqs.q0[it.s + 1] - p.seqs.q0[it.s];
   it.n_k = p.seqs.k0[it.s + 1] - p.seqs.k0[it.s];
   it.tiles = (it.n_q + p.tok - 1) / p.tok;
-  const int local = item - p.seqs.item[it.s];
-  it.piece = local / it.tiles;
-  it.tile = it.tiles - 1 - (local - it.piece * it.tiles);   // the longest first
+  int local = item - p.seqs.item[it.s];
+  for (it.piece = 0;; ++it.piece) {
+    const int have = it.tiles - first_tile(it.piece, p.chunk, p.tok, it.n_q, it.n_k);
+    if (local < have) break;
+    local -= have;
+  }
+  it.tile = it.tiles - 1 - local;
   tile_span(p, it);
   return it;
 }
 
-__device__ __forceinline__ int64_t part_slot(const PromptParams& p, const PromptItem& it,
-                                             int piece, int g) {
-  const int item = p.seqs.item[it.s] + piece * it.tiles + (it.tiles - 1 - it.tile);
-  return static_cast<int64_t>(item) * p.n_kv + g;
+// the item number of piece 0 of a tile; of the next piece: + next_piece()
+__device__ __forceinline__ int first_item(const PromptParams& p, const PromptItem& it) {
+  return p.seqs.item[it.s] + it.tiles - 1 - it.tile;
+}
+__device__ __forceinline__ int next_piece(const PromptParams& p, const PromptItem& it,
+                                          int piece) {
+  return it.tiles - first_tile(piece, p.chunk, p.tok, it.n_q, it.n_k);
+}
+__device__ __forceinline__ float* part_rows(const PromptParams& p, int item, int g, int hd) {
+  return p.part + (static_cast<int64_t>(item) * p.n_kv + g) * p.rows * (hd + kPartPad);
 }
 
 // ------------------------------------------------------------ CUDA cores, f32
@@ -79,9 +96,8 @@ __global__ void __launch_bounds__(kRowThreads)
   extern __shared__ __align__(16) float smem[];
   pdl_launch_dependents();
   pdl_wait();
-  const PromptItem it = prompt_item(p, blockIdx.x);
-  if (it.piece >= it.pieces) return;
-  const int g = blockIdx.y;
+  const int item = blockIdx.x / p.n_kv, g = blockIdx.x - item * p.n_kv;
+  const PromptItem it = prompt_item(p, item);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t q_base = p.seqs.q0[it.s], k_base = p.seqs.k0[it.s];
   const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
@@ -112,9 +128,8 @@ __global__ void __launch_bounds__(kRowThreads)
     const int row = warp * kR + r;
     if (row >= live) continue;
     if (it.pieces > 1) {
-      store_partial<kPL>(
-          p.part + (part_slot(p, it, it.piece, g) * p.rows + row) * (kHd + kPartPad), lane,
-          tile.acc[r], tile.m[r], tile.l[r]);
+      store_partial<kPL>(part_rows(p, item, g, kHd) + row * (kHd + kPartPad), lane, tile.acc[r],
+                         tile.m[r], tile.l[r]);
     } else {
       const int i = it.i0 + row / p.group, h = g * p.group + row % p.group;
       store_final<kPL>(p.out.data + (q_base + i) * p.out.token_stride + h * p.out.head_stride,
@@ -147,16 +162,19 @@ __global__ void __launch_bounds__(256)
   tile_span(p, it);
   if (it.pieces < 2) return;
   const int row = (i - it.i0) * p.group + (h - g * p.group);
-  const auto part = [&](int c) {
-    return p.part + (part_slot(p, it, c, g) * p.rows + row) * (kHd + kPartPad);
-  };
+  // lane c holds where piece c is (a tile has at most 32: the plan sees to it)
+  int64_t where = first_item(p, it);
+  for (int c = 1; c <= lane && c < it.pieces; ++c) where += next_piece(p, it, c - 1);
+  where = ((where * p.n_kv + g) * p.rows + row) * (kHd + kPartPad);
+  const auto mine = [&](int) { return p.part + where; };
+  const auto part = [&](int c) { return p.part + __shfl_sync(0xFFFFFFFFu, where, c); };
   constexpr int kV = kPL >= 4 ? 4 : kPL;
   float* dst = p.out.data + static_cast<int64_t>(token) * p.out.token_stride +
                h * p.out.head_stride;
 #pragma unroll
   for (int c = 0; c < kHd; c += 32 * kV) {
     float acc[kV];
-    const float l = join_parts<kHd, kV>(it.pieces, lane, c + lane * kV, part, acc);
+    const float l = join_parts<kHd, kV>(it.pieces, lane, c + lane * kV, mine, part, acc);
     store_final<kV>(dst + c, lane, acc, l);
   }
 }
@@ -190,10 +208,9 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   auto& sh = *reinterpret_cast<MmaShared<Cfg>*>(stages + Cfg::kRing);
-  const PromptItem it = prompt_item(p, blockIdx.x);
+  const int item = blockIdx.x / p.n_kv, g = blockIdx.x - item * p.n_kv;
+  const PromptItem it = prompt_item(p, item);
   pdl_launch_dependents();
-  if (it.piece >= it.pieces) return;
-  const int g = blockIdx.y;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
   const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
@@ -282,8 +299,7 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
     if (alive && !dead) {
       constexpr float kUnshift = 1.0f / (1 << kPShift);
       if (it.pieces > 1) {
-        float* dst =
-            p.part + (part_slot(p, it, it.piece, g) * p.rows + row) * (kHd + kPartPad);
+        float* dst = part_rows(p, item, g, kHd) + row * (kHd + kPartPad);
         store_columns<Cfg>(st, dst, part, kUnshift);
         if (part == 0) {
           dst[kHd] = st.m;
@@ -322,35 +338,59 @@ struct PromptPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// items of a sequence, as prompt_item counts them
+int64_t seq_items(int64_t nq, int64_t nk, int tok, int chunk) {
+  if (nq == 0) return 0;
+  const int64_t tiles = ceil_div(nq, tok);
+  int64_t items = tiles;
+  for (int64_t piece = 1; piece * chunk < nk; ++piece)
+    items += tiles - first_tile(static_cast<int>(piece), chunk, tok, static_cast<int>(nq),
+                                static_cast<int>(nk));
+  return items;
+}
+
 // The form, tile and piece lengths of a call, and the sizes of its workspace.
 PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
                        int head_dim) {
   PromptPlan pl = {};
   const int group = n_q / n_kv;
-  // (row, key) pairs that are scored, per kv head, counted in whole rows
-  int64_t pairs = 0;
+  // (row, key) pairs that are scored, per kv head, and the longest sequence's keys
+  int64_t pairs = 0, longest = 1;
   for (int s = 0; s < n_seqs; ++s) {
     const int64_t nq = cu_q[s + 1] - cu_q[s], nk = cu_k[s + 1] - cu_k[s];
     pairs += nq * group * std::max<int64_t>(1, nk - std::min(nq, nk) / 2);
+    if (nq) longest = std::max(longest, nk);
   }
   pl.mma = pairs * n_kv > kMmaFrom;
   pl.rows = pl.mma ? kTileRows : 4 * kRowWarps;
   pl.tok = pl.rows / group;
-  pl.chunk = 512;
-  if (pl.mma) {
-    // about eight pieces an SM, of at least 8 tiles
-    const int64_t tiles = pairs / (kTileRows * kTileKeys) * n_kv;
-    pl.chunk = static_cast<int>(std::max<int64_t>(8, ceil_div(tiles, 8 * 152))) * kTileKeys;
+  const int unit = pl.mma ? kTileKeys : 32;         // keys of a step
+  const int slots = pl.mma ? 152 : 304;             // items that run at once
+  // steps of the longest tile, and an SM's share of all
+  const int64_t steps = ceil_div(longest, unit);
+  const int64_t share = ceil_div(pairs * n_kv, static_cast<int64_t>(pl.rows) * unit * slots);
+  // A tile is cut where it is longer than an SM's share of the work.  Each item costs
+  // kItemSteps more; of 1 .. 32 pieces of the longest tile the number is taken whose
+  // last wave ends first, were all tiles that long.
+  constexpr int64_t kItemSteps = 5;
+  int64_t best = 1, best_cost = INT64_MAX;
+  const int64_t tiles = std::max<int64_t>(1, pairs * n_kv / (pl.rows * unit * steps));
+  for (int64_t k = 1; k <= 32 && (k == 1 || (steps > share && ceil_div(steps, k) >= 2)); ++k) {
+    const int64_t cost = ceil_div(tiles * k, slots) * (ceil_div(steps, k) + kItemSteps);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = k;
+    }
   }
+  pl.chunk = static_cast<int>(ceil_div(steps, best)) * unit;
   for (int s0 = 0; s0 < n_seqs; s0 += kMaxSeqs) {
     int64_t items = 0, ktiles = 0;
     for (int s = s0; s < std::min(n_seqs, s0 + kMaxSeqs); ++s) {
       const int64_t nq = cu_q[s + 1] - cu_q[s], nk = cu_k[s + 1] - cu_k[s];
       if (nq == 0) continue;
-      const int64_t pieces = std::max<int64_t>(1, ceil_div(nk, pl.chunk));
-      items += ceil_div(nq, pl.tok) * pieces;
+      items += seq_items(nq, nk, pl.tok, pl.chunk);
       ktiles += ceil_div(nk, kTileKeys);
-      pl.split = pl.split || pieces > 1;
+      pl.split = pl.split || nk > pl.chunk;
     }
     pl.items = std::max(pl.items, items);
     pl.ktiles = std::max(pl.ktiles, ktiles);
@@ -374,7 +414,7 @@ template <int kPL>
 cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int64_t ktiles,
                        cudaStream_t st) {
   constexpr int kHd = kPL * 32;
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(p.n_kv));
+  const dim3 grid(static_cast<unsigned>(items * p.n_kv));
   cudaError_t e;
   if (pl.mma) {
     using Cfg = PromptCfg<kHd>;
@@ -439,7 +479,7 @@ cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, cons
       if (s == t.n) break;
       const int64_t nq = cu_q[s0 + s + 1] - cu_q[s0 + s], nk = cu_k[s0 + s + 1] - cu_k[s0 + s];
       if (nq == 0) continue;
-      items += ceil_div(nq, pl.tok) * std::max<int64_t>(1, ceil_div(nk, pl.chunk));
+      items += seq_items(nq, nk, pl.tok, pl.chunk);
       ktiles += ceil_div(nk, kTileKeys);
     }
     if (items == 0) continue;
