@@ -110,6 +110,8 @@ class QwsError(RuntimeError):
 def lib():
     """The loaded library.  Raises if libqws.so has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -121,7 +123,7 @@ def lib():
                 fn = getattr(h, name)
                 fn.restype = res
                 fn.argtypes = args
-            _lib = h
+            _lib = h                     # complete: read without the lock
         return _lib
 
 

@@ -29,8 +29,10 @@ __all__ = [
 
 
 def stream_handle(stream: torch.cuda.Stream | None = None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle itself: building a Stream object around it takes 3 us
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
@@ -220,31 +222,34 @@ def kv_attention(q, k_cache, v_cache, n_q_heads: int, n_kv_heads: int, head_dim:
 
 
 # ------------------------------------------------------------ prompts and batches
-def _here(t: torch.Tensor, name: str) -> None:
+def _here(t: torch.Tensor, name: str, dev: int) -> None:
     """Refuses a tensor of another device than the one the call launches on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _heads(t: torch.Tensor, name: str, heads: int | None = None, head_dim: int | None = None):
+def _heads(t: torch.Tensor, name: str, dev: int, heads: int | None = None,
+           head_dim: int | None = None):
     """qws_heads of a [tokens, heads, head_dim] f32 view; its last dimension is dense."""
-    _here(t, name)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _here(t, name, dev)
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if t.dim() != 3 or (heads is not None and (t.shape[1] != heads or t.shape[2] != head_dim)):
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and (shape[1] != heads or shape[2] != head_dim)):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {head_dim or 'head_dim'}], "
-                         f"got {tuple(t.shape)}")
+                         f"got {tuple(shape)}")
     a, b, c = t.stride()
     if c != 1:
         raise ValueError(f"{name}: the values of a head must be contiguous")
-    return _lib.QwsHeads(t.data_ptr(), a if t.shape[0] > 1 else 0, b if t.shape[1] > 1 else 0)
+    return _lib.QwsHeads(t.data_ptr(), a if shape[0] > 1 else 0, b if shape[1] > 1 else 0)
 
 
-def _vec(t, name: str, dtype: torch.dtype, n: int) -> int:
-    _here(t, name)
+def _vec(t, name: str, dev: int, dtype: torch.dtype, n: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _here(t, name, dev)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
@@ -262,22 +267,22 @@ def _host_ints(v, name: str):
     return (C.c_int64 * len(v))(*v)
 
 
-def _workspace(need: int, workspace, like: torch.Tensor, stream):
+def _workspace(need: int, workspace, dev: int, stream):
     """(tensor, bytes) of the caller's workspace, or of a fresh one kept for the stream."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         if stream is not None:
             workspace.record_stream(stream)
     else:
-        _here(workspace, "workspace")
+        _here(workspace, "workspace", dev)
         _dev(workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _new(shape, like: torch.Tensor, stream) -> torch.Tensor:
-    t = torch.empty(shape, dtype=torch.float32, device=like.device)
+def _new(shape, dev: int, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=torch.float32, device=dev)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -287,18 +292,19 @@ def embed_tokens(fmt: int, W, tokens, vocab: int, hidden: int, scale: float = 1.
                  stream=None):
     """out [n, hidden] = scale * rows `tokens` (int64, [n]) of the quantised table W (uint8,
     vocab rows).  A token outside the table gives zeros and sets device_error() bit 512."""
-    _here(W, "W")
+    dev = torch.cuda.current_device()
+    _here(W, "W", dev)
     n = tokens.numel()
     block, size = {Q4_0: (32, 18), Q8_0: (32, 34), Q4_K: (256, 144), Q6_K: (256, 210)}.get(
         fmt, (1, 0))
     if W.numel() < vocab * (hidden // block) * size:
         raise ValueError(f"W has {W.numel()} bytes, {vocab} rows of {hidden} need "
                          f"{vocab * (hidden // block) * size}")
-    out = _new((n, hidden), W, stream) if out is None else out
+    out = _new((n, hidden), dev, stream) if out is None else out
     check(lib().qws_embed_tokens(fmt, _dev(W, "W", torch.uint8),
-                                 _vec(tokens, "tokens", torch.int64, n),
-                                 _vec(out, "out", torch.float32, n * hidden), vocab, hidden, n,
-                                 float(scale), stream_handle(stream)) if n else 0)
+                                 _vec(tokens, "tokens", dev, torch.int64, n),
+                                 _vec(out, "out", dev, torch.float32, n * hidden), vocab, hidden,
+                                 n, scale, stream_handle(stream)) if n else 0)
     return out
 
 
@@ -307,23 +313,24 @@ def qk_norm_rope(q, k, positions, rot_dim: int, base: float, w_q=None, w_k=None,
     """RMS norm of every head of q [T, n_q, hd] and k [T, n_kv, hd] (w_q, w_k [hd]; None: no
     norm) and its rotation at positions [T] (int64).  Strided views welcome; q_out / k_out may
     be q / k themselves, or for k a view of a cache.  Returns (q_out, k_out)."""
-    qh, kh = _heads(q, "q"), _heads(k, "k")
+    dev = torch.cuda.current_device()
+    qh, kh = _heads(q, "q", dev), _heads(k, "k", dev)
     n, n_q, hd = q.shape
     n_kv = k.shape[1]
     if k.shape[0] != n or k.shape[2] != hd:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not match")
-    q_out = _new(q.shape, q, stream) if q_out is None else q_out
-    k_out = _new(k.shape, k, stream) if k_out is None else k_out
-    qo, ko = _heads(q_out, "q_out", n_q, hd), _heads(k_out, "k_out", n_kv, hd)
+    q_out = _new((n, n_q, hd), dev, stream) if q_out is None else q_out
+    k_out = _new((n, n_kv, hd), dev, stream) if k_out is None else k_out
+    qo, ko = _heads(q_out, "q_out", dev, n_q, hd), _heads(k_out, "k_out", dev, n_kv, hd)
     if q_out.shape[0] != n or k_out.shape[0] != n:
         raise ValueError(f"q_out and k_out must have {n} tokens")
     if n:
         check(lib().qws_qk_norm_rope(
             C.byref(qh), C.byref(kh), C.byref(qo), C.byref(ko),
-            None if w_q is None else _vec(w_q, "w_q", torch.float32, hd),
-            None if w_k is None else _vec(w_k, "w_k", torch.float32, hd),
-            _vec(positions, "positions", torch.int64, n), n, n_q, n_kv, hd, rot_dim, float(base),
-            float(eps), stream_handle(stream)))
+            None if w_q is None else _vec(w_q, "w_q", dev, torch.float32, hd),
+            None if w_k is None else _vec(w_k, "w_k", dev, torch.float32, hd),
+            _vec(positions, "positions", dev, torch.int64, n), n, n_q, n_kv, hd, rot_dim, base,
+            eps, stream_handle(stream)))
     return q_out, k_out
 
 
@@ -333,10 +340,11 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu
     at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (host integers) of q, and of k and v, or at
     cu_seqlens_k there; its last query sees all of its keys.  Rows of out behind the last
     sequence are left as they were."""
-    qh = _heads(q, "q")
-    n_q, hd = q.shape[1], q.shape[2]
+    dev = torch.cuda.current_device()
+    qh = _heads(q, "q", dev)
+    _, n_q, hd = q.shape
     n_kv = k.shape[1]
-    kh, vh = _heads(k, "k", n_kv, hd), _heads(v, "v", n_kv, hd)
+    kh, vh = _heads(k, "k", dev, n_kv, hd), _heads(v, "v", dev, n_kv, hd)
     cu = _host_ints(cu_seqlens, "cu_seqlens")
     ck = cu if cu_seqlens_k is None else _host_ints(cu_seqlens_k, "cu_seqlens_k")
     n = len(cu) - 1
@@ -344,19 +352,18 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu
         raise ValueError("cu_seqlens (and cu_seqlens_k) hold one offset more than sequences")
     if max(cu) > q.shape[0] or max(ck) > min(k.shape[0], v.shape[0]):
         raise ValueError("the offsets pass the end of q, k or v")
-    out = _new(q.shape, q, stream) if out is None else out
-    oh = _heads(out, "out", n_q, hd)
+    out = _new(q.shape, dev, stream) if out is None else out
+    oh = _heads(out, "out", dev, n_q, hd)
     if max(cu) > out.shape[0]:
         raise ValueError("the offsets pass the end of out")
     if cu[0] == cu[n]:
         return out
     L = lib()
     ws, nbytes = _workspace(
-        L.qws_prompt_attention_workspace_bytes(cu, ck, n, n_q, n_kv, hd), workspace, q, stream)
+        L.qws_prompt_attention_workspace_bytes(cu, ck, n, n_q, n_kv, hd), workspace, dev, stream)
     check(L.qws_prompt_attention(
         C.byref(qh), C.byref(kh), C.byref(vh), C.byref(oh), cu, ck, n, n_q, n_kv, hd,
-        float(scale), float(softcap), None if ws is None else ws.data_ptr(), nbytes,
-        stream_handle(stream)))
+        scale, softcap, None if ws is None else ws.data_ptr(), nbytes, stream_handle(stream)))
     return out
 
 
@@ -365,34 +372,37 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
     """One decode step of a batch, q [B, n_q, hd]: row b attends to positions 0 .. n_prefix - 1
     of the shared caches [n_kv, max_prefix, hd] and then to 0 .. n_ctx[b] - 1 (host integers)
     of its own, k_caches and v_caches [B, n_kv, max_seq, hd]."""
-    qh = _heads(q, "q")
+    dev = torch.cuda.current_device()
+    qh = _heads(q, "q", dev)
     B, n_q, hd = q.shape
     n_kv = k_prefix.shape[0]
     for t, name, dims in ((k_prefix, "k_prefix", 3), (v_prefix, "v_prefix", 3),
                           (k_caches, "k_caches", 4), (v_caches, "v_caches", 4)):
-        _here(t, name)
-        if t.dim() != dims or t.shape[-1] != hd or t.shape[-3] != n_kv:
-            raise ValueError(f"{name} {tuple(t.shape)} does not match {n_kv} heads of {hd}")
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+            _here(t, name, dev)
+        shape = t.shape
+        if len(shape) != dims or shape[-1] != hd or shape[-3] != n_kv:
+            raise ValueError(f"{name} {tuple(shape)} does not match {n_kv} heads of {hd}")
     if v_prefix.shape != k_prefix.shape or v_caches.shape != k_caches.shape:
         raise ValueError("key and value caches must have the same shape")
     lens = _host_ints(n_ctx, "n_ctx")
     if len(lens) != B or k_caches.shape[0] != B:
         raise ValueError(f"q has {B} rows, n_ctx {len(lens)}, the caches {k_caches.shape[0]}")
-    out = _new(q.shape, q, stream) if out is None else out
-    oh = _heads(out, "out", n_q, hd)
+    out = _new(q.shape, dev, stream) if out is None else out
+    oh = _heads(out, "out", dev, n_q, hd)
     if out.shape[0] != B:
         raise ValueError(f"out must have {B} rows")
     if B == 0:
         return out
     L = lib()
     ws, nbytes = _workspace(
-        L.qws_prefix_attention_workspace_bytes(n_prefix, lens, B, n_q, n_kv, hd), workspace, q,
+        L.qws_prefix_attention_workspace_bytes(n_prefix, lens, B, n_q, n_kv, hd), workspace, dev,
         stream)
     check(L.qws_prefix_attention(
         C.byref(qh), _dev(k_prefix, "k_prefix", torch.float32),
         _dev(v_prefix, "v_prefix", torch.float32), k_prefix.shape[1], n_prefix,
         _dev(k_caches, "k_caches", torch.float32), _dev(v_caches, "v_caches", torch.float32),
-        k_caches.shape[2], lens, C.byref(oh), B, n_q, n_kv, hd, float(scale), float(softcap),
+        k_caches.shape[2], lens, C.byref(oh), B, n_q, n_kv, hd, scale, softcap,
         None if ws is None else ws.data_ptr(), nbytes, stream_handle(stream)))
     return out
 
