@@ -53,6 +53,7 @@ enum : unsigned {
 
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
+__device__ constexpr float kTanh[8] = {1.0f, -0.333332777f, 0.133321598f, -0.0538709126f, 0.0214648172f, -0.00791743957f, 0.00228222599f, -0.000353344454f};
 constexpr int kPShift = 14;            // weights are 2^14 exp2(s - max)
 
 // what a key tile carries beside its values
@@ -82,6 +83,8 @@ struct MmaCfg {
   static constexpr uint32_t kRing = 2 * kStages * kUnit;
   // softmax warps, then the helpers
   static constexpr int kRowsWarps = 4 * kSplit;
+  static constexpr uint32_t kScratch = kRowsWarps * 32 * 36 * 4;   // in the V ring
+  static_assert(kScratch <= kStages * kUnit, "the V ring holds the scratch");
   static constexpr int kLoadK = kRowsWarps, kLoadV = kRowsWarps + 1;
   static constexpr int kMmaQk = kRowsWarps + 2, kMmaPv = kRowsWarps + 3;
   static constexpr int kThreads = 32 * (kRowsWarps + 4);
@@ -146,6 +149,38 @@ __device__ __forceinline__ void scale_add2(float& d0, float& d1, float a, float 
       "mov.b64 {%0, %1}, rd;\n\t}"
       : "+f"(d0), "+f"(d1)
       : "f"(a), "f"(b0), "f"(b1));
+}
+
+// out = scale * tanh(y) in place, for a thread's scores of a tile.  |y| <= 1 (scores
+// within the cap): y P(y^2), P fitted to tanh(y) / y on [0, 1] in y^2 with a relative
+// error below 5e-9, so 1e-7 with the roundings; beyond, 1 - 2 / (1 + e^2|y|), which is 1.2e-7
+// absolute on values above 0.76.  The library's tanhf costs some 60 instructions a score
+// here, four times the rest of the softmax; this 12.
+__device__ __forceinline__ float tanh_small(float y) {
+  const float z = y * y;
+  float p = kTanh[7];
+#pragma unroll
+  for (int i = 6; i >= 0; --i) p = fmaf(p, z, kTanh[i]);
+  return y * p;
+}
+template <int kN>
+__device__ __forceinline__ void tanh_scaled(float (&y)[kN], float scale) {
+  float a = fabsf(y[0]);
+#pragma unroll
+  for (int i = 1; i < kN; ++i) a = fmaxf(a, fabsf(y[i]));
+  if (!__any_sync(0xFFFFFFFFu, a > 1.f)) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) y[i] = tanh_small(y[i]) * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const float b = fabsf(y[i]);
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(b * (2.f * kLog2e))));
+      const float big = copysignf(1.f - 2.f * r, y[i]);
+      y[i] = (b > 1.f ? big : tanh_small(y[i])) * scale;
+    }
+  }
 }
 
 // e with a 2^e in [2^14, 2^15) for a finite a >= 0 (0 for zero), within +-126 (a
@@ -322,11 +357,12 @@ struct RowState {
   bool any_left_out;
 };
 
-// q: the row's head_dim values, or null (a row of zeros); vis: it sees the keys
+// scratch: kScratch bytes that nothing else uses until q_ready, and again from the last
+// O_tile on; q: the row's head_dim values, or null (a row of zeros); vis: it sees the keys
 // below vis (relative to the first key of tile 0 of the run); all_vis: a bound
 // below which every row of the CTA sees every key.
 template <class Cfg, bool kCap>
-__device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int n, int vis, int all_vis, float scale, float cap,
+__device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, float* scratch, const float* q, int n, int vis, int all_vis, float scale, float cap,
                                          RowState<Cfg>& st, bool& dead) {
   constexpr int kKeys = Cfg::kKeys, kSplit = Cfg::kSplit;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -339,19 +375,46 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
   st.l = 0.f;
   st.any_left_out = false;
   float qscale;
-  // ---- Q: this thread's part of the row, scaled and split into tensor memory
+  // ---- Q: this thread's part of the row, scaled and split into tensor memory.  A lane
+  // of its own row would touch 32 lines a load: a warp reads its 32 rows in runs of
+  // kQRun columns, several lanes a row, and turns them through its scratch
   {
     constexpr int kQC = Cfg::kHd / kSplit;
+    constexpr int kQRun = kQC < 32 ? kQC : 32, kLanes = kQRun / 4, kAt = 32 / kLanes;
+    constexpr int kLoads = 32 / kAt, kRuns = kQC / kQRun, kPitch = kQRun + 4;
+    float* mine = scratch + warp * 32 * kPitch;
+    float4 v[kRuns][kLoads];
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const float* src = reinterpret_cast<const float*>(__shfl_sync(
+          0xFFFFFFFFu, reinterpret_cast<unsigned long long>(q), k * kAt + lane / kLanes));
+#pragma unroll
+      for (int r = 0; r < kRuns; ++r) {
+        v[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src)
+          v[r][k] = *reinterpret_cast<const float4*>(src + part * kQC + r * kQRun +
+                                                     (lane % kLanes) * 4);
+      }
+    }
     float x[kQC];
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQC; i += 4) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (q) v = *reinterpret_cast<const float4*>(q + part * kQC + i);
-      x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    for (int r = 0; r < kRuns; ++r) {
+      __syncwarp();
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (finite_bits(x[i + c])) a = fmaxf(a, fabsf(x[i + c]));
+      for (int k = 0; k < kLoads; ++k)
+        *reinterpret_cast<float4*>(mine + (k * kAt + lane / kLanes) * kPitch + (lane % kLanes) * 4) =
+            v[r][k];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kQRun; i += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(mine + lane * kPitch + i);
+        float* o = x + r * kQRun + i;
+        o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
+      }
     }
     sh.xmax[1][part][row] = a;
     row_sync();
@@ -377,6 +440,7 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
       }
     }
     tc_wait_st();
+    fence_proxy_async_smem();      // the scratch is overwritten by copies next
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.q_ready);
@@ -385,7 +449,7 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
   for (int c = 0; c < Cfg::kNC; ++c)
 #pragma unroll
     for (int i = 0; i < Cfg::kOC; ++i) st.o[c][i] = 0.f;
-  const float rowf = qscale * scale * (kCap ? 1.f : kLog2e);
+  const float rowf = kCap ? qscale * (scale / cap) : qscale * scale * kLog2e;
   const uint32_t t_o = lanes + kTmO + static_cast<uint32_t>(part * Cfg::kOC);
   float alpha = 1.f, vs = 1.f, alpha_next = 1.f;
   uint32_t hi[kKeys / 2], lo[kKeys / 2];
@@ -422,10 +486,7 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, const float* q, int
         x[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * (f.w * rowf);
       }
     }
-    if constexpr (kCap) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) x[i] = cap * tanhf(x[i] / cap) * kLog2e;
-    }
+    if constexpr (kCap) tanh_scaled<kKeys>(x, cap * kLog2e);
     if ((j + 1) * kTileKeys > all_vis) {
       const int left = vis - j * kTileKeys - kKeys * part;    // of this thread's keys, how many
 #pragma unroll
@@ -539,16 +600,33 @@ __device__ __forceinline__ void add_left_out(RowState<Cfg>& st, const float* q, 
       st.o[c][i] = fmaf(p, v[c * Cfg::kHC + part * Cfg::kOC + i], st.o[c][i]);
 }
 
-// this thread's columns of a row: f * o
+// f * o into the rows at dst (null: not stored), turned through the warp's scratch so
+// that a store covers whole lines
 template <class Cfg>
-__device__ __forceinline__ void store_columns(const RowState<Cfg>& st, float* dst, int part,
-                                              float f) {
+__device__ __forceinline__ void store_rows(const RowState<Cfg>& st, float* scratch, float* dst,
+                                           float f) {
+  constexpr int kLanes = Cfg::kOC / 4, kAt = 32 / kLanes, kPitch = Cfg::kOC + 4;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int part = warp >> 2;
+  float* mine = scratch + warp * 32 * kPitch;
 #pragma unroll
-  for (int c = 0; c < Cfg::kNC; ++c)
+  for (int c = 0; c < Cfg::kNC; ++c) {
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < Cfg::kOC; i += 4)
-      *reinterpret_cast<float4*>(dst + c * Cfg::kHC + part * Cfg::kOC + i) =
+      *reinterpret_cast<float4*>(mine + lane * kPitch + i) =
           make_float4(st.o[c][i] * f, st.o[c][i + 1] * f, st.o[c][i + 2] * f, st.o[c][i + 3] * f);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 32 / kAt; ++k) {
+      const int r = k * kAt + lane / kLanes, i = (lane % kLanes) * 4;
+      float* to = reinterpret_cast<float*>(
+          __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(dst), r));
+      if (to)
+        *reinterpret_cast<float4*>(to + c * Cfg::kHC + part * Cfg::kOC + i) =
+            *reinterpret_cast<const float4*>(mine + r * kPitch + i);
+    }
+  }
 }
 
 // ------------------------------------------------------------ key tiles

@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(kRowThreads)
 // scaled value is not in [2^-3, 65504] would overflow or lose bits; it is left out of
 // the tile and added at the end in f32.
 template <int kHd>
-struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : 2)> {
-  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : 2)>;
-  static constexpr int kDepth = kHd > 128 ? 1 : 2;          // tiles of a ring
+struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)> {
+  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)>;
+  static constexpr int kDepth = kHd > 128 ? 1 : kHd > 64 ? 2 : 4;   // tiles of a ring
   static constexpr int kConvWarps = 4;
   static constexpr int kConv = Base::kRowsWarps + 4;        // first converter warp
   static constexpr int kThreads = 32 * (kConv + kConvWarps);
@@ -187,6 +187,8 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     const int stage = (j % Cfg::kDepth) * kNC;
     uint64_t* empty = is_v ? sh.mma.v_empty : sh.mma.k_empty;
     wait(is_v ? &sh.mma.vmeta_free[slot] : &sh.mma.meta_free[slot], free_par);
+    // the V ring is the softmax warps' scratch until Q is stored
+    if (jh == 1) wait(&sh.mma.q_ready, 0);
     // the last chunk of the tile that was there: commits come in order
     wait(&empty[stage + kNC - 1], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
     uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
@@ -324,7 +326,8 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
                      (g * p.group + rc % p.group) * p.q.head_stride;
     RowState<Cfg> st;
     bool dead;
-    mma_rows<Cfg, kCap>(sh.mma, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
+    float* scratch = reinterpret_cast<float*>(v_ring);
+    mma_rows<Cfg, kCap>(sh.mma, scratch, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttRows);
     if (st.any_left_out && alive) {
       for (int t = 0; t < keys; ++t)
@@ -332,15 +335,12 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
           add_left_out<Cfg>(st, q, p.kp + at + static_cast<int64_t>(t) * kHd,
                             p.vp + at + static_cast<int64_t>(t) * kHd, part, p.scale, p.cap);
     }
-    if (alive && !dead) {
-      constexpr float kUnshift = 1.0f / (1 << kPShift);
-      float* dst = p.part + prefix_part<kHd / 32>(p, piece, g, r);
-      store_columns<Cfg>(st, dst, part, kUnshift);
-      if (part == 0) {
-        dst[kHd] = st.m;
-        dst[kHd + 1] = st.l * kUnshift;
-      }
-    }
+    constexpr float kUnshift = 1.0f / (1 << kPShift);
+    const bool store = alive && !dead;
+    float* dst = p.part + prefix_part<kHd / 32>(p, piece, g, rc);
+    store_rows<Cfg>(st, scratch, store ? dst : nullptr, kUnshift);
+    if (store && part == 0)
+      *reinterpret_cast<float2*>(dst + kHd) = make_float2(st.m, st.l * kUnshift);
   }
   // every MMA has completed before tensor memory is freed
   tc_fence_before();

@@ -253,6 +253,8 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
       mma_load<Cfg>(
           sh.v_full, sh.v_empty, n,
           [&](int j) {
+            // the ring is the softmax warps' scratch until Q is stored
+            if (j == 0 && !mbar_wait(&sh.q_ready, 0)) return false;
             const int s = j & 1;
             if (!mbar_wait(&sh.vmeta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
             mbar_arrive_expect_tx(&sh.vmeta_full[s], 16);
@@ -281,7 +283,8 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
     const int vis = visible(i, it.n_q, it.n_k) - ka;
     RowState<Cfg> st;
     bool dead;
-    mma_rows<Cfg, kCap>(sh, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
+    float* scratch = reinterpret_cast<float*>(v_ring);
+    mma_rows<Cfg, kCap>(sh, scratch, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
                   p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
     if (st.any_left_out && alive) {
@@ -296,19 +299,16 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
         }
       }
     }
-    if (alive && !dead) {
-      constexpr float kUnshift = 1.0f / (1 << kPShift);
-      if (it.pieces > 1) {
-        float* dst = part_rows(p, item, g, kHd) + row * (kHd + kPartPad);
-        store_columns<Cfg>(st, dst, part, kUnshift);
-        if (part == 0) {
-          dst[kHd] = st.m;
-          dst[kHd + 1] = st.l * kUnshift;
-        }
-      } else {
-        store_columns<Cfg>(st, p.out.data + token * p.out.token_stride + h * p.out.head_stride,
-                           part, st.l == 0.f ? 0.f : 1.0f / st.l);
-      }
+    constexpr float kUnshift = 1.0f / (1 << kPShift);
+    const bool store = alive && !dead;
+    if (it.pieces > 1) {
+      float* dst = part_rows(p, item, g, kHd) + row * (kHd + kPartPad);
+      store_rows<Cfg>(st, scratch, store ? dst : nullptr, kUnshift);
+      if (store && part == 0)
+        *reinterpret_cast<float2*>(dst + kHd) = make_float2(st.m, st.l * kUnshift);
+    } else {
+      float* dst = p.out.data + token * p.out.token_stride + h * p.out.head_stride;
+      store_rows<Cfg>(st, scratch, store ? dst : nullptr, st.l == 0.f ? 0.f : 1.0f / st.l);
     }
   }
   // every MMA has completed before tensor memory is freed
