@@ -360,8 +360,11 @@ struct RowState {
 // scratch: kScratch bytes that nothing else uses until q_ready, and again from the last
 // O_tile on; q: the row's head_dim values, or null (a row of zeros); vis: it sees the keys
 // below vis (relative to the first key of tile 0 of the run); all_vis: a bound
-// below which every row of the CTA sees every key.
-template <class Cfg, bool kCap>
+// below which every row of the CTA sees every key.  kAhead: S(j+1) is turned into weights
+// before O_tile(j) is drained, which hides the softmax behind the MMAs; where the key
+// tiles come slower than the MMAs take them it would only hold O_tile(j), and with it
+// the V buffer, until K(j+1) is there.
+template <class Cfg, bool kCap, bool kAhead>
 __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, float* scratch, const float* q, int n, int vis, int all_vis, float scale, float cap,
                                          RowState<Cfg>& st, bool& dead) {
   constexpr int kKeys = Cfg::kKeys, kSplit = Cfg::kSplit;
@@ -532,9 +535,15 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, float* scratch, con
   // one copy of each step: the code of a tile is read anew for every tile, and two
   // copies of it do not stay in the instruction caches
 #pragma unroll 1
-  for (int j = -1; j < n; ++j) {
-    alpha = alpha_next;
-    if (j + 1 < n) weights(j + 1);
+  for (int j = kAhead ? -1 : 0; j < n; ++j) {
+    if constexpr (kAhead) {
+      alpha = alpha_next;
+      if (j + 1 < n) weights(j + 1);
+    } else {
+      weights(j);
+      alpha = alpha_next;
+      store_p(j);
+    }
     if (j >= 0) {
       const uint32_t ph = static_cast<uint32_t>(j) & 1u;
       if (!dead)
@@ -568,7 +577,8 @@ __device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, float* scratch, con
       }
     }
     }
-    if (j + 1 < n) store_p(j + 1);      // P(j) has been multiplied by now
+    if constexpr (kAhead)
+      if (j + 1 < n) store_p(j + 1);    // P(j) has been multiplied by now
   }
   // the row's whole sum
   row_sync();

@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
     RowState<Cfg> st;
     bool dead;
     float* scratch = reinterpret_cast<float*>(v_ring);
-    mma_rows<Cfg, kCap>(sh.mma, scratch, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
+    mma_rows<Cfg, kCap, false>(sh.mma, scratch, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttRows);
     if (st.any_left_out && alive) {
       for (int t = 0; t < keys; ++t)

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
     RowState<Cfg> st;
     bool dead;
     float* scratch = reinterpret_cast<float*>(v_ring);
-    mma_rows<Cfg, kCap>(sh, scratch, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
+    mma_rows<Cfg, kCap, true>(sh, scratch, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
                   p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
     if (st.any_left_out && alive) {
