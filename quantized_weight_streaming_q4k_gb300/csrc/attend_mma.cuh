@@ -640,41 +640,48 @@ __device__ __forceinline__ void store_rows(const RowState<Cfg>& st, float* scrat
 }
 
 // ------------------------------------------------------------ key tiles
-// One key row (a lane's kPL = head_dim / 32 columns of it, times sc) as hi and lo f16
-// into row r of the units at dst.
+// One key row (a lane's kPL = head_dim / 32 columns of it, times sc) as hi and lo f16 at
+// the lane's place in the units: `at` for its first columns, a unit further for the
+// group of columns 128 on (two units).
+template <class Cfg>
+__device__ __forceinline__ void store_split_at(const float (&x)[Cfg::kHd / 32], float sc, int lane,
+                                               uint8_t* at) {
+  constexpr int kPL = Cfg::kHd / 32;
+  if constexpr (kPL >= 4) {
+#pragma unroll
+    for (int i = 0; i < kPL; i += 4) {
+      float a, b, c, d;
+      mul2(a, b, x[i], x[i + 1], sc, sc);
+      mul2(c, d, x[i + 2], x[i + 3], sc, sc);
+      uint2 hi, lo;
+      split_f16x2(a, b, hi.x, lo.x);
+      split_f16x2(c, d, hi.y, lo.y);
+      uint8_t* u = at + (i / 4) * 2 * Cfg::kUnit;
+      *reinterpret_cast<uint2*>(u) = hi;
+      *reinterpret_cast<uint2*>(u + Cfg::kPart) = lo;
+    }
+  } else {
+    float a = x[0] * sc, b;
+    if constexpr (kPL == 2) b = x[1] * sc;
+    else b = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
+    uint32_t hi, lo;
+    split_f16x2(a, b, hi, lo);
+    if (kPL == 2 || !(lane & 1)) {
+      *reinterpret_cast<uint32_t*>(at) = hi;
+      *reinterpret_cast<uint32_t*>(at + Cfg::kPart) = lo;
+    }
+  }
+}
+
+// the same into row r of the units at dst
 template <class Cfg>
 __device__ __forceinline__ void store_split_row(const float (&x)[Cfg::kHd / 32], float sc, int r,
                                                 int lane, uint8_t* dst) {
-  constexpr int kPL = Cfg::kHd / 32;
-  if constexpr (kPL >= 2) {
-#pragma unroll
-    for (int i = 0; i < kPL; i += (kPL >= 4 ? 4 : 2)) {
-      const int c = lane_col<kPL>(lane, i);
-      uint8_t* u = dst + (c / 64) * Cfg::kUnit +
-                   sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(c % 64) / 8u) + (c % 8) * 2;
-      uint32_t h0, l0;
-      split_f16x2(x[i] * sc, x[i + 1] * sc, h0, l0);
-      if constexpr (kPL >= 4) {
-        uint32_t h1, l1;
-        split_f16x2(x[i + 2] * sc, x[i + 3] * sc, h1, l1);
-        *reinterpret_cast<uint2*>(u) = make_uint2(h0, h1);
-        *reinterpret_cast<uint2*>(u + Cfg::kPart) = make_uint2(l0, l1);
-      } else {
-        *reinterpret_cast<uint32_t*>(u) = h0;
-        *reinterpret_cast<uint32_t*>(u + Cfg::kPart) = l0;
-      }
-    }
-  } else {
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, x[0], 1);
-    if (!(lane & 1)) {
-      uint32_t h0, l0;
-      split_f16x2(x[0] * sc, other * sc, h0, l0);
-      uint8_t* u = dst + sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(lane) / 8u) +
-                   (lane % 8) * 2;
-      *reinterpret_cast<uint32_t*>(u) = h0;
-      *reinterpret_cast<uint32_t*>(u + Cfg::kPart) = l0;
-    }
-  }
+  const int c = lane_col<Cfg::kHd / 32>(lane, 0);
+  store_split_at<Cfg>(x, sc, lane,
+                      dst + (c / 64) * Cfg::kUnit +
+                          sw128_off(static_cast<uint32_t>(r), static_cast<uint32_t>(c % 64) / 8u) +
+                          (c % 8) * 2);
 }
 
 // largest finite magnitude of a row over the warp; `all`: every value is finite.  The

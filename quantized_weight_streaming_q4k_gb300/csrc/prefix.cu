@@ -98,10 +98,12 @@ __global__ void __launch_bounds__(kRowThreads)
 // and kv head; at head_dim 256 a tile of 64 keys is 128 KB, about 5800 cycles of an
 // SM's share of the memory, against 3072 cycles of MMAs).
 //
-// The values of a tile have one scale, taken from its first run of rows before the
-// others are there: that run's largest value at [2^12, 2^13).  A row whose largest
-// scaled value is not in [2^-3, 65504] would overflow or lose bits; it is left out of
-// the tile and added at the end in f32.
+// The converters bound it next (with a maximum over every row and a scale of its own
+// they took 12200 cycles a tile).  So a piece has one scale for its keys and one for its
+// values, taken from its first run of rows: that run's largest value at [2^12, 2^13).
+// Rows whose largest scaled value is in [2^-3, 65504] keep their 22 bits with it, which
+// two votes check; the others are rare: such a key gets a scale of its own, such a
+// value row is left out of the tile and added at the end in f32.
 template <int kHd>
 struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)> {
   using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)>;
@@ -121,7 +123,7 @@ template <int kHd>
 struct PrefixShared {
   uint64_t stg_full[PrefixCfg<kHd>::kStaging], stg_empty[PrefixCfg<kHd>::kStaging];
   uint32_t left_out[kMaxPieceTiles][2];
-  float vmax[4];
+  float vmax[2][4];
   MmaShared<PrefixCfg<kHd>> mma;
 };
 
@@ -170,15 +172,23 @@ template <int kHd>
 __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint8_t* staging,
                                                uint8_t* k_ring, uint8_t* v_ring, int keys, int n) {
   using Cfg = PrefixCfg<kHd>;
-  constexpr int kPL = kHd / 32, kNC = Cfg::kNC;
+  constexpr int kPL = kHd / 32, kNC = Cfg::kNC, kRows = Cfg::kRunRows;
+  static_assert(Cfg::kConvWarps == 4 && Cfg::kRun % 8 == 0, "the rows' places below");
   const int lane = static_cast<int>(threadIdx.x & 31);
   const int cw = static_cast<int>(threadIdx.x >> 5) - Cfg::kConv;
+  // A warp's row i of a run is row cw + 4 i: in the swizzled units rows 8 apart are 1024
+  // bytes apart, and row cw + 4 follows another pattern than row cw.
+  const uint32_t col = static_cast<uint32_t>(lane_col<kPL>(lane, 0));
+  const uint32_t in_unit = (col / 64) * Cfg::kUnit + (col % 8) * 2;
+  const uint32_t even = in_unit + sw128_off(static_cast<uint32_t>(cw), col % 64 / 8);
+  const uint32_t odd = in_unit + sw128_off(static_cast<uint32_t>(cw) + 4u, col % 64 / 8);
   RingAt<Cfg::kStaging> at;
   bool dead = false;           // a wait gave up: no more waits, the barriers go on
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
   };
   bool seen = false;           // the next run of rows was seen to be there
+  float k_scale = 1.f, v_scale = 1.f;           // powers of two
 #pragma unroll 1
   for (int jh = 0; jh < 2 * n; ++jh) {
     const int j = jh >> 1, slot = j & 1;
@@ -193,15 +203,15 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     wait(&empty[stage + kNC - 1], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
     uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
     TileMeta& meta = sh.mma.meta[slot];
-    float vsc = 1.f;
+    uint32_t out_lo = 0, out_hi = 0;              // rows of the tile this warp leaves out
 #pragma unroll 1
     for (int r = 0; r < Cfg::kRuns; ++r) {
       const int rows = min(Cfg::kRun, keys - j * kTileKeys - r * Cfg::kRun);
-      float x[Cfg::kRunRows][kPL];
+      float x[kRows][kPL], m[kRows];
       if (rows > 0 && !__all_sync(0xFFFFFFFFu, seen)) wait(&sh.stg_full[at.stage], at.phase);
 #pragma unroll
-      for (int i = 0; i < Cfg::kRunRows; ++i) {
-        const int row = cw + Cfg::kConvWarps * i;
+      for (int i = 0; i < kRows; ++i) {
+        const int row = cw + 4 * i;
 #pragma unroll
         for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
         if (row < rows)
@@ -209,60 +219,76 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
                             row * kHd,
                         lane, x[i]);
       }
-      float am[Cfg::kRunRows];
-      uint32_t fin = 0;
 #pragma unroll
-      for (int i = 0; i < Cfg::kRunRows; ++i) {
-        bool f;
-        am[i] = row_amax<kPL>(x[i], f);
-        fin |= static_cast<uint32_t>(f) << i;
+      for (int i = 0; i < kRows; ++i) {
+        m[i] = fabsf(x[i][0]);
+#pragma unroll
+        for (int c = 1; c < kPL; ++c) m[i] = fmaxf(m[i], fabsf(x[i][c]));
       }
+      if (j == 0 && r == 0) {
+        // the piece's scale
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (m[i] <= 3.4028235e38f) a = fmaxf(a, m[i]);
+        a = warp_max(a);
+        if (lane == 0) sh.vmax[is_v][cw] = a;
+        bar_sync(5, 32 * Cfg::kConvWarps);
+#pragma unroll
+        for (int w = 0; w < Cfg::kConvWarps; ++w) a = fmaxf(a, sh.vmax[is_v][w]);
+        const int e = a > 0.f ? max(split_exp(a) - 2, -126) : 0;
+        (is_v ? v_scale : k_scale) = exp2i(e);
+      }
+      const float sc = is_v ? v_scale : k_scale;
+      bool fit = true, over = false;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        fit = __any_sync(0xFFFFFFFFu, m[i] * sc >= 0.125f) && fit;
+        over = over || m[i] * sc > 65504.f;
+      }
+      fit = !__any_sync(0xFFFFFFFFu, over) && fit;
       if (rows > 0) {
         // the stage may be overwritten once every lane HAS its values: loads that nothing
-        // has used yet may be scheduled behind the arrival, so it hangs on the maxima
-        uint32_t had = 0;
-#pragma unroll
-        for (int i = 0; i < Cfg::kRunRows; ++i) had |= __float_as_uint(am[i]);
-        if (lane == 0 && had != 0xFFFFFFFFu) mbar_arrive(&sh.stg_empty[at.stage]);
+        // has used yet may be scheduled behind the arrival, so it follows the votes
+        if (lane == 0) mbar_arrive(&sh.stg_empty[at.stage]);
         at.next();
         seen = mbar_test(&sh.stg_full[at.stage], at.phase);
       }
-      if (is_v && r == 0) {
-        float a = 0.f;
+      float mine = 1.0f / k_scale;        // lane i: 2^-e of key row i
+      float by[kRows];
 #pragma unroll
-        for (int i = 0; i < Cfg::kRunRows; ++i) a = fmaxf(a, (fin >> i) & 1u ? am[i] : 0.f);
-        if (lane == 0) sh.vmax[cw] = a;
-        if (cw == 0 && lane < 2) sh.left_out[j][lane] = 0;
-        bar_sync(5, 32 * Cfg::kConvWarps);
-        a = fmaxf(fmaxf(sh.vmax[0], sh.vmax[1]), fmaxf(sh.vmax[2], sh.vmax[3]));
-        const int e = a > 0.f ? max(split_exp(a) - 2, -126) : 0;
-        vsc = exp2i(e);
-        if (cw == 0 && lane == 0) meta.vscale = exp2i(-e);
-      }
+      for (int i = 0; i < kRows; ++i) by[i] = sc;
+      if (!fit) {
 #pragma unroll
-      for (int i = 0; i < Cfg::kRunRows; ++i) {
-        const int row = r * Cfg::kRun + cw + Cfg::kConvWarps * i;
-        float sc;
-        if (is_v) {
-          sc = vsc;
-          const float top = am[i] * vsc;
-          const bool in = ((fin >> i) & 1u) && (am[i] == 0.f || (top >= 0.125f && top <= 65504.f));
-          if (!in) {
+        for (int i = 0; i < kRows; ++i) {
+          bool fin;
+          const float am = row_amax<kPL>(x[i], fin);
+          const bool in = fin && (am == 0.f || (am * sc >= 0.125f && am * sc <= 65504.f));
+          if (in) continue;
+          if (is_v) {
+            const int row = r * Cfg::kRun + cw + 4 * i;
+            (row < 32 ? out_lo : out_hi) |= 1u << (row & 31);
 #pragma unroll
             for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
-            if (lane == 0) atomicOr(&sh.left_out[j][row >> 5], 1u << (row & 31));
+          } else {
+            const int e = split_exp(am);
+            by[i] = exp2i(e);
+            if (lane == i) mine = exp2i(-e);
           }
-        } else {
-          const int e = split_exp(am[i]);
-          sc = exp2i(e);
-          if (lane == 0) meta.kscale[row] = exp2i(-e);
         }
-        store_split_row<typename Cfg::Base>(x[i], sc, row, lane, dst);
       }
+      if (!is_v && lane < kRows) meta.kscale[r * Cfg::kRun + cw + 4 * lane] = mine;
+      uint8_t* at_rows = dst + r * (Cfg::kRun / 8) * 1024;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        store_split_at<typename Cfg::Base>(x[i], by[i], lane,
+                                           at_rows + (i >> 1) * 1024 + ((i & 1) ? odd : even));
     }
     if (is_v) {
+      if ((out_lo | out_hi) && lane < 2) atomicOr(&sh.left_out[j][lane], lane ? out_hi : out_lo);
       bar_sync(5, 32 * Cfg::kConvWarps);          // every warp's left_out is in
       if (cw == 0 && lane < 2) meta.left_out[lane] = sh.left_out[j][lane];
+      if (cw == 0 && lane == 0) meta.vscale = 1.0f / v_scale;
     }
     fence_proxy_async_smem();                     // generic stores -> visible to the MMAs
     __syncwarp();
@@ -291,6 +317,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int ka = piece * p.chunk, keys = min(p.n_prefix, ka + p.chunk) - ka;
   const int n = (keys + kTileKeys - 1) / kTileKeys;
+  if (threadIdx.x < 2 * kMaxPieceTiles) sh.left_out[threadIdx.x >> 1][threadIdx.x & 1] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStaging; ++s) {
       mbar_init(&sh.stg_full[s], 1);
