@@ -66,9 +66,11 @@ struct __align__(16) TileMeta {
 static_assert(sizeof(TileMeta) == 272, "copied in 16-byte units");
 
 // A unit: 64 keys x 64 columns of K or V, hi then lo.
-template <int kHdT, int kSplitT, int kDepthT = 0>
+// kWholeT: the units of a half tile come and go together, by their first one's barriers.
+template <int kHdT, int kSplitT, int kDepthT = 0, bool kWholeT = false>
 struct MmaCfg {
   static constexpr int kHd = kHdT;
+  static constexpr bool kWhole = kWholeT;
   static constexpr int kSplit = kSplitT;                // threads of a query row
   static constexpr int kNC = kHd > 64 ? kHd / 64 : 1;   // chunks of head_dim
   static constexpr int kHC = kHd / kNC;                 // columns of a chunk
@@ -249,14 +251,15 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
   for (int j = 0; j < n && ok; ++j) {
 #pragma unroll 1
     for (int c = 0; c < Cfg::kNC; ++c) {
-      if (!there) wait(&sh.k_full[at.stage], at.phase);
+      if (!there && !(Cfg::kWhole && c > 0)) wait(&sh.k_full[at.stage], at.phase);
       if (c == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
       tc_fence_after();
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
-      uint64_t* empty = &sh.k_empty[at.stage];
+      uint64_t* empty = &sh.k_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
-      const bool next = mbar_test(&sh.k_full[at.stage], at.phase);
+      const bool next = (!Cfg::kWhole || c == Cfg::kNC - 1) &&
+                        mbar_test(&sh.k_full[at.stage], at.phase);
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
 #pragma unroll
@@ -266,7 +269,7 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
           tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdesc, (c | t | k) != 0 ? 1u : 0u, one);
         }
       }
-      tc_commit(empty, one);
+      if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
       if (c == Cfg::kNC - 1) tc_commit(&sh.s_full, one);
       there = __all_sync(0xFFFFFFFFu, next);
     }
@@ -292,7 +295,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
 #pragma unroll 1
     for (int c = 0; c < Cfg::kNC; ++c) {
       if (!there) {
-        wait(&sh.v_full[at.stage], at.phase);
+        if (!(Cfg::kWhole && c > 0)) wait(&sh.v_full[at.stage], at.phase);
         wait(&sh.o_free[buf.stage], buf.phase ^ 1u);   // the first use of each passes
       }
       if (c == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);   // the last to come
@@ -300,10 +303,12 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
       const uint32_t d = kTmO + static_cast<uint32_t>(buf.stage) * 64u;
-      uint64_t *full = &sh.o_full[buf.stage], *empty = &sh.v_empty[at.stage];
+      uint64_t* full = &sh.o_full[buf.stage];
+      uint64_t* empty = &sh.v_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
       buf.next();
-      const bool next = mbar_test(&sh.v_full[at.stage], at.phase) &
+      const bool next = ((Cfg::kWhole && c < Cfg::kNC - 1) ||
+                         mbar_test(&sh.v_full[at.stage], at.phase)) &
                         mbar_test(&sh.o_free[buf.stage], buf.phase ^ 1u);
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
@@ -315,7 +320,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
         }
       }
       tc_commit(full, one);
-      tc_commit(empty, one);
+      if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
       there = __all_sync(0xFFFFFFFFu, next);
     }
   }

@@ -102,13 +102,13 @@ __global__ void __launch_bounds__(kRowThreads)
 // they took 12200 cycles a tile).  So a piece has one scale for its keys and one for its
 // values, taken from its first run of rows: that run's largest value at [2^12, 2^13).
 // Rows whose largest scaled value is in [2^-3, 65504] keep their 22 bits with it, which
-// two votes check; the others are rare: such a key gets a scale of its own, such a
+// one vote checks; the others are rare: such a key gets a scale of its own, such a
 // value row is left out of the tile and added at the end in f32.
 template <int kHd>
-struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)> {
-  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4)>;
+struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true> {
+  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true>;
   static constexpr int kDepth = kHd > 128 ? 1 : kHd > 64 ? 2 : 4;   // tiles of a ring
-  static constexpr int kConvWarps = 4;
+  static constexpr int kConvWarps = 8;
   static constexpr int kConv = Base::kRowsWarps + 4;        // first converter warp
   static constexpr int kThreads = 32 * (kConv + kConvWarps);
   static constexpr int kRun = kHd >= 64 ? 4096 / kHd : 64;  // rows of a staging stage
@@ -123,12 +123,12 @@ template <int kHd>
 struct PrefixShared {
   uint64_t stg_full[PrefixCfg<kHd>::kStaging], stg_empty[PrefixCfg<kHd>::kStaging];
   uint32_t left_out[kMaxPieceTiles][2];
-  float vmax[2][4];
+  float vmax[2][PrefixCfg<kHd>::kConvWarps];
   MmaShared<PrefixCfg<kHd>> mma;
 };
 
-// 512 threads, 128 registers each at launch; per scheduler 2 softmax warps at 176, a
-// helper at 56 and a converter at 104: 2 x 176 + 56 + 104 = 4 x 128.
+// 640 threads, 96 registers each at launch; per scheduler 2 softmax warps at 160, a
+// helper at 40 and 2 converters at 56: 2 x 160 + 40 + 2 x 56 = 472 of 5 x 96.
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -173,15 +173,14 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
                                                uint8_t* k_ring, uint8_t* v_ring, int keys, int n) {
   using Cfg = PrefixCfg<kHd>;
   constexpr int kPL = kHd / 32, kNC = Cfg::kNC, kRows = Cfg::kRunRows;
-  static_assert(Cfg::kConvWarps == 4 && Cfg::kRun % 8 == 0, "the rows' places below");
+  static_assert(Cfg::kConvWarps == 8 && Cfg::kRun % 8 == 0, "the rows' places below");
   const int lane = static_cast<int>(threadIdx.x & 31);
   const int cw = static_cast<int>(threadIdx.x >> 5) - Cfg::kConv;
-  // A warp's row i of a run is row cw + 4 i: in the swizzled units rows 8 apart are 1024
-  // bytes apart, and row cw + 4 follows another pattern than row cw.
+  // A warp's row i of a run is row cw + 8 i: in the swizzled units rows 8 apart have the
+  // same pattern, 1024 bytes apart.
   const uint32_t col = static_cast<uint32_t>(lane_col<kPL>(lane, 0));
-  const uint32_t in_unit = (col / 64) * Cfg::kUnit + (col % 8) * 2;
-  const uint32_t even = in_unit + sw128_off(static_cast<uint32_t>(cw), col % 64 / 8);
-  const uint32_t odd = in_unit + sw128_off(static_cast<uint32_t>(cw) + 4u, col % 64 / 8);
+  const uint32_t place = (col / 64) * Cfg::kUnit + (col % 8) * 2 +
+                         sw128_off(static_cast<uint32_t>(cw), col % 64 / 8);
   RingAt<Cfg::kStaging> at;
   bool dead = false;           // a wait gave up: no more waits, the barriers go on
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -199,8 +198,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     wait(is_v ? &sh.mma.vmeta_free[slot] : &sh.mma.meta_free[slot], free_par);
     // the V ring is the softmax warps' scratch until Q is stored
     if (jh == 1) wait(&sh.mma.q_ready, 0);
-    // the last chunk of the tile that was there: commits come in order
-    wait(&empty[stage + kNC - 1], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
+    wait(&empty[stage], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
     uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
     TileMeta& meta = sh.mma.meta[slot];
     uint32_t out_lo = 0, out_hi = 0;              // rows of the tile this warp leaves out
@@ -211,7 +209,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
       if (rows > 0 && !__all_sync(0xFFFFFFFFu, seen)) wait(&sh.stg_full[at.stage], at.phase);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const int row = cw + 4 * i;
+        const int row = cw + 8 * i;
 #pragma unroll
         for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
         if (row < rows)
@@ -240,17 +238,18 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
         (is_v ? v_scale : k_scale) = exp2i(e);
       }
       const float sc = is_v ? v_scale : k_scale;
-      bool fit = true, over = false;
+      // bit i: row i has a value of 2^-3 or more; bit 31: some value does not fit
+      uint32_t has = 0;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        fit = __any_sync(0xFFFFFFFFu, m[i] * sc >= 0.125f) && fit;
-        over = over || m[i] * sc > 65504.f;
+        has |= static_cast<uint32_t>(m[i] * sc >= 0.125f) << i;
+        has |= static_cast<uint32_t>(m[i] * sc > 65504.f) << 31;
       }
-      fit = !__any_sync(0xFFFFFFFFu, over) && fit;
+      const bool fit = __reduce_or_sync(0xFFFFFFFFu, has) == (1u << kRows) - 1u;
       if (rows > 0) {
         // the stage may be overwritten once every lane HAS its values: loads that nothing
-        // has used yet may be scheduled behind the arrival, so it follows the votes
-        if (lane == 0) mbar_arrive(&sh.stg_empty[at.stage]);
+        // has used yet may be scheduled behind the arrival, so it hangs on the vote
+        if (lane == 0 && (fit || has != 0xFFFFFFFFu)) mbar_arrive(&sh.stg_empty[at.stage]);
         at.next();
         seen = mbar_test(&sh.stg_full[at.stage], at.phase);
       }
@@ -266,7 +265,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
           const bool in = fin && (am == 0.f || (am * sc >= 0.125f && am * sc <= 65504.f));
           if (in) continue;
           if (is_v) {
-            const int row = r * Cfg::kRun + cw + 4 * i;
+            const int row = r * Cfg::kRun + cw + 8 * i;
             (row < 32 ? out_lo : out_hi) |= 1u << (row & 31);
 #pragma unroll
             for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
@@ -277,12 +276,11 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
           }
         }
       }
-      if (!is_v && lane < kRows) meta.kscale[r * Cfg::kRun + cw + 4 * lane] = mine;
+      if (!is_v && lane < kRows) meta.kscale[r * Cfg::kRun + cw + 8 * lane] = mine;
       uint8_t* at_rows = dst + r * (Cfg::kRun / 8) * 1024;
 #pragma unroll
       for (int i = 0; i < kRows; ++i)
-        store_split_at<typename Cfg::Base>(x[i], by[i], lane,
-                                           at_rows + (i >> 1) * 1024 + ((i & 1) ? odd : even));
+        store_split_at<typename Cfg::Base>(x[i], by[i], lane, at_rows + i * 1024 + place);
     }
     if (is_v) {
       if ((out_lo | out_hi) && lane < 2) atomicOr(&sh.left_out[j][lane], lane ? out_hi : out_lo);
@@ -293,8 +291,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     fence_proxy_async_smem();                     // generic stores -> visible to the MMAs
     __syncwarp();
     if (lane == 0) {
-      uint64_t* full = is_v ? sh.mma.v_full : sh.mma.k_full;
-      for (int c = 0; c < kNC; ++c) mbar_arrive(&full[stage + c]);
+      mbar_arrive(&(is_v ? sh.mma.v_full : sh.mma.k_full)[stage]);
       mbar_arrive(is_v ? &sh.mma.vmeta_full[slot] : &sh.mma.meta_full[slot]);
     }
   }
@@ -335,16 +332,16 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   pdl_wait();
   const int64_t at = (static_cast<int64_t>(g) * p.max_prefix + ka) * kHd;
   if (warp >= Cfg::kConv) {
-    regs_dec<104>();
+    regs_dec<56>();
     prefix_convert<kHd>(sh, staging, k_ring, v_ring, keys, n);
   } else if (warp >= Cfg::kRowsWarps) {
-    regs_dec<56>();
+    regs_dec<40>();
     if (warp == Cfg::kLoadK && lane == 0)
       prefix_load<kHd>(sh, staging, p.kp + at, p.vp + at, keys, n);
     if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh.mma, k_ring, n, &g_err_prefix);
     if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh.mma, v_ring, n, &g_err_prefix);
   } else {
-    regs_inc<176>();
+    regs_inc<160>();
     const int row = 32 * (warp & 3) + lane, part = warp >> 2;
     const int r = rt * kTileRows + row, live = p.batch * p.group;
     const bool alive = r < live;
