@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <exception>
 #include <string>
 
 #include "../../include/qws.h"
@@ -520,8 +521,12 @@ size_t qws_prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* 
       check_offsets(fn, "cu_q", cu_q, n_seqs) != QWS_OK ||
       check_offsets(fn, "cu_k", cu_k, n_seqs) != QWS_OK)
     return 0;
-  return round256(qws::prompt_attention_workspace_bytes(cu_q, cu_k, n_seqs, n_q_heads, n_kv_heads,
-                                                        head_dim));
+  try {
+    return round256(qws::prompt_attention_workspace_bytes(cu_q, cu_k, n_seqs, n_q_heads,
+                                                          n_kv_heads, head_dim));
+  } catch (const std::exception&) {
+    return 0;
+  }
 }
 
 qws_status qws_prompt_attention(const qws_heads* q, const qws_heads* k, const qws_heads* v,
@@ -544,13 +549,20 @@ qws_status qws_prompt_attention(const qws_heads* q, const qws_heads* k, const qw
   if (out->data == q->data || out->data == k->data || out->data == v->data)
     return fail(QWS_ERR_SHAPE, "%s: out must not be q, k or v", fn);
   if (cu_q[n_seqs] == cu_q[0]) return ok();
-  QWS_TRY(check_ws(fn, ws, ws_bytes,
-                   qws::prompt_attention_workspace_bytes(cu_q, cu_k, n_seqs, n_q_heads,
-                                                         n_kv_heads, head_dim)));
-  const cudaError_t e = qws::launch_prompt_attention(
-      *q, *k, *v, *out, cu_q, cu_k, n_seqs, n_q_heads, n_kv_heads, head_dim, scale, softcap, ws,
-      reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, fn, "");
+  if (!aligned(ws, 16)) return fail(QWS_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
+  size_t need = 0;
+  cudaError_t e = cudaSuccess;
+  qws_status rc;
+  try {
+    rc = qws::launch_prompt_attention(*q, *k, *v, *out, cu_q, cu_k, n_seqs, n_q_heads, n_kv_heads,
+                                      head_dim, scale, softcap, ws, ws_bytes, &need,
+                                      reinterpret_cast<cudaStream_t>(stream), &e);
+  } catch (const std::exception& x) {      // the plan's host memory
+    return fail(QWS_ERR_SHAPE, "%s: %s", fn, x.what());
+  }
+  if (rc == QWS_ERR_WORKSPACE)
+    return fail(rc, "%s: workspace %zu bytes, need %zu", fn, ws_bytes, need);
+  if (rc != QWS_OK) return cuda_fail(e, fn, "");
   return ok();
 }
 

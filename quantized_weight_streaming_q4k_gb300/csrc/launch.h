@@ -184,11 +184,13 @@ cudaError_t launch_qk_norm_rope(const qws_heads& q, const qws_heads& k, const qw
 // causal attention over packed prompts (prompt.cu); cu_q, cu_k host arrays
 size_t prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k, int n_seqs,
                                         int n_q, int n_kv, int head_dim);
-cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
-                                    const qws_heads& out, const int64_t* cu_q,
-                                    const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
-                                    int head_dim, float scale, float cap, void* ws,
-                                    cudaStream_t st);
+// QWS_OK, QWS_ERR_WORKSPACE (*need bytes) or QWS_ERR_CUDA (*err)
+qws_status launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
+                                   const qws_heads& out, const int64_t* cu_q,
+                                   const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
+                                   int head_dim, float scale, float cap, void* ws,
+                                   size_t ws_bytes, size_t* need, cudaStream_t st,
+                                   cudaError_t* err);
 unsigned read_clear_prompt_errors();
 // decode attention of a batch over a shared prefix (prefix.cu); n_ctx a host array
 size_t prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_ctx, int batch,

@@ -22,7 +22,8 @@ namespace qws {
 
 __device__ unsigned g_err_prefix;
 
-constexpr int kOwnChunk = 128;      // keys of an own-cache item
+constexpr int kOwnWarps = 8, kOwnKeys = 4;
+constexpr int kOwnChunk = kOwnWarps * kOwnKeys;     // keys of an own-cache item
 constexpr int kMaxBatch = 256;      // sequences of one launch
 
 struct PrefixParams {
@@ -34,6 +35,7 @@ struct PrefixParams {
   int b0, batch;        // sequences b0 .. b0 + batch - 1 of the call
   int n_q, n_kv, group;
   int n_prefix, chunk, pieces, row_tiles;
+  int beside;           // the own parts run beside the shared part
   float scale, cap;
   int n_ctx[kMaxBatch];
   int first[kMaxBatch + 1];   // first own item of each sequence
@@ -53,7 +55,6 @@ __global__ void __launch_bounds__(kRowThreads)
   using Tile = RowTile<kPL, kR>;
   constexpr int kHd = Tile::kHd;
   extern __shared__ __align__(16) float smem[];
-  pdl_launch_dependents();
   pdl_wait();
   const int piece = blockIdx.x / p.row_tiles, rt = blockIdx.x - piece * p.row_tiles;
   const int g = blockIdx.y;
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  pdl_launch_dependents();
   const int64_t at = (static_cast<int64_t>(g) * p.max_prefix + ka) * kHd;
   if (warp >= Cfg::kConv) {
     regs_dec<56>();
@@ -378,74 +380,69 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   }
 }
 
-// Own parts: grid (own items, n_kv).  A warp takes keys w, w + 8, ... of the
-// item's piece in fours: K and V rows straight from memory, a lane holding its
-// columns, the dot products by warp sums; the warps are joined in shared memory
-// in order.
-constexpr int kOwnWarps = 8;
-constexpr int kOwnKeys = 4;
-
+// Own parts: grid (own items, n_kv).  A warp takes four neighbouring keys: K and V
+// rows straight from memory, all at once, a lane holding its columns, the dot products
+// by warp sums; the warps are joined in shared memory in order.  Short items, because
+// one costs three trips to memory however long it is: with 128 keys an item, four
+// sequences of up to 130 keys took 10.6 us.
+//
+// This kernel does not need the shared part's results: it runs beside that kernel and
+// waits for it only at its end, so that the joining kernel behind finds both done.  (The
+// shared part lets it start only after everything before the call has completed.)
 template <int kPL, int kG>
 __global__ void __launch_bounds__(kOwnWarps * 32)
     own_part_kernel(const __grid_constant__ PrefixParams p) {
   constexpr int kHd = kPL * 32;
   __shared__ __align__(16) float sacc[kOwnWarps][kG][kHd];
   __shared__ float sm[kOwnWarps][kG], sl[kOwnWarps][kG];
+  if (!p.beside) pdl_wait();
   pdl_launch_dependents();
-  pdl_wait();
   const int b = find_seq(p.first, p.batch, blockIdx.x);
   const int g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ka = (blockIdx.x - p.first[b]) * kOwnChunk, kb = min(p.n_ctx[b], ka + kOwnChunk);
   const int64_t head = (static_cast<int64_t>(p.b0 + b) * p.n_kv + g) * p.max_seq * kHd;
+  const int t = ka + warp * kOwnKeys;
   float q[kG][kPL], acc[kG][kPL], m[kG], l[kG];
+  float k[kOwnKeys][kPL], v[kOwnKeys][kPL];
 #pragma unroll
-  for (int h = 0; h < kG; ++h) {
+  for (int i = 0; i < kOwnKeys; ++i) {
+    const int64_t at = head + static_cast<int64_t>(min(t + i, kb - 1)) * kHd;
+    load_row<kPL>(p.kc + at, lane, k[i]);
+    load_row<kPL>(p.vc + at, lane, v[i]);
+  }
+#pragma unroll
+  for (int h = 0; h < kG; ++h)
     load_row<kPL>(p.q.data + static_cast<int64_t>(p.b0 + b) * p.q.token_stride +
                       (g * kG + h) * p.q.head_stride,
                   lane, q[h]);
-    m[h] = -INFINITY;
-    l[h] = 0.f;
 #pragma unroll
-    for (int j = 0; j < kPL; ++j) acc[h][j] = 0.f;
-  }
-  for (int t = ka + warp * kOwnKeys; t < kb; t += kOwnWarps * kOwnKeys) {
-    float k[kOwnKeys][kPL], v[kOwnKeys][kPL];
+  for (int h = 0; h < kG; ++h) {
+    float s[kOwnKeys];
+    m[h] = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kOwnKeys; ++i) {
-      const int64_t at = head + static_cast<int64_t>(min(t + i, kb - 1)) * kHd;
-      load_row<kPL>(p.kc + at, lane, k[i]);
-      load_row<kPL>(p.vc + at, lane, v[i]);
+      float d = 0.f;
+#pragma unroll
+      for (int j = 0; j < kPL; ++j) d = fmaf(q[h][j], k[i][j], d);
+      s[i] = t + i < kb ? soft_cap(warp_sum(d) * p.scale, p.cap) * kLog2e : -INFINITY;
+      m[h] = fmaxf(m[h], s[i]);
+    }
+    const float base = m[h] == -INFINITY ? 0.f : m[h];
+    float pr[kOwnKeys];
+    l[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kOwnKeys; ++i) {
+      pr[i] = exp2f(s[i] - base);
+      l[h] += pr[i];
     }
 #pragma unroll
-    for (int h = 0; h < kG; ++h) {
-      float s[kOwnKeys], mn = m[h];
+    for (int j = 0; j < kPL; ++j) {
+      float a = 0.f;
 #pragma unroll
-      for (int i = 0; i < kOwnKeys; ++i) {
-        float d = 0.f;
-#pragma unroll
-        for (int j = 0; j < kPL; ++j) d = fmaf(q[h][j], k[i][j], d);
-        s[i] = t + i < kb ? soft_cap(warp_sum(d) * p.scale, p.cap) * kLog2e : -INFINITY;
-        mn = fmaxf(mn, s[i]);
-      }
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m[h] - base);
-      float pr[kOwnKeys];
-      l[h] *= alpha;
-#pragma unroll
-      for (int i = 0; i < kOwnKeys; ++i) {
-        pr[i] = exp2f(s[i] - base);
-        l[h] += pr[i];
-      }
-#pragma unroll
-      for (int j = 0; j < kPL; ++j) {
-        float a = acc[h][j] * alpha;
-#pragma unroll
-        for (int i = 0; i < kOwnKeys; ++i)
-          if (t + i < kb) a = fmaf(pr[i], v[i][j], a);
-        acc[h][j] = a;
-      }
-      m[h] = mn;
+      for (int i = 0; i < kOwnKeys; ++i)
+        if (t + i < kb) a = fmaf(pr[i], v[i][j], a);
+      acc[h][j] = a;
     }
   }
 #pragma unroll
@@ -476,6 +473,7 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
       dst[kHd + 1] = L;
     }
   }
+  if (p.beside) pdl_wait();
 }
 
 // One warp per (sequence, query head, 64 columns): the prefix pieces, then the own ones.
@@ -622,6 +620,7 @@ cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const f
   p.n_q = n_q; p.n_kv = n_kv; p.group = n_q / n_kv;
   p.n_prefix = static_cast<int>(n_prefix);
   p.chunk = pl.chunk; p.pieces = pl.pieces;
+  p.beside = pl.pieces > 0;
   p.scale = scale; p.cap = cap;
   for (int b0 = 0; b0 < batch; b0 += kMaxBatch) {
     p.b0 = b0;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <vector>
 
 #include "attend_mma.cuh"
 #include "attend_rows.cuh"
@@ -349,6 +350,43 @@ int64_t seq_items(int64_t nq, int64_t nk, int tok, int chunk) {
   return items;
 }
 
+// When the last item ends, in steps of `unit` keys, if pieces are c steps long, an item
+// costs kItemSteps more than its steps, and the items start in their order on `slots`
+// places: a count of free places per time, so a few nanoseconds an item.
+constexpr int64_t kItemSteps = 5;
+int64_t end_of_items(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int n_kv, int tok,
+                     int64_t c, int unit, int slots) {
+  std::vector<int> free_at(static_cast<size_t>(c + kItemSteps) + 1, 0);
+  free_at[0] = slots;
+  size_t now = 0, last = 0;
+  const int chunk = static_cast<int>(c) * unit;
+  for (int s = 0; s < n_seqs; ++s) {
+    const int nq = static_cast<int>(cu_q[s + 1] - cu_q[s]);
+    const int nk = static_cast<int>(cu_k[s + 1] - cu_k[s]);
+    const int tiles = (nq + tok - 1) / tok;
+    for (int piece = 0; piece == 0 || static_cast<int64_t>(piece) * chunk < nk; ++piece) {
+      if (tiles == 0) break;
+      const int from = first_tile(piece, chunk, tok, nq, nk);
+      for (int tile = tiles - 1; tile >= from; --tile) {
+        const int64_t row = std::min<int64_t>(nq, (tile + int64_t(1)) * tok) + nk - nq;
+        const int64_t left = std::max<int64_t>(
+            0, std::min<int64_t>(row, nk) - static_cast<int64_t>(piece) * chunk);
+        const size_t size = static_cast<size_t>(std::min(c, ceil_div(left, unit)) + kItemSteps);
+        for (int m = n_kv; m > 0;) {
+          while (free_at[now] == 0) ++now;
+          const int take = std::min(m, free_at[now]);
+          free_at[now] -= take;
+          if (free_at.size() <= now + size) free_at.resize(2 * (now + size) + 1, 0);
+          free_at[now + size] += take;
+          last = std::max(last, now + size);
+          m -= take;
+        }
+      }
+    }
+  }
+  return static_cast<int64_t>(last);
+}
+
 // The form, tile and piece lengths of a call, and the sizes of its workspace.
 PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
                        int head_dim) {
@@ -368,18 +406,20 @@ PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int
   const int slots = pl.mma ? 152 : 304;             // items that run at once
   // steps of the longest tile, and an SM's share of all
   const int64_t steps = ceil_div(longest, unit);
-  const int64_t share = ceil_div(pairs * n_kv, static_cast<int64_t>(pl.rows) * unit * slots);
-  // A tile is cut where it is longer than an SM's share of the work.  Each item costs
-  // kItemSteps more; of 1 .. 32 pieces of the longest tile the number is taken whose
-  // last wave ends first, were all tiles that long.
-  constexpr int64_t kItemSteps = 5;
-  int64_t best = 1, best_cost = INT64_MAX;
-  const int64_t tiles = std::max<int64_t>(1, pairs * n_kv / (pl.rows * unit * steps));
-  for (int64_t k = 1; k <= 32 && (k == 1 || (steps > share && ceil_div(steps, k) >= 2)); ++k) {
-    const int64_t cost = ceil_div(tiles * k, slots) * (ceil_div(steps, k) + kItemSteps);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = k;
+  const int64_t total = ceil_div(pairs * n_kv, static_cast<int64_t>(pl.rows) * unit);
+  // A tile is cut where it is longer than an SM's share of the work, into the number of
+  // pieces (of the longest tile, 1 .. 32) that ends first.
+  int64_t best = 1;
+  if (steps * slots > total) {
+    int64_t best_end = INT64_MAX;
+    for (int64_t k = 1; k <= 32; k += k < 6 ? 1 : k < 12 ? 2 : 4) {
+      const int64_t c = ceil_div(steps, k);
+      if (k > 1 && c < 2) break;
+      const int64_t end = end_of_items(cu_q, cu_k, n_seqs, n_kv, pl.tok, c, unit, slots);
+      if (end < best_end) {
+        best_end = end;
+        best = k;
+      }
     }
   }
   pl.chunk = static_cast<int>(ceil_div(steps, best)) * unit;
@@ -453,12 +493,15 @@ size_t prompt_attention_workspace_bytes(const int64_t* cu_q, const int64_t* cu_k
   return pl.packed_bytes + pl.meta_bytes + pl.part_bytes;
 }
 
-cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
-                                    const qws_heads& out, const int64_t* cu_q,
-                                    const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
-                                    int head_dim, float scale, float cap, void* ws,
-                                    cudaStream_t st) {
+qws_status launch_prompt_attention(const qws_heads& q, const qws_heads& k, const qws_heads& v,
+                                   const qws_heads& out, const int64_t* cu_q,
+                                   const int64_t* cu_k, int n_seqs, int n_q, int n_kv,
+                                   int head_dim, float scale, float cap, void* ws,
+                                   size_t ws_bytes, size_t* need, cudaStream_t st,
+                                   cudaError_t* err) {
   const PromptPlan pl = plan_prompt(cu_q, cu_k, n_seqs, n_q, n_kv, head_dim);
+  *need = pl.packed_bytes + pl.meta_bytes + pl.part_bytes;
+  if (*need && (!ws || ws_bytes < *need)) return QWS_ERR_WORKSPACE;
   PromptParams p;
   p.q = q; p.k = k; p.v = v; p.out = out;
   p.packed = static_cast<uint8_t*>(ws);
@@ -490,9 +533,12 @@ cudaError_t launch_prompt_attention(const qws_heads& q, const qws_heads& k, cons
       case 128: e = run_prompt<4>(p, pl, items, ktiles, st); break;
       case 256: e = run_prompt<8>(p, pl, items, ktiles, st); break;
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess) {
+      *err = e;
+      return QWS_ERR_CUDA;
+    }
   }
-  return cudaSuccess;
+  return QWS_OK;
 }
 
 unsigned read_clear_prompt_errors() {

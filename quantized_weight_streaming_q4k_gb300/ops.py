@@ -257,6 +257,12 @@ def _vec(t, name: str, dev: int, dtype: torch.dtype, n: int) -> int:
     return t.data_ptr()
 
 
+def _cache(t, name: str, dev: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _here(t, name, dev)
+    return _dev(t, name, torch.float32)
+
+
 def _host_ints(v, name: str):
     """A ctypes int64 array of a list, tuple or CPU tensor of whole numbers."""
     if isinstance(v, torch.Tensor):
@@ -375,19 +381,20 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
     dev = torch.cuda.current_device()
     qh = _heads(q, "q", dev)
     B, n_q, hd = q.shape
-    n_kv = k_prefix.shape[0]
-    for t, name, dims in ((k_prefix, "k_prefix", 3), (v_prefix, "v_prefix", 3),
-                          (k_caches, "k_caches", 4), (v_caches, "v_caches", 4)):
-        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-            _here(t, name, dev)
-        shape = t.shape
-        if len(shape) != dims or shape[-1] != hd or shape[-3] != n_kv:
-            raise ValueError(f"{name} {tuple(shape)} does not match {n_kv} heads of {hd}")
-    if v_prefix.shape != k_prefix.shape or v_caches.shape != k_caches.shape:
-        raise ValueError("key and value caches must have the same shape")
+    shape_p, shape_c = k_prefix.shape, k_caches.shape
+    n_kv = shape_p[0]
+    if len(shape_p) != 3 or shape_p[2] != hd or v_prefix.shape != shape_p:
+        raise ValueError(f"k_prefix {tuple(shape_p)} and v_prefix {tuple(v_prefix.shape)} must be "
+                         f"[n_kv, max_prefix, {hd}]")
+    if (len(shape_c) != 4 or shape_c[0] != B or shape_c[1] != n_kv or shape_c[3] != hd
+            or v_caches.shape != shape_c):
+        raise ValueError(f"k_caches {tuple(shape_c)} and v_caches {tuple(v_caches.shape)} must be "
+                         f"[{B}, {n_kv}, max_seq, {hd}]")
+    kp, vp = _cache(k_prefix, "k_prefix", dev), _cache(v_prefix, "v_prefix", dev)
+    kc, vc = _cache(k_caches, "k_caches", dev), _cache(v_caches, "v_caches", dev)
     lens = _host_ints(n_ctx, "n_ctx")
-    if len(lens) != B or k_caches.shape[0] != B:
-        raise ValueError(f"q has {B} rows, n_ctx {len(lens)}, the caches {k_caches.shape[0]}")
+    if len(lens) != B:
+        raise ValueError(f"q has {B} rows, n_ctx {len(lens)}")
     out = _new(q.shape, dev, stream) if out is None else out
     oh = _heads(out, "out", dev, n_q, hd)
     if out.shape[0] != B:
@@ -399,10 +406,7 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
         L.qws_prefix_attention_workspace_bytes(n_prefix, lens, B, n_q, n_kv, hd), workspace, dev,
         stream)
     check(L.qws_prefix_attention(
-        C.byref(qh), _dev(k_prefix, "k_prefix", torch.float32),
-        _dev(v_prefix, "v_prefix", torch.float32), k_prefix.shape[1], n_prefix,
-        _dev(k_caches, "k_caches", torch.float32), _dev(v_caches, "v_caches", torch.float32),
-        k_caches.shape[2], lens, C.byref(oh), B, n_q, n_kv, hd, scale, softcap,
+        C.byref(qh), kp, vp, shape_p[1], n_prefix, kc, vc, shape_c[2], lens, C.byref(oh), B, n_q, n_kv, hd, scale, softcap,
         None if ws is None else ws.data_ptr(), nbytes, stream_handle(stream)))
     return out
 
