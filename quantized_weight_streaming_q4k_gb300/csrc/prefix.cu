@@ -48,49 +48,6 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
          (kPL * 32 + kPartPad);
 }
 
-// grid (pieces * row tiles, n_kv)
-template <int kPL, int kR>
-__global__ void __launch_bounds__(kRowThreads)
-    prefix_rows_kernel(const __grid_constant__ PrefixParams p) {
-  using Tile = RowTile<kPL, kR>;
-  constexpr int kHd = Tile::kHd;
-  extern __shared__ __align__(16) float smem[];
-  pdl_wait();
-  const int piece = blockIdx.x / p.row_tiles, rt = blockIdx.x - piece * p.row_tiles;
-  const int g = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = p.batch * p.group;
-  const int ka = piece * p.chunk, kb = min(p.n_prefix, ka + p.chunk);
-  Tile tile;
-  tile.init();
-  int vis[kR];
-  float* qs = Tile::q_rows(smem);
-#pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const int row = rt * (kRowWarps * kR) + warp * kR + r;
-    float x[kPL];
-#pragma unroll
-    for (int j = 0; j < kPL; ++j) x[j] = 0.f;
-    vis[r] = 0;
-    if (row < rows) {
-      vis[r] = p.n_prefix;
-      load_row<kPL>(p.q.data + static_cast<int64_t>(p.b0 + row / p.group) * p.q.token_stride +
-                        (g * p.group + row % p.group) * p.q.head_stride,
-                    lane, x);
-    }
-    store_row<kPL>(qs + r * kHd, lane, x);
-  }
-  tile.run(smem, p.kp + g * p.max_prefix * kHd, p.vp + g * p.max_prefix * kHd, kHd, kHd, ka, kb,
-           vis, p.scale, p.cap);
-#pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const int row = rt * (kRowWarps * kR) + warp * kR + r;
-    if (row < rows)
-      store_partial<kPL>(p.part + prefix_part<kPL>(p, piece, g, row), lane, tile.acc[r],
-                         tile.m[r], tile.l[r]);
-  }
-}
-
 // ------------------------------------------------------------ tensor cores
 // The shared part of 128 rows of one kv head against one piece of the prefix, on
 // the core of attend_mma.cuh.  The prefix is read once, as f32, straight from the cache:
@@ -476,6 +433,100 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
   if (p.beside) pdl_wait();
 }
 
+// Few keys in all: one CTA per sequence and kv head takes the shared and the own
+// positions, kOwnKeys neighbours a warp in turns, and writes out; no partial results, one
+// launch in place of three.  grid (batch, n_kv).
+template <int kPL, int kG>
+__global__ void __launch_bounds__(kOwnWarps * 32)
+    prefix_few_kernel(const __grid_constant__ PrefixParams p) {
+  constexpr int kHd = kPL * 32;
+  __shared__ __align__(16) float sacc[kOwnWarps][kG][kHd];
+  __shared__ float sm[kOwnWarps][kG], sl[kOwnWarps][kG];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int b = blockIdx.x, g = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t shared_at = static_cast<int64_t>(g) * p.max_prefix * kHd;
+  const int64_t own_at = (static_cast<int64_t>(p.b0 + b) * p.n_kv + g) * p.max_seq * kHd;
+  const int n = p.n_prefix + p.n_ctx[b];
+  float q[kG][kPL], acc[kG][kPL], m[kG], l[kG];
+#pragma unroll
+  for (int h = 0; h < kG; ++h) {
+    load_row<kPL>(p.q.data + static_cast<int64_t>(p.b0 + b) * p.q.token_stride +
+                      (g * kG + h) * p.q.head_stride,
+                  lane, q[h]);
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPL; ++j) acc[h][j] = 0.f;
+  }
+  for (int t = warp * kOwnKeys; t < n; t += kOwnChunk) {
+    float k[kOwnKeys][kPL], v[kOwnKeys][kPL];
+#pragma unroll
+    for (int i = 0; i < kOwnKeys; ++i) {
+      const int key = min(t + i, n - 1);
+      const bool own = key >= p.n_prefix;
+      const int64_t at = own ? own_at + static_cast<int64_t>(key - p.n_prefix) * kHd
+                             : shared_at + static_cast<int64_t>(key) * kHd;
+      load_row<kPL>((own ? p.kc : p.kp) + at, lane, k[i]);
+      load_row<kPL>((own ? p.vc : p.vp) + at, lane, v[i]);
+    }
+#pragma unroll
+    for (int h = 0; h < kG; ++h) {
+      float s[kOwnKeys], mn = m[h];
+#pragma unroll
+      for (int i = 0; i < kOwnKeys; ++i) {
+        float d = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPL; ++j) d = fmaf(q[h][j], k[i][j], d);
+        s[i] = t + i < n ? soft_cap(warp_sum(d) * p.scale, p.cap) * kLog2e : -INFINITY;
+        mn = fmaxf(mn, s[i]);
+      }
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f(m[h] - base);
+      float pr[kOwnKeys];
+      l[h] *= alpha;
+#pragma unroll
+      for (int i = 0; i < kOwnKeys; ++i) {
+        pr[i] = exp2f(s[i] - base);
+        l[h] += pr[i];
+      }
+#pragma unroll
+      for (int j = 0; j < kPL; ++j) {
+        float a = acc[h][j] * alpha;
+#pragma unroll
+        for (int i = 0; i < kOwnKeys; ++i)
+          if (t + i < n) a = fmaf(pr[i], v[i][j], a);
+        acc[h][j] = a;
+      }
+      m[h] = mn;
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kG; ++h) {
+    store_row<kPL>(sacc[warp][h], lane, acc[h]);
+    if (lane == 0) {
+      sm[warp][h] = m[h];
+      sl[warp][h] = l[h];
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < kG * kHd; e += kOwnWarps * 32) {
+    const int h = e / kHd, c = e - h * kHd;
+    float M = -INFINITY;
+    for (int w = 0; w < kOwnWarps; ++w) M = fmaxf(M, sm[w][h]);
+    const float base = M == -INFINITY ? 0.f : M;
+    float a = 0.f, L = 0.f;
+    for (int w = 0; w < kOwnWarps; ++w) {
+      const float f = exp2f(sm[w][h] - base);
+      a = fmaf(sacc[w][h][c], f, a);
+      L = fmaf(sl[w][h], f, L);
+    }
+    p.out.data[static_cast<int64_t>(p.b0 + b) * p.out.token_stride +
+               (g * kG + h) * p.out.head_stride + c] = L == 0.f ? 0.f : a / L;
+  }
+}
+
 // One warp per (sequence, query head, 64 columns): the prefix pieces, then the own ones.
 template <int kPL>
 __global__ void __launch_bounds__(128)
@@ -506,36 +557,31 @@ __global__ void __launch_bounds__(128)
 // ------------------------------------------------------------ host side
 namespace {
 
-constexpr int kPrefixR = 4;
-constexpr int kPrefixRows = kRowWarps * kPrefixR;
-
-constexpr int64_t kPrefixMmaFrom = 1;
+// Shared and own positions of the longest sequence up to which one CTA a sequence and kv
+// head takes them all.
+constexpr int64_t kFewKeys = 256;
 
 struct PrefixPlan {
-  bool mma;              // the shared part on the tensor cores
-  int rows;              // of a row tile
+  bool few;              // all positions by one kernel
   int chunk, pieces;
   size_t part_floats, own_floats;    // of the largest launch
 };
 
 PrefixPlan plan_prefix(int64_t n_prefix, const int64_t* n_ctx, int batch, int n_q, int n_kv,
                        int head_dim) {
-  PrefixPlan pl;
+  PrefixPlan pl = {};
   const int group = n_q / n_kv, some = std::min(batch, kMaxBatch);
-  pl.mma = n_prefix >= kPrefixMmaFrom;
-  pl.rows = pl.mma ? kTileRows : kPrefixRows;
-  const int64_t tiles = (static_cast<int64_t>(some) * group + pl.rows - 1) / pl.rows;
-  int64_t chunk;
-  if (pl.mma) {
-    // one item an SM
-    const int64_t want = std::max<int64_t>(1, 152 / (tiles * n_kv));
-    const int64_t key_tiles = (n_prefix + kTileKeys - 1) / kTileKeys;
-    chunk = std::min<int64_t>((key_tiles + want - 1) / want, kMaxPieceTiles) * kTileKeys;
-  } else {
-    // about two items an SM
-    const int64_t want = std::max<int64_t>(1, 304 / (tiles * n_kv));
-    chunk = std::max<int64_t>(64, ((n_prefix + want - 1) / want + 31) / 32 * 32);
-  }
+  int64_t longest = 0;
+  for (int b = 0; b < batch; ++b) longest = std::max(longest, n_ctx[b]);
+  pl.few = n_prefix + longest <= kFewKeys;
+  if (pl.few) return pl;
+  const int64_t tiles = (static_cast<int64_t>(some) * group + kTileRows - 1) / kTileRows;
+  // one item an SM
+  const int64_t want = std::max<int64_t>(1, 152 / (tiles * n_kv));
+  const int64_t key_tiles = (n_prefix + kTileKeys - 1) / kTileKeys;
+  const int64_t chunk =
+      std::max<int64_t>(1, std::min<int64_t>((key_tiles + want - 1) / want, kMaxPieceTiles)) *
+      kTileKeys;
   pl.chunk = static_cast<int>(chunk);
   pl.pieces = static_cast<int>((n_prefix + chunk - 1) / chunk);
   const size_t row = static_cast<size_t>(head_dim) + kPartPad;
@@ -553,10 +599,19 @@ PrefixPlan plan_prefix(int64_t n_prefix, const int64_t* n_ctx, int batch, int n_
 
 template <int kPL>
 cudaError_t run_prefix(const PrefixParams& p, const PrefixPlan& pl, cudaStream_t st) {
-  using Tile = RowTile<kPL, kPrefixR>;
   cudaError_t e = cudaSuccess;
   const unsigned nkv = static_cast<unsigned>(p.n_kv);
-  if (p.pieces > 0 && pl.mma) {
+  if (pl.few) {
+    const dim3 grid(static_cast<unsigned>(p.batch), nkv);
+    switch (p.group) {
+      case 1: return pdl_launch(prefix_few_kernel<kPL, 1>, grid, kOwnWarps * 32, 0, st, p);
+      case 2: return pdl_launch(prefix_few_kernel<kPL, 2>, grid, kOwnWarps * 32, 0, st, p);
+      case 3: return pdl_launch(prefix_few_kernel<kPL, 3>, grid, kOwnWarps * 32, 0, st, p);
+      case 4: return pdl_launch(prefix_few_kernel<kPL, 4>, grid, kOwnWarps * 32, 0, st, p);
+    }
+    return cudaErrorInvalidValue;
+  }
+  if (p.pieces > 0) {
     constexpr int kHd = kPL * 32;
     using Cfg = PrefixCfg<kHd>;
     constexpr size_t kSmem =
@@ -568,15 +623,6 @@ cudaError_t run_prefix(const PrefixParams& p, const PrefixPlan& pl, cudaStream_t
     if (e != cudaSuccess) return e;
     e = pdl_launch(kernel, dim3(static_cast<unsigned>(p.pieces * p.row_tiles), nkv), Cfg::kThreads,
                    kSmem, st, p);
-    if (e != cudaSuccess) return e;
-  } else if (p.pieces > 0) {
-    e = cudaFuncSetAttribute(prefix_rows_kernel<kPL, kPrefixR>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(Tile::kSmem));
-    if (e != cudaSuccess) return e;
-    e = pdl_launch(prefix_rows_kernel<kPL, kPrefixR>,
-                   dim3(static_cast<unsigned>(p.pieces * p.row_tiles), nkv), kRowThreads,
-                   Tile::kSmem, st, p);
     if (e != cudaSuccess) return e;
   }
   if (const int items = p.first[p.batch]) {
@@ -625,7 +671,7 @@ cudaError_t launch_prefix_attention(const qws_heads& q, const float* kp, const f
   for (int b0 = 0; b0 < batch; b0 += kMaxBatch) {
     p.b0 = b0;
     p.batch = std::min(batch - b0, kMaxBatch);
-    p.row_tiles = (p.batch * p.group + pl.rows - 1) / pl.rows;
+    p.row_tiles = (p.batch * p.group + kTileRows - 1) / kTileRows;
     p.first[0] = 0;
     for (int b = 0; b < p.batch; ++b) {
       p.n_ctx[b] = static_cast<int>(n_ctx[b0 + b]);

@@ -123,7 +123,7 @@ def test_prompt_workspace(lib):
 
 
 def test_prefix_attention(lib):
-    ok = dict(q=heads(A), kp=B, vp=D, max_prefix=100, n_prefix=100, kc=B, vc=D, max_seq=50,
+    ok = dict(q=heads(A), kp=B, vp=D, max_prefix=1000, n_prefix=1000, kc=B, vc=D, max_seq=50,
               n_ctx=ints(1, 50, 0), out=heads(E), batch=3, nq=4, nkv=2, hd=64, scale=1.0, cap=0.0)
 
     def call(ws=A, ws_bytes=1 << 40, **kw):
@@ -139,15 +139,17 @@ def test_prefix_attention(lib):
     for name in ("kp", "vp", "kc", "vc"):
         assert call(**{name: None}) == NULL and call(**{name: A + 8}) == ALIGN
     assert call(n_ctx=None) == NULL
-    assert call(n_prefix=101) == SHAPE and call(n_prefix=-1) == SHAPE
+    assert call(n_prefix=1001) == SHAPE and call(n_prefix=-1) == SHAPE
     assert call(max_prefix=2 ** 31, n_prefix=5) == SHAPE and call(max_seq=2 ** 31) == SHAPE
     assert call(n_ctx=ints(1, 51, 0)) == SHAPE and call(n_ctx=ints(1, -1, 0)) == SHAPE
     assert call(batch=-1) == SHAPE
     assert call(nq=5) == SHAPE and call(hd=65) == SHAPE and call(nq=16, nkv=2) == SHAPE
     assert call(scale=float("nan")) == SHAPE and call(cap=-0.5) == SHAPE
     assert call(out=heads(A)) == SHAPE and call(out=heads(E, 64, 64)) == SHAPE
-    need = lib.qws_prefix_attention_workspace_bytes(100, ints(1, 50, 0), 3, 4, 2, 64)
+    need = lib.qws_prefix_attention_workspace_bytes(1000, ints(1, 50, 0), 3, 4, 2, 64)
     assert need > 0
     assert call(ws=None, ws_bytes=0) == WORKSPACE and call(ws_bytes=need // 2) == WORKSPACE
     assert call(ws=A + 4) == ALIGN
-    assert lib.qws_prefix_attention_workspace_bytes(100, ints(1, -1), 2, 4, 2, 64) == 0
+    assert lib.qws_prefix_attention_workspace_bytes(1000, ints(1, -1), 2, 4, 2, 64) == 0
+    # few positions in all: one kernel, no workspace
+    assert lib.qws_prefix_attention_workspace_bytes(100, ints(1, 50, 0), 3, 4, 2, 64) == 0

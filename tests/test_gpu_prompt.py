@@ -396,6 +396,60 @@ def test_prefix_lengths(n_prefix, batch):
     run_prefix(gen(30 + batch), n_prefix, n_ctx, 8, 4, 256)
 
 
+@pytest.mark.parametrize("n_prefix", [0, 1, 33, 64, 65, 130])
+@pytest.mark.parametrize("nq,nkv,hd", [(8, 4, 256), (4, 1, 64), (2, 2, 32), (3, 1, 128)])
+def test_prefix_short_shared_long_own(n_prefix, nq, nkv, hd):
+    run_prefix(gen(37), n_prefix, [0, 1, 400, 31, 32, 33, 257], nq, nkv, hd)
+
+
+@pytest.mark.parametrize("n_prefix,n_ctx", [(0, [0, 0]), (1, [0]), (5, [0, 3]), (200, [56, 0, 1]),
+                                            (256, [0]), (257, [0]), (0, [256, 7]), (0, [257, 7])])
+def test_prefix_few_positions(n_prefix, n_ctx):
+    # around the border of the one-kernel form, with and without either part
+    run_prefix(gen(38), n_prefix, n_ctx, 8, 4, 128)
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("mag", [1e-20, 1e-6, 1e4, 1e15])
+def test_prefix_magnitudes(mag, hd):
+    g = gen(39)
+    q, kp, vp = normal(g, 5, 4, hd) * mag, normal(g, 2, 900, hd) / mag, normal(g, 2, 900, hd) * mag
+    kc, vc = normal(g, 5, 2, 20, hd) / mag, normal(g, 5, 2, 20, hd) * mag
+    out = ops.prefix_attention(q, kp, vp, 900, kc, vc, [20, 0, 1, 7, 20], hd ** -0.5)
+    check_prefix(q, kp, vp, 900, kc, vc, [20, 0, 1, 7, 20], hd ** -0.5, 0.0, out)
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+def test_prefix_rows_of_very_different_size(hd):
+    # key and value rows far from the piece's scale: each still counts with its own bits
+    g = gen(41)
+    q, kp, vp = normal(g, 3, 4, hd), normal(g, 2, 700, hd), normal(g, 2, 700, hd)
+    kp[:, 100:110] *= 1e-6
+    kp[:, 300] *= 30.0
+    q[..., : hd // 2] *= 0.05
+    vp[:, 200:205] *= 1e7
+    vp[:, 400:420] *= 1e-9
+    vp[:, 650] = 0.0
+    vp[0, 0:64] *= 1e-12          # the rows that the scale is taken from
+    kc, vc = normal(g, 3, 2, 5, hd), normal(g, 3, 2, 5, hd)
+    out = ops.prefix_attention(q, kp, vp, 700, kc, vc, [5, 0, 2], hd ** -0.5)
+    check_prefix(q, kp, vp, 700, kc, vc, [5, 0, 2], hd ** -0.5, 0.0, out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefix_seen_infinities_show(bad):
+    g = gen(42)
+    q, kp, vp = normal(g, 3, 4, 64), normal(g, 2, 700, 64), normal(g, 2, 700, 64)
+    kc = normal(g, 3, 2, 5, 64)
+    want = ops.prefix_attention(q, kp, vp, 700, kc, kc, [5, 0, 2], 0.125)
+    vp[1, 333, 7] = bad
+    got = ops.prefix_attention(q, kp, vp, 700, kc, kc, [5, 0, 2], 0.125)
+    assert not torch.isfinite(got[:, 2:, 7]).any()
+    keep = [i for i in range(64) if i != 7]
+    assert torch.all((got[:, 2:][..., keep] - want[:, 2:][..., keep]).abs() <= 2e-5)
+    assert torch.all((got[:, :2] - want[:, :2]).abs() <= 2e-5)
+
+
 @pytest.mark.parametrize("nq,nkv,hd", [(1, 1, 32), (4, 4, 128), (8, 2, 64), (6, 3, 32), (16, 4, 128),
                                        (3, 1, 256), (4, 1, 256)])
 def test_prefix_head_layouts(nq, nkv, hd):
@@ -516,7 +570,8 @@ def test_prompt_refusals():
     with pytest.raises(ValueError):
         ops.prefix_attention(q[:3], kp, kp, 8, kc, kc, [0, 0], 1.0)
     with pytest.raises(ops.QwsError):
-        ops.prefix_attention(q[:3], kp, kp, 8, kc, kc, [1, 2, 3], 1.0,
+        long = torch.zeros(2, 300, 64, device="cuda")
+        ops.prefix_attention(q[:3], long, long, 300, kc, kc, [1, 2, 3], 1.0,
                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     W = torch.zeros(10, 18, dtype=torch.uint8, device="cuda")
     with pytest.raises(ops.QwsError):
