@@ -13,28 +13,20 @@
 // in f32, by the rows that see it.
 //
 // Per tile of 64 keys, S = Q K^T (128 x 64) and O_tile = P V (128 x head_dim).
-// Q hi / lo and P hi / lo are A operands in tensor memory; K and V come through
-// rings in shared memory, both as rows (a key) of 128 bytes (64 columns), swizzled: K
-// as a K-major B operand, V as an MN-major one, so neither is transposed.  O_tile is
-// NOT accumulated in tensor memory: the tensor cores' f32 accumulation does
-// not round to nearest, and its bias grows with the number of steps.  Each
-// tile's O_tile (12 accumulation steps) is added to f32 registers with the
-// softmax's rescaling, one multiplication and one fma a value, which the three
-// products per value leave time for (256 of about 3000 cycles a tile at head_dim
-// 256).  This also spares the correction pass over tensor memory.
+// Q and P are A operands in tensor memory; K and V come through rings in shared
+// memory, both as rows (a key) of 128 bytes (64 columns), swizzled: K as a K-major B
+// operand, V as an MN-major one, so neither is transposed.  O_tile is NOT accumulated
+// in tensor memory: the tensor cores' f32 accumulation does not round to nearest, and
+// its bias grows with the number of steps.  Each tile's O_tile (12 accumulation steps)
+// is added to f32 registers with the softmax's rescaling, one multiplication and one fma
+// a value, which the three products per value leave time for (256 of about 3000 cycles a
+// tile at head_dim 256).  This also spares the correction pass over tensor memory.
 //
-// TMEM columns (all 512 are allocated, so they start at 0): Q hi 0.., Q lo 128..,
-// S 256.., P hi 320.., P lo 352.., O_tile 384.. and 448.. (64 columns each: the 64-column
-// chunks of O_tile take turns).
-//
-// Roles: 4 * kSplit softmax warps (thread = row 32 (w % 4) + lane, w / 4 = which part of
-// the tile's keys and of the output columns) and four helper warps: two load K and V
-// chunks into their rings, two issue the MMAs of Q K^T and of P V.  One issuing warp
-// would do, but a commit holds the issuing warp until its MMAs are done, and the tensor
-// cores then idle for the next wait; with two, one's MMAs are queued behind the other's.
-// A softmax warp turns S(j+1) into weights before it drains O_tile(j), so that Q K(j+2)^T
-// and P V(j) run behind it; the chunks of O_tile alternate between two accumulators, so
-// that a chunk is drained while the next is multiplied.
+// Two warps load K and V chunks into the rings, two issue the MMAs of Q K^T and of P V.
+// One issuing warp would do, but a commit holds the issuing warp until its MMAs are
+// done, and the tensor cores then idle for the next wait; with two, one's MMAs are
+// queued behind the other's.  The chunks of O_tile alternate between two accumulators,
+// so that one is drained while the next is multiplied.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -53,7 +45,6 @@ enum : unsigned {
 
 constexpr int kTileRows = 128;
 constexpr int kTileKeys = 64;
-__device__ constexpr float kTanh[8] = {1.0f, -0.333332777f, 0.133321598f, -0.0538709126f, 0.0214648172f, -0.00791743957f, 0.00228222599f, -0.000353344454f};
 constexpr int kPShift = 14;            // weights are 2^14 exp2(s - max)
 
 // what a key tile carries beside its values
@@ -67,15 +58,18 @@ static_assert(sizeof(TileMeta) == 272, "copied in 16-byte units");
 
 // A unit: 64 keys x 64 columns of K or V, hi then lo.
 // kWholeT: the units of a half tile come and go together, by their first one's barriers.
-template <int kHdT, int kSplitT, int kDepthT = 0, bool kWholeT = false>
+// kBufsT: buffers of S and of P in tensor memory.
+template <int kHdT, int kDepthT, bool kWholeT, int kBufsT>
 struct MmaCfg {
   static constexpr int kHd = kHdT;
   static constexpr bool kWhole = kWholeT;
-  static constexpr int kSplit = kSplitT;                // threads of a query row
+  static constexpr int kBufs = kBufsT;
+  // tiles whose meta records are there: with only two, the loads of a tile's K would wait
+  // for the softmax of the tile before the last, and the ring would not run ahead
+  static constexpr int kMetas = 2 * kBufs;
   static constexpr int kNC = kHd > 64 ? kHd / 64 : 1;   // chunks of head_dim
   static constexpr int kHC = kHd / kNC;                 // columns of a chunk
-  static constexpr int kKeys = kTileKeys / kSplit;      // of a tile, a thread's
-  static constexpr int kOC = kHC / kSplit;              // of a chunk, a thread's
+  static constexpr int kOC = kHC / 2;                   // of a chunk, a thread's
   static constexpr uint32_t kPart = kTileKeys * 128;    // hi or lo of a unit
   static constexpr uint32_t kUnit = 2 * kPart;
   static constexpr uint32_t kHalfTile = kNC * kUnit;    // K, or V, of a tile
@@ -83,45 +77,52 @@ struct MmaCfg {
   // units of each of the two rings: 6, or kDepth whole tiles
   static constexpr int kStages = kDepthT ? kDepthT * kNC : 6;
   static constexpr uint32_t kRing = 2 * kStages * kUnit;
-  // softmax warps, then the helpers
-  static constexpr int kRowsWarps = 4 * kSplit;
+  // 8 warps keep the output (thread = row 32 (w % 4) + lane, w / 4 = which half of the
+  // output columns); with two buffers of S and P, 8 others the softmax
+  static constexpr int kRowsWarps = 8;
   static constexpr uint32_t kScratch = kRowsWarps * 32 * 36 * 4;   // in the V ring
   static_assert(kScratch <= kStages * kUnit, "the V ring holds the scratch");
-  static constexpr int kLoadK = kRowsWarps, kLoadV = kRowsWarps + 1;
-  static constexpr int kMmaQk = kRowsWarps + 2, kMmaPv = kRowsWarps + 3;
-  static constexpr int kThreads = 32 * (kRowsWarps + 4);
-  // Registers: a scheduler's quarter of the file (16384) holds 3 (5 for kSplit = 4)
-  // warps, 168 (96) a thread at launch; the helpers keep few and the softmax warps
-  // take what that frees: 2 x 224 + 56 = 3 x 168, 4 x 112 + 32 = 5 x 96.
-  static_assert(kSplit == 2 || kSplit == 4, "register split");
+  static constexpr int kSoftWarps = kBufs > 1 ? 4 : 8;    // of a tile
+  static constexpr int kLoadK = kRowsWarps + (kBufs > 1 ? 8 : 0), kLoadV = kLoadK + 1;
+  static constexpr int kMmaQk = kLoadK + 2, kMmaPv = kLoadK + 3;
+  // Tensor memory columns (all 512 are allocated, so they start at 0): Q hi, Q lo, the
+  // buffers of S, those of P (hi, lo), and two of O_tile.  Where that is too much, Q lo
+  // is in shared memory (its MMAs take 48 cycles a step in place of 32).
+  static constexpr bool kQLoSmem = kBufs > 1 && kHd > 128;
+  static constexpr uint32_t kQLoBytes = kQLoSmem ? kNC * kTileRows * 128 : 0;
+  static constexpr uint32_t kTmQhi = 0, kTmQlo = kHd / 2;
+  static constexpr uint32_t kTmS = kHd > 128 && !kQLoSmem ? 256 : 128;
+  static constexpr uint32_t kTmP = kTmS + 64 * kBufs;
+  static constexpr uint32_t kTmO = kTmP + 64 * kBufs;
+  static_assert(kTmO + 128 <= 512, "tensor memory");
 };
 
-template <class Cfg>
-__device__ __forceinline__ void regs_few() {
-  if constexpr (Cfg::kSplit == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  else asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-template <class Cfg>
-__device__ __forceinline__ void regs_many() {
-  if constexpr (Cfg::kSplit == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-
-constexpr uint32_t kTmQhi = 0, kTmQlo = 128, kTmS = 256, kTmPhi = 320, kTmPlo = 352, kTmO = 384;
 
 // barriers and small exchanges of one CTA
 template <class Cfg>
 struct MmaShared {
   uint64_t k_full[Cfg::kStages], k_empty[Cfg::kStages];
   uint64_t v_full[Cfg::kStages], v_empty[Cfg::kStages];
-  uint64_t meta_full[2], meta_free[2];      // kscale
-  uint64_t vmeta_full[2], vmeta_free[2];    // vscale, left_out
+  uint64_t meta_full[Cfg::kMetas], meta_free[Cfg::kMetas];      // kscale
+  uint64_t vmeta_full[Cfg::kMetas], vmeta_free[Cfg::kMetas];    // vscale, left_out
   uint64_t o_full[2], o_free[2];
-  uint64_t q_ready, s_full, s_free, p_ready, done[2];
+  uint64_t s_full[Cfg::kBufs], s_free[Cfg::kBufs];
+  uint64_t p_ready[Cfg::kBufs], p_free[Cfg::kBufs];
+  uint64_t m_free[2];
+  uint64_t q_ready, done[2];
   uint32_t tmem;
-  uint32_t pad;
-  float xmax[2][Cfg::kSplit][kTileRows];
-  TileMeta meta[2];
+  uint32_t dead;
+  float qmax[2][kTileRows];
+  float x[2][2][kTileRows];
+  TileMeta meta[Cfg::kMetas];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -130,57 +131,64 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// (d0, d1) = (a0, a1) * (b, b)
-__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0,
-                                     float b1) {
-  asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rc, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, rc;\n\t}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+__device__ __forceinline__ float2 bits2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
-// (d0, d1) = (d0, d1) * (a, a) + (b0, b1)
-__device__ __forceinline__ void scale_add2(float& d0, float& d1, float a, float b0, float b1) {
-  asm("{\n\t.reg .b64 rd, ra, rb;\n\t"
-      "mov.b64 rd, {%0, %1};\n\t"
-      "mov.b64 ra, {%2, %2};\n\t"
-      "mov.b64 rb, {%3, %4};\n\t"
-      "fma.rn.f32x2 rd, rd, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, rd;\n\t}"
-      : "+f"(d0), "+f"(d1)
-      : "f"(a), "f"(b0), "f"(b1));
+// a two-f32 version of split_f16x2: hi and lo of both
+__device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16x2(x.x, x.y);
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), x);      // exact
+  lo = pack_f16x2(r.x, r.y);
 }
 
-// out = scale * tanh(y) in place, for a thread's scores of a tile.  |y| <= 1 (scores
-// within the cap): y P(y^2), P fitted to tanh(y) / y on [0, 1] in y^2 with a relative
-// error below 5e-9, so 1e-7 with the roundings; beyond, 1 - 2 / (1 + e^2|y|), which is 1.2e-7
-// absolute on values above 0.76.  The library's tanhf costs some 60 instructions a score
-// here, four times the rest of the softmax; this 12.
-__device__ __forceinline__ float tanh_small(float y) {
-  const float z = y * y;
-  float p = kTanh[7];
+// y = scale * tanh(y), for a thread's scores of a tile.  tanh(y) = y P(y^2), P fitted to
+// tanh(y) / y in y^2 with a relative error below 6e-9 (1e-7 with the roundings): with four
+// terms while |y| <= 1/4 in the whole warp, which scores well within the cap are, with
+// eight to 1; beyond, 1 - 2 / (1 + e^2|y|), which is 1.2e-7 absolute on values above 0.76.
+// The library's tanhf costs some 60 instructions a score here, four times the rest of the
+// softmax; this 4 or 7.
+template <int kN>
+__device__ __forceinline__ float2 tanh_poly(float2 y, const float (&c)[kN]) {
+  const float2 z = __fmul2_rn(y, y);
+  float2 p = make_float2(c[kN - 1], c[kN - 1]);
 #pragma unroll
-  for (int i = 6; i >= 0; --i) p = fmaf(p, z, kTanh[i]);
-  return y * p;
+  for (int i = kN - 2; i >= 0; --i) p = __ffma2_rn(p, z, make_float2(c[i], c[i]));
+  return __fmul2_rn(y, p);
+}
+__device__ __forceinline__ float tanh_big(float y) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(fabsf(y) * (2.f * kLog2e))));
+  return copysignf(1.f - 2.f * r, y);
 }
 template <int kN>
 __device__ __forceinline__ void tanh_scaled(float (&y)[kN], float scale) {
+  constexpr float kSmall[4] = {1.0f, -0.33333206f, 0.13323133f, -0.051327724f};
+  constexpr float kAll[8] = {1.0f,          -0.333332777f,   0.133321598f,  -0.0538709126f,
+                             0.0214648172f, -0.00791743957f, 0.00228222599f, -0.000353344454f};
+  const float2 s = make_float2(scale, scale);
   float a = fabsf(y[0]);
 #pragma unroll
   for (int i = 1; i < kN; ++i) a = fmaxf(a, fabsf(y[i]));
-  if (!__any_sync(0xFFFFFFFFu, a > 1.f)) {
+  if (!__any_sync(0xFFFFFFFFu, a > 0.25f)) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) y[i] = tanh_small(y[i]) * scale;
+    for (int i = 0; i < kN; i += 2) {
+      const float2 r = __fmul2_rn(tanh_poly(make_float2(y[i], y[i + 1]), kSmall), s);
+      y[i] = r.x;
+      y[i + 1] = r.y;
+    }
   } else {
+    const bool big = __any_sync(0xFFFFFFFFu, a > 1.f);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float b = fabsf(y[i]);
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(b * (2.f * kLog2e))));
-      const float big = copysignf(1.f - 2.f * r, y[i]);
-      y[i] = (b > 1.f ? big : tanh_small(y[i])) * scale;
+    for (int i = 0; i < kN; i += 2) {
+      float2 t = tanh_poly(make_float2(y[i], y[i + 1]), kAll);
+      if (big) {
+        t.x = fabsf(y[i]) > 1.f ? tanh_big(y[i]) : t.x;
+        t.y = fabsf(y[i + 1]) > 1.f ? tanh_big(y[i + 1]) : t.y;
+      }
+      const float2 r = __fmul2_rn(t, s);
+      y[i] = r.x;
+      y[i + 1] = r.y;
     }
   }
 }
@@ -203,19 +211,26 @@ __device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh, uint32_t f
     mbar_init(&sh.v_full[s], full_count);
     mbar_init(&sh.v_empty[s], 1);
   }
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < Cfg::kMetas; ++s) {
     mbar_init(&sh.meta_full[s], full_count);
-    mbar_init(&sh.meta_free[s], Cfg::kRowsWarps);
+    mbar_init(&sh.meta_free[s], Cfg::kSoftWarps);
     mbar_init(&sh.vmeta_full[s], full_count);
     mbar_init(&sh.vmeta_free[s], Cfg::kRowsWarps);
+  }
+  for (int s = 0; s < 2; ++s) {
     mbar_init(&sh.o_full[s], 1);
     mbar_init(&sh.o_free[s], Cfg::kRowsWarps);
+    mbar_init(&sh.m_free[s], Cfg::kRowsWarps);
     mbar_init(&sh.done[s], 1);
   }
+  for (int s = 0; s < Cfg::kBufs; ++s) {
+    mbar_init(&sh.s_full[s], 1);
+    mbar_init(&sh.s_free[s], Cfg::kSoftWarps);
+    mbar_init(&sh.p_ready[s], Cfg::kSoftWarps);
+    mbar_init(&sh.p_free[s], 1);
+  }
   mbar_init(&sh.q_ready, Cfg::kRowsWarps);
-  mbar_init(&sh.s_full, 1);
-  mbar_init(&sh.s_free, Cfg::kRowsWarps);
-  mbar_init(&sh.p_ready, Cfg::kRowsWarps);
+  sh.dead = 0;
   fence_barrier_init();
 }
 
@@ -233,46 +248,62 @@ struct RingAt {
 };
 
 // ------------------------------------------------------------ the MMA issuers
-// Each a whole warp.  S(j) = Q K(j)^T, chunk after chunk of head_dim, once S(j-1) has
-// been read; of each chunk the small cross terms first.
+// Each a whole warp.  A wait costs some 200 cycles here even if it is over, so the barriers
+// of a chunk are asked together, and waited for one by one only after a no.
+// S(j) = Q K(j)^T, chunk after chunk of head_dim, once what was in its buffer has been
+// read; of each chunk the small cross terms first.
 template <class Cfg>
-__device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring, int n,
-                                             unsigned* err) {
+__device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring,
+                                             const uint8_t* q_lo, int n, unsigned* err) {
   constexpr uint32_t kIdesc = tc_idesc_f16(kTileRows, kTileKeys);
   constexpr int kSteps = Cfg::kHC / 16;
   const uint32_t one = elect_one();
   const uint32_t base = sw128_lo(smem_addr(k_ring));   // units of 16 bytes
+  const uint32_t lo_base = sw128_lo(smem_addr(q_lo));
   RingAt<Cfg::kStages> at;
-  bool ok = true, there = false;       // there: this chunk's unit has been seen to land
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-  };
-  if (n > 0) wait(&sh.q_ready, 0);
+  RingAt<Cfg::kBufs> buf;
+  bool ok = n <= 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
   for (int j = 0; j < n && ok; ++j) {
+    const uint32_t d = Cfg::kTmS + static_cast<uint32_t>(buf.stage) * 64u;
+    uint32_t acc = 0;
 #pragma unroll 1
     for (int c = 0; c < Cfg::kNC; ++c) {
-      if (!there && !(Cfg::kWhole && c > 0)) wait(&sh.k_full[at.stage], at.phase);
-      if (c == 0 && j > 0) wait(&sh.s_free, static_cast<uint32_t>(j - 1) & 1u);
+      const bool unit = !(Cfg::kWhole && c > 0), tile = c == 0 && j >= Cfg::kBufs;
+      uint64_t* const s_free = &sh.s_free[buf.stage];
+      uint64_t* const k_full = &sh.k_full[at.stage];
+      const bool there = (!unit || mbar_test(k_full, at.phase)) &
+                         (!tile || mbar_test(s_free, buf.phase ^ 1u));
+      if (!__all_sync(0xFFFFFFFFu, there))
+        ok = __all_sync(0xFFFFFFFFu, (!unit || mbar_wait(k_full, at.phase)) &&
+                                         (!tile || mbar_wait(s_free, buf.phase ^ 1u)));
       tc_fence_after();
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
       uint64_t* empty = &sh.k_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
-      const bool next = (!Cfg::kWhole || c == Cfg::kNC - 1) &&
-                        mbar_test(&sh.k_full[at.stage], at.phase);
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          const uint32_t a = (t == 1 ? kTmQlo : kTmQhi) + static_cast<uint32_t>(c * kSteps + k) * 8u;
           const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 32u;
-          tc_mma_f16_ts(kTmS, a, b + (off >> 4), kIdesc, (c | t | k) != 0 ? 1u : 0u, one);
+          const uint32_t add = (t | k) != 0 ? 1u : acc;
+          if constexpr (Cfg::kQLoSmem) {
+            if (t == 1) {
+              tc_mma_f16_ss(d, lo_base + static_cast<uint32_t>(c * kTileRows * 8 + k * 2),
+                            b + (off >> 4), kIdesc, add, one);
+              continue;
+            }
+          }
+          const uint32_t a = (t == 1 ? Cfg::kTmQlo : Cfg::kTmQhi) +
+                             static_cast<uint32_t>(c * kSteps + k) * 8u;
+          tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, add, one);
         }
       }
+      acc = 1;
       if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
-      if (c == Cfg::kNC - 1) tc_commit(&sh.s_full, one);
-      there = __all_sync(0xFFFFFFFFu, next);
+      if (c == Cfg::kNC - 1) tc_commit(&sh.s_full[buf.stage], one);
     }
+    buf.next();
   }
   if (!ok && one) atomicOr(err, kErrAttMma);
   tc_commit(&sh.done[0], one);     // arrives when every MMA above has completed
@@ -287,42 +318,45 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
   const uint32_t base = sw128_lo(smem_addr(v_ring));
   RingAt<Cfg::kStages> at;
   RingAt<2> buf;
-  bool ok = true, there = false;       // there: unit and accumulator seen to be ready
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-  };
+  RingAt<Cfg::kBufs> pb;
+  bool ok = true;
   for (int j = 0; j < n && ok; ++j) {
 #pragma unroll 1
     for (int c = 0; c < Cfg::kNC; ++c) {
-      if (!there) {
-        if (!(Cfg::kWhole && c > 0)) wait(&sh.v_full[at.stage], at.phase);
-        wait(&sh.o_free[buf.stage], buf.phase ^ 1u);   // the first use of each passes
-      }
-      if (c == 0) wait(&sh.p_ready, static_cast<uint32_t>(j) & 1u);   // the last to come
+      const bool unit = !(Cfg::kWhole && c > 0), tile = c == 0;
+      uint64_t* const v_full = &sh.v_full[at.stage];
+      uint64_t* const o_free = &sh.o_free[buf.stage];       // the first use of each passes
+      uint64_t* const p_ready = &sh.p_ready[pb.stage];
+      const bool there = (!unit || mbar_test(v_full, at.phase)) &
+                         mbar_test(o_free, buf.phase ^ 1u) &
+                         (!tile || mbar_test(p_ready, pb.phase));
+      if (!__all_sync(0xFFFFFFFFu, there))
+        ok = __all_sync(0xFFFFFFFFu, (!unit || mbar_wait(v_full, at.phase)) &&
+                                         mbar_wait(o_free, buf.phase ^ 1u) &&
+                                         (!tile || mbar_wait(p_ready, pb.phase)));
       tc_fence_after();
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
-      const uint32_t d = kTmO + static_cast<uint32_t>(buf.stage) * 64u;
+      const uint32_t d = Cfg::kTmO + static_cast<uint32_t>(buf.stage) * 64u;
+      const uint32_t hi = Cfg::kTmP + static_cast<uint32_t>(pb.stage) * 64u, lo = hi + 32u;
       uint64_t* full = &sh.o_full[buf.stage];
       uint64_t* empty = &sh.v_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
       buf.next();
-      const bool next = ((Cfg::kWhole && c < Cfg::kNC - 1) ||
-                         mbar_test(&sh.v_full[at.stage], at.phase)) &
-                        mbar_test(&sh.o_free[buf.stage], buf.phase ^ 1u);
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k) {
-          const uint32_t a = (t == 1 ? kTmPlo : kTmPhi) + static_cast<uint32_t>(k) * 8u;
+          const uint32_t a = (t == 1 ? lo : hi) + static_cast<uint32_t>(k) * 8u;
           const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 2048u;
           tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, (t | k) != 0 ? 1u : 0u, one);
         }
       }
       tc_commit(full, one);
       if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
-      there = __all_sync(0xFFFFFFFFu, next);
+      if (Cfg::kBufs > 1 && c == Cfg::kNC - 1) tc_commit(&sh.p_free[pb.stage], one);
     }
+    pb.next();
   }
   if (!ok && one) atomicOr(err, kErrAttMma);
   tc_commit(&sh.done[1], one);
@@ -352,247 +386,108 @@ __device__ __forceinline__ void mma_load(uint64_t* full, uint64_t* empty, int n,
   if (!ok) atomicOr(err, kErrAttLoad);
 }
 
-// ------------------------------------------------------------ softmax and output
-// kSplit threads share a query row: each has its part of a tile's keys and, of
-// each chunk of head_dim, its part of the output columns.
+// ------------------------------------------------------------ rows
 template <class Cfg>
 struct RowState {
-  float o[Cfg::kNC][Cfg::kOC];
-  float m, l;              // of the whole row; l of this thread's keys until the end
+  float2 o[Cfg::kNC][Cfg::kOC / 2];
+  float m, l;              // of the whole row
   bool any_left_out;
 };
 
-// scratch: kScratch bytes that nothing else uses until q_ready, and again from the last
-// O_tile on; q: the row's head_dim values, or null (a row of zeros); vis: it sees the keys
-// below vis (relative to the first key of tile 0 of the run); all_vis: a bound
-// below which every row of the CTA sees every key.  kAhead: S(j+1) is turned into weights
-// before O_tile(j) is drained, which hides the softmax behind the MMAs; where the key
-// tiles come slower than the MMAs take them it would only hold O_tile(j), and with it
-// the V buffer, until K(j+1) is there.
-template <class Cfg, bool kCap, bool kAhead>
-__device__ __forceinline__ void mma_rows(MmaShared<Cfg>& sh, float* scratch, const float* q, int n, int vis, int all_vis, float scale, float cap,
-                                         RowState<Cfg>& st, bool& dead) {
-  constexpr int kKeys = Cfg::kKeys, kSplit = Cfg::kSplit;
+// The 128 query rows, scaled and split into tensor memory (Q lo: into q_lo, if it is in
+// shared memory), by the 8 warps that keep the output.  q: the row's head_dim values, or
+// null (a row of zeros).  A lane of its own row would touch 32 lines a load: a warp reads
+// its half of its 32 rows in runs of kRun columns, several lanes a row, and turns what
+// goes to tensor memory through its part of scratch (kScratch bytes that nothing else
+// uses until q_ready).
+template <class Cfg>
+__device__ __forceinline__ void store_q(MmaShared<Cfg>& sh, float* scratch, uint8_t* q_lo,
+                                        const float* q) {
+  constexpr int kQC = Cfg::kHd / 2, kRun = kQC < 32 ? kQC : 32, kLanes = kRun / 4;
+  constexpr int kAt = 32 / kLanes, kLoads = 32 / kAt, kRuns = kQC / kRun;
+  constexpr int kPitch = kRun / 2 + 4;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int quad = warp & 3, part = warp >> 2;
-  const int row = 32 * quad + lane;
-  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
-  auto row_sync = [&]() { bar_sync(1 + quad, 32 * kSplit); };
-  dead = false;
-  st.m = -INFINITY;
-  st.l = 0.f;
-  st.any_left_out = false;
-  float qscale;
-  // ---- Q: this thread's part of the row, scaled and split into tensor memory.  A lane
-  // of its own row would touch 32 lines a load: a warp reads its 32 rows in runs of
-  // kQRun columns, several lanes a row, and turns them through its scratch
-  {
-    constexpr int kQC = Cfg::kHd / kSplit;
-    constexpr int kQRun = kQC < 32 ? kQC : 32, kLanes = kQRun / 4, kAt = 32 / kLanes;
-    constexpr int kLoads = 32 / kAt, kRuns = kQC / kQRun, kPitch = kQRun + 4;
-    float* mine = scratch + warp * 32 * kPitch;
-    float4 v[kRuns][kLoads];
+  const int r0 = 32 * quad + lane / kLanes, at = lane % kLanes;
+  float4 v[kRuns][kLoads];
 #pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-      const float* src = reinterpret_cast<const float*>(__shfl_sync(
-          0xFFFFFFFFu, reinterpret_cast<unsigned long long>(q), k * kAt + lane / kLanes));
+  for (int k = 0; k < kLoads; ++k) {
+    const float* src = reinterpret_cast<const float*>(__shfl_sync(
+        0xFFFFFFFFu, reinterpret_cast<unsigned long long>(q), k * kAt + lane / kLanes));
 #pragma unroll
-      for (int r = 0; r < kRuns; ++r) {
-        v[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src)
-          v[r][k] = *reinterpret_cast<const float4*>(src + part * kQC + r * kQRun +
-                                                     (lane % kLanes) * 4);
-      }
+    for (int r = 0; r < kRuns; ++r) {
+      v[r][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (src) v[r][k] = *reinterpret_cast<const float4*>(src + part * kQC + r * kRun + at * 4);
     }
-    float x[kQC];
+  }
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
     float a = 0.f;
 #pragma unroll
     for (int r = 0; r < kRuns; ++r) {
-      __syncwarp();
+      const float4 y = v[r][k];
+      const float o[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k)
-        *reinterpret_cast<float4*>(mine + (k * kAt + lane / kLanes) * kPitch + (lane % kLanes) * 4) =
-            v[r][k];
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < kQRun; i += 4) {
-        const float4 y = *reinterpret_cast<const float4*>(mine + lane * kPitch + i);
-        float* o = x + r * kQRun + i;
-        o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
-      }
+      for (int c = 0; c < 4; ++c)
+        if (finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
     }
-    sh.xmax[1][part][row] = a;
-    row_sync();
 #pragma unroll
-    for (int c = 0; c < kSplit; ++c) a = fmaxf(a, sh.xmax[1][c][row]);
-    const int e = split_exp(a);
-    const float sc = exp2i(e);
-    qscale = exp2i(-e);
-    constexpr int kStep = kQC < 16 ? kQC : 16;
-#pragma unroll
-    for (int i = 0; i < kQC; i += kStep) {
-      uint32_t hi[8], lo[8];
-#pragma unroll
-      for (int c = 0; c < kStep / 2; ++c)
-        split_f16x2(x[i + 2 * c] * sc, x[i + 2 * c + 1] * sc, hi[c], lo[c]);
-      const uint32_t col = static_cast<uint32_t>((part * kQC + i) / 2);
-      if constexpr (kStep == 16) {
-        tc_st8(lanes + kTmQhi + col, hi);
-        tc_st8(lanes + kTmQlo + col, lo);
-      } else {
-        tc_st4(lanes + kTmQhi + col, hi[0], hi[1], hi[2], hi[3]);
-        tc_st4(lanes + kTmQlo + col, lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-    tc_wait_st();
-    fence_proxy_async_smem();      // the scratch is overwritten by copies next
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_ready);
+    for (int o = kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    if (at == 0) sh.qmax[part][r0 + k * kAt] = a;
   }
+  bar_sync(1 + quad, 64);
+  float sc[kLoads];
 #pragma unroll
-  for (int c = 0; c < Cfg::kNC; ++c)
+  for (int k = 0; k < kLoads; ++k)
+    sc[k] = exp2i(split_exp(fmaxf(sh.qmax[0][r0 + k * kAt], sh.qmax[1][r0 + k * kAt])));
+  uint32_t* mine = reinterpret_cast<uint32_t*>(scratch) + warp * 32 * kPitch;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
 #pragma unroll
-    for (int i = 0; i < Cfg::kOC; ++i) st.o[c][i] = 0.f;
-  const float rowf = kCap ? qscale * (scale / cap) : qscale * scale * kLog2e;
-  const uint32_t t_o = lanes + kTmO + static_cast<uint32_t>(part * Cfg::kOC);
-  float alpha = 1.f, vs = 1.f, alpha_next = 1.f;
-  uint32_t hi[kKeys / 2], lo[kKeys / 2];
-  // waits unless an earlier mbar_test saw the phase over
-  auto wait = [&](uint64_t* bar, uint32_t parity, bool seen) {
-    if (!__all_sync(0xFFFFFFFFu, seen) && !dead)
-      dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
-  };
-  RingAt<2> buf;
-  bool s_seen = false, o_seen = false;
-  // S(j) -> the weights of tile j, split, in registers
-  auto weights = [&](int j) {
-    const uint32_t ph = static_cast<uint32_t>(j) & 1u;
-    const uint32_t mph = static_cast<uint32_t>(j >> 1) & 1u;
-    if (!__all_sync(0xFFFFFFFFu, s_seen) && !dead)
-      dead = !__all_sync(0xFFFFFFFFu,
-                         mbar_wait(&sh.meta_full[ph], mph) && mbar_wait(&sh.s_full, ph));
-    tc_fence_after();
-    float x[kKeys];
-    {
-      uint32_t v[kKeys];
-      tc_ld<kKeys>(lanes + kTmS + static_cast<uint32_t>(kKeys * part), v);
-      tc_wait_ld();
-      tc_fence_before();
+  for (int r = 0; r < kRuns; ++r) {
+    uint2 lo[kLoads];
+#pragma unroll
+    for (int t = 0; t < (Cfg::kQLoSmem ? 1 : 2); ++t) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.s_free);
-      const float4* ks = reinterpret_cast<const float4*>(sh.meta[ph].kscale + kKeys * part);
 #pragma unroll
-      for (int i = 0; i < kKeys / 4; ++i) {
-        const float4 f = ks[i];
-        x[4 * i] = __uint_as_float(v[4 * i]) * (f.x * rowf);
-        x[4 * i + 1] = __uint_as_float(v[4 * i + 1]) * (f.y * rowf);
-        x[4 * i + 2] = __uint_as_float(v[4 * i + 2]) * (f.z * rowf);
-        x[4 * i + 3] = __uint_as_float(v[4 * i + 3]) * (f.w * rowf);
+      for (int k = 0; k < kLoads; ++k) {
+        uint2 hi;
+        if (t == 0) {
+          const float4 y = v[r][k];
+          split_f16x2(y.x * sc[k], y.y * sc[k], hi.x, lo[k].x);
+          split_f16x2(y.z * sc[k], y.w * sc[k], hi.y, lo[k].y);
+        }
+        *reinterpret_cast<uint2*>(mine + (k * kAt + lane / kLanes) * kPitch + at * 2) =
+            t == 0 ? hi : lo[k];
+        if constexpr (Cfg::kQLoSmem) {
+          const uint32_t col = static_cast<uint32_t>(part * kQC + r * kRun + at * 4);
+          *reinterpret_cast<uint2*>(
+              q_lo + (col / 64) * (kTileRows * 128) +
+              sw128_off(static_cast<uint32_t>(r0 + k * kAt), (col % 64) / 8) + (col % 8) * 2) =
+              lo[k];
+        }
       }
-    }
-    if constexpr (kCap) tanh_scaled<kKeys>(x, cap * kLog2e);
-    if ((j + 1) * kTileKeys > all_vis) {
-      const int left = vis - j * kTileKeys - kKeys * part;    // of this thread's keys, how many
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i >= left) x[i] = -INFINITY;                      // a select: nothing is multiplied
-    }
-    float mx = x[0];
-#pragma unroll
-    for (int i = 1; i < kKeys; ++i) mx = fmaxf(mx, x[i]);
-    sh.xmax[ph][part][row] = mx;
-    row_sync();
-    // what was stored came of the scales: they have been read
-    if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
-#pragma unroll
-    for (int c = 0; c < kSplit; ++c) mx = fmaxf(mx, sh.xmax[ph][c][row]);
-    const float mn = fmaxf(st.m, mx);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    alpha_next = ex2(st.m - base);
-    st.m = mn;
-    const float sub = base - static_cast<float>(kPShift);
-    o_seen = mbar_test(&sh.o_full[buf.stage], buf.phase);   // the chunk drained next
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kKeys / 2; ++i) {
-      const float a = ex2(x[2 * i] - sub), b = ex2(x[2 * i + 1] - sub);
-      sum[i & 3] += a + b;
-      split_f16x2(a, b, hi[i], lo[i]);
-    }
-    st.l = fmaf(st.l, alpha_next, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-  };
-  auto store_p = [&](int j) {
-    // S of the tile after next, meanwhile
-    const uint32_t ph = static_cast<uint32_t>(j + 1) & 1u;
-    s_seen = mbar_test(&sh.meta_full[ph], static_cast<uint32_t>((j + 1) >> 1) & 1u) &
-             mbar_test(&sh.s_full, ph);
-    tc_st<kKeys / 2>(lanes + kTmPhi + static_cast<uint32_t>(kKeys / 2 * part), hi);
-    tc_st<kKeys / 2>(lanes + kTmPlo + static_cast<uint32_t>(kKeys / 2 * part), lo);
-    tc_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.p_ready);
-  };
-  // one copy of each step: the code of a tile is read anew for every tile, and two
-  // copies of it do not stay in the instruction caches
-#pragma unroll 1
-  for (int j = kAhead ? -1 : 0; j < n; ++j) {
-    if constexpr (kAhead) {
-      alpha = alpha_next;
-      if (j + 1 < n) weights(j + 1);
-    } else {
-      weights(j);
-      alpha = alpha_next;
-      store_p(j);
-    }
-    if (j >= 0) {
-      const uint32_t ph = static_cast<uint32_t>(j) & 1u;
-      if (!dead)
-        dead = !__all_sync(0xFFFFFFFFu,
-                           mbar_wait(&sh.vmeta_full[ph], static_cast<uint32_t>(j >> 1) & 1u));
-      vs = sh.meta[ph].vscale;
-      const bool left = (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]) != 0;
-      // the arrival hangs on the values read: loads that nothing has used yet may be
-      // scheduled behind it (vs is a power of two; left is the same in all lanes)
-      const uint32_t lefts = __ballot_sync(0xFFFFFFFFu, left && vs > 0.f);
-      st.any_left_out = st.any_left_out || lefts;
-      if (lane == 0 && (vs > 0.f || lefts)) mbar_arrive(&sh.vmeta_free[ph]);
-#pragma unroll
-    for (int c = 0; c < Cfg::kNC; ++c) {
-      wait(&sh.o_full[buf.stage], buf.phase, o_seen);
-      tc_fence_after();
-      uint32_t v[Cfg::kOC];
-      tc_ld<Cfg::kOC>(t_o + static_cast<uint32_t>(buf.stage) * 64u, v);
-      uint64_t* free_bar = &sh.o_free[buf.stage];
-      buf.next();
-      o_seen = c + 1 < Cfg::kNC && mbar_test(&sh.o_full[buf.stage], buf.phase);
-      tc_wait_ld();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(free_bar);
+      uint32_t w[kRun / 2];
 #pragma unroll
-      for (int i = 0; i < Cfg::kOC; i += 2) {
-        float a, b;
-        mul2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), vs, vs);
-        scale_add2(st.o[c][i], st.o[c][i + 1], alpha, a, b);
+      for (int i = 0; i < kRun / 2; i += 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(mine + lane * kPitch + i);
+        w[i] = y.x; w[i + 1] = y.y; w[i + 2] = y.z; w[i + 3] = y.w;
       }
+      tc_st<kRun / 2>(lanes + (t == 0 ? Cfg::kTmQhi : Cfg::kTmQlo) +
+                          static_cast<uint32_t>((part * kQC + r * kRun) / 2),
+                      w);
     }
-    }
-    if constexpr (kAhead)
-      if (j + 1 < n) store_p(j + 1);    // P(j) has been multiplied by now
   }
-  // the row's whole sum
-  row_sync();
-  sh.xmax[0][part][row] = st.l;
-  row_sync();
-  float l = 0.f;
-#pragma unroll
-  for (int c = 0; c < kSplit; ++c) l += sh.xmax[0][c][row];
-  st.l = l;
+  tc_wait_st();
+  fence_proxy_async_smem();      // Q lo is read, and the scratch overwritten, by that proxy
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.q_ready);
+}
+// 2^-e of a row's split, once q_ready has been waited for (or by store_q's warps)
+template <class Cfg>
+__device__ __forceinline__ float q_unscale(const MmaShared<Cfg>& sh, int row) {
+  return exp2i(-split_exp(fmaxf(sh.qmax[0][row], sh.qmax[1][row])));
 }
 
 // A key left out of its tile (see the head of this file): its weight from the
@@ -611,8 +506,10 @@ __device__ __forceinline__ void add_left_out(RowState<Cfg>& st, const float* q, 
 #pragma unroll
   for (int c = 0; c < Cfg::kNC; ++c)
 #pragma unroll
-    for (int i = 0; i < Cfg::kOC; ++i)
-      st.o[c][i] = fmaf(p, v[c * Cfg::kHC + part * Cfg::kOC + i], st.o[c][i]);
+    for (int i = 0; i < Cfg::kOC; i += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(v + c * Cfg::kHC + part * Cfg::kOC + i);
+      st.o[c][i / 2] = __ffma2_rn(make_float2(p, p), x, st.o[c][i / 2]);
+    }
 }
 
 // f * o into the rows at dst (null: not stored), turned through the warp's scratch so
@@ -630,7 +527,8 @@ __device__ __forceinline__ void store_rows(const RowState<Cfg>& st, float* scrat
 #pragma unroll
     for (int i = 0; i < Cfg::kOC; i += 4)
       *reinterpret_cast<float4*>(mine + lane * kPitch + i) =
-          make_float4(st.o[c][i] * f, st.o[c][i + 1] * f, st.o[c][i + 2] * f, st.o[c][i + 3] * f);
+          make_float4(st.o[c][i / 2].x * f, st.o[c][i / 2].y * f, st.o[c][i / 2 + 1].x * f,
+                      st.o[c][i / 2 + 1].y * f);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 32 / kAt; ++k) {
@@ -655,12 +553,10 @@ __device__ __forceinline__ void store_split_at(const float (&x)[Cfg::kHd / 32], 
   if constexpr (kPL >= 4) {
 #pragma unroll
     for (int i = 0; i < kPL; i += 4) {
-      float a, b, c, d;
-      mul2(a, b, x[i], x[i + 1], sc, sc);
-      mul2(c, d, x[i + 2], x[i + 3], sc, sc);
+      const float2 f = make_float2(sc, sc);
       uint2 hi, lo;
-      split_f16x2(a, b, hi.x, lo.x);
-      split_f16x2(c, d, hi.y, lo.y);
+      split2(__fmul2_rn(make_float2(x[i], x[i + 1]), f), hi.x, lo.x);
+      split2(__fmul2_rn(make_float2(x[i + 2], x[i + 3]), f), hi.y, lo.y);
       uint8_t* u = at + (i / 4) * 2 * Cfg::kUnit;
       *reinterpret_cast<uint2*>(u) = hi;
       *reinterpret_cast<uint2*>(u + Cfg::kPart) = lo;

@@ -63,8 +63,8 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
 // one vote checks; the others are rare: such a key gets a scale of its own, such a
 // value row is left out of the tile and added at the end in f32.
 template <int kHd>
-struct PrefixCfg : MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true> {
-  using Base = MmaCfg<kHd, 2, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true>;
+struct PrefixCfg : MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1> {
+  using Base = MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1>;
   static constexpr int kDepth = kHd > 128 ? 1 : kHd > 64 ? 2 : 4;   // tiles of a ring
   static constexpr int kConvWarps = 8;
   static constexpr int kConv = Base::kRowsWarps + 4;        // first converter warp
@@ -87,14 +87,6 @@ struct PrefixShared {
 
 // 640 threads, 96 registers each at launch; per scheduler 2 softmax warps at 160, a
 // helper at 40 and 2 converters at 56: 2 x 160 + 40 + 2 x 56 = 472 of 5 x 96.
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
 
 template <int kHd>
 __device__ __forceinline__ void prefix_load(PrefixShared<kHd>& sh, uint8_t* staging,
@@ -256,6 +248,157 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
   if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttLoad);
 }
 
+// Softmax and output of a row's half: two threads share a query row, each has half of a
+// tile's keys and, of each chunk of head_dim, half of the output columns.
+template <class Cfg, bool kCap>
+__device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, int n, int keys, float scale,
+                                            float cap, RowState<Cfg>& st, bool& dead) {
+  constexpr int kKeys = kTileKeys / 2;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int quad = warp & 3, part = warp >> 2;
+  const int row = 32 * quad + lane;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+  auto row_sync = [&]() { bar_sync(1 + quad, 64); };
+  dead = false;
+  st.m = -INFINITY;
+  st.l = 0.f;
+  st.any_left_out = false;
+  const float qscale = q_unscale(sh, row);
+#pragma unroll
+  for (int c = 0; c < Cfg::kNC; ++c)
+#pragma unroll
+    for (int i = 0; i < Cfg::kOC / 2; ++i) st.o[c][i] = make_float2(0.f, 0.f);
+  const float rowf = kCap ? qscale * (scale / cap) : qscale * scale * kLog2e;
+  const uint32_t t_o = lanes + Cfg::kTmO + static_cast<uint32_t>(part * Cfg::kOC);
+  float alpha = 1.f, vs = 1.f;
+  uint32_t hi[kKeys / 2], lo[kKeys / 2];
+  // waits unless an earlier mbar_test saw the phase over
+  auto wait = [&](uint64_t* bar, uint32_t parity, bool seen) {
+    if (!__all_sync(0xFFFFFFFFu, seen) && !dead)
+      dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  RingAt<2> buf;
+  bool s_seen = false, o_seen = false;
+  // S(j) -> the weights of tile j, split, in registers
+  auto weights = [&](int j) {
+    const uint32_t ph = static_cast<uint32_t>(j) & 1u;
+    const uint32_t mph = static_cast<uint32_t>(j >> 1) & 1u;
+    if (!__all_sync(0xFFFFFFFFu, s_seen) && !dead)
+      dead = !__all_sync(0xFFFFFFFFu,
+                         mbar_wait(&sh.meta_full[ph], mph) && mbar_wait(&sh.s_full[0], ph));
+    tc_fence_after();
+    float x[kKeys];
+    {
+      uint32_t v[kKeys];
+      tc_ld<kKeys>(lanes + Cfg::kTmS + static_cast<uint32_t>(kKeys * part), v);
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[0]);
+      const float4* ks = reinterpret_cast<const float4*>(sh.meta[ph].kscale + kKeys * part);
+#pragma unroll
+      for (int i = 0; i < kKeys / 4; ++i) {
+        const float4 f = ks[i];
+        const float2 rf = make_float2(rowf, rowf);
+        const float2 a =
+            __fmul2_rn(bits2(v[4 * i], v[4 * i + 1]), __fmul2_rn(make_float2(f.x, f.y), rf));
+        const float2 b =
+            __fmul2_rn(bits2(v[4 * i + 2], v[4 * i + 3]), __fmul2_rn(make_float2(f.z, f.w), rf));
+        x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+      }
+    }
+    if constexpr (kCap) tanh_scaled<kKeys>(x, cap * kLog2e);
+    if ((j + 1) * kTileKeys > keys) {
+      const int left = keys - j * kTileKeys - kKeys * part;    // of this thread's keys, how many
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (i >= left) x[i] = -INFINITY;                      // a select: nothing is multiplied
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int i = 1; i < kKeys; ++i) mx = fmaxf(mx, x[i]);
+    sh.x[ph][part][row] = mx;
+    row_sync();
+    // what was stored came of the scales: they have been read
+    if (lane == 0) mbar_arrive(&sh.meta_free[ph]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) mx = fmaxf(mx, sh.x[ph][c][row]);
+    const float mn = fmaxf(st.m, mx);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    alpha = ex2(st.m - base);
+    st.m = mn;
+    const float sub = static_cast<float>(kPShift) - base;
+    o_seen = mbar_test(&sh.o_full[buf.stage], buf.phase);   // the chunk drained next
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kKeys / 2; ++i) {
+      float2 a = __fadd2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(sub, sub));
+      a.x = ex2(a.x);
+      a.y = ex2(a.y);
+      sum = __fadd2_rn(sum, a);
+      split2(a, hi[i], lo[i]);
+    }
+    st.l = fmaf(st.l, alpha, sum.x + sum.y);
+  };
+  auto store_p = [&](int j) {
+    // S of the tile after next, meanwhile
+    const uint32_t ph = static_cast<uint32_t>(j + 1) & 1u;
+    s_seen = mbar_test(&sh.meta_full[ph], static_cast<uint32_t>((j + 1) >> 1) & 1u) &
+             mbar_test(&sh.s_full[0], ph);
+    tc_st<kKeys / 2>(lanes + Cfg::kTmP + static_cast<uint32_t>(kKeys / 2 * part), hi);
+    tc_st<kKeys / 2>(lanes + Cfg::kTmP + 32u + static_cast<uint32_t>(kKeys / 2 * part), lo);
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.p_ready[0]);
+  };
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    weights(j);
+    store_p(j);
+    {
+      const uint32_t ph = static_cast<uint32_t>(j) & 1u;
+      if (!dead)
+        dead = !__all_sync(0xFFFFFFFFu,
+                           mbar_wait(&sh.vmeta_full[ph], static_cast<uint32_t>(j >> 1) & 1u));
+      vs = sh.meta[ph].vscale;
+      const bool left = (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]) != 0;
+      // the arrival hangs on the values read: loads that nothing has used yet may be
+      // scheduled behind it (vs is a power of two; left is the same in all lanes)
+      const uint32_t lefts = __ballot_sync(0xFFFFFFFFu, left && vs > 0.f);
+      st.any_left_out = st.any_left_out || lefts;
+      if (lane == 0 && (vs > 0.f || lefts)) mbar_arrive(&sh.vmeta_free[ph]);
+#pragma unroll
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      wait(&sh.o_full[buf.stage], buf.phase, o_seen);
+      tc_fence_after();
+      uint32_t v[Cfg::kOC];
+      tc_ld<Cfg::kOC>(t_o + static_cast<uint32_t>(buf.stage) * 64u, v);
+      uint64_t* free_bar = &sh.o_free[buf.stage];
+      buf.next();
+      o_seen = c + 1 < Cfg::kNC && mbar_test(&sh.o_full[buf.stage], buf.phase);
+      tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(free_bar);
+#pragma unroll
+      for (int i = 0; i < Cfg::kOC; i += 2) {
+        st.o[c][i / 2] = __ffma2_rn(st.o[c][i / 2], make_float2(alpha, alpha),
+                                    __fmul2_rn(bits2(v[i], v[i + 1]), make_float2(vs, vs)));
+      }
+    }
+    }
+  }
+  // the row's whole sum
+  row_sync();
+  sh.x[0][part][row] = st.l;
+  row_sync();
+  float l = 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) l += sh.x[0][c][row];
+  st.l = l;
+}
+
 // grid (pieces * row tiles, n_kv)
 template <int kHd, bool kCap>
 __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
@@ -297,7 +440,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
     regs_dec<40>();
     if (warp == Cfg::kLoadK && lane == 0)
       prefix_load<kHd>(sh, staging, p.kp + at, p.vp + at, keys, n);
-    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh.mma, k_ring, n, &g_err_prefix);
+    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh.mma, k_ring, nullptr, n, &g_err_prefix);
     if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh.mma, v_ring, n, &g_err_prefix);
   } else {
     regs_inc<160>();
@@ -310,7 +453,8 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
     RowState<Cfg> st;
     bool dead;
     float* scratch = reinterpret_cast<float*>(v_ring);
-    mma_rows<Cfg, kCap, false>(sh.mma, scratch, alive ? q : nullptr, n, keys, keys, p.scale, p.cap, st, dead);
+    store_q<Cfg>(sh.mma, scratch, nullptr, alive ? q : nullptr);
+    prefix_rows<Cfg, kCap>(sh.mma, n, keys, p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttRows);
     if (st.any_left_out && alive) {
       for (int t = 0; t < keys; ++t)

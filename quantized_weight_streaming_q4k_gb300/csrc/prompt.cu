@@ -181,8 +181,202 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ tensor cores
+// 20 warps: 0..7 keep the output, 8..11 and 12..15 turn the scores of the even and of the
+// odd tiles into weights, 16..19 load and issue (attend_mma.cuh).  Each has its own warps
+// because each is a chain of waits, tensor memory accesses and exchanges: when the same
+// warps did both in turn, a tile took 4750 cycles (2830 at head_dim 128; 3590 with a
+// softcap) where its MMAs take 3330 (1540).  S and P have two buffers, so that Q K(j+2)^T
+// and P V(j+1) do not wait for one tile's softmax.  8192 positions, 8 q / 4 kv heads of 256:
+// 616 -> 525 us; 16 q / 4 kv heads of 128: 619 -> 572 us, with a softcap 785 -> 683 us (the
+// MMAs at the measured rate: 428 us).  Bound by the MMAs and the waits between them at
+// head_dim 256, and by the softmax's instructions below (1400 a scheduler and tile).
 template <int kHd>
-using PromptCfg = MmaCfg<kHd, 2>;
+struct PromptCfg : MmaCfg<kHd, (kHd > 128 ? 1 : 0), false, 2> {
+  static constexpr int kThreads = 32 * 20;
+  static constexpr uint32_t kSmem = MmaCfg<kHd, (kHd > 128 ? 1 : 0), false, 2>::kRing +
+                                    MmaCfg<kHd, (kHd > 128 ? 1 : 0), false, 2>::kQLoBytes;
+};
+// 96 registers a thread at launch; per scheduler 2 output warps, 2 softmax warps and a
+// helper: 2 x 160 + 2 x 64 + 32, or 2 x 104 + 2 x 104 + 64, of 5 x 96.
+template <int kHd>
+constexpr int kRegsOut = kHd > 128 ? 160 : 104;
+template <int kHd>
+constexpr int kRegsSoft = kHd > 128 ? 64 : 104;
+template <int kHd>
+constexpr int kRegsHelp = kHd > 128 ? 32 : 64;
+
+// Both phases are over, or dead: asked together, as a wait costs some 200 cycles even so.
+__device__ __forceinline__ void wait2(uint64_t* a, uint32_t a_par, uint64_t* b, uint32_t b_par,
+                                      bool& dead) {
+  if (!__all_sync(0xFFFFFFFFu, mbar_test(a, a_par) & mbar_test(b, b_par)) && !dead)
+    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(a, a_par) && mbar_wait(b, b_par));
+}
+
+// The weights of the tiles first, first + 2, ... of a row: a thread has the whole row, so
+// nothing is exchanged.  The scaled scores go back to S for the second pass, because 64 of
+// them and the packed weights do not fit the registers.  Each of the two groups of warps
+// has its own running maximum; the output warps bring the tiles to one.  vis: the row sees
+// the keys below vis; all_vis: below this one, every row of the CTA does.
+template <class Cfg, bool kCap>
+__device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int n, int vis,
+                                             int all_vis, float scale, float cap) {
+  const int lane = static_cast<int>(threadIdx.x & 31), quad = (threadIdx.x >> 5) & 3;
+  const int row = 32 * quad + lane;
+  const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
+  const uint32_t t_s = lanes + Cfg::kTmS + static_cast<uint32_t>(first) * 64u;
+  const uint32_t t_p = lanes + Cfg::kTmP + static_cast<uint32_t>(first) * 64u;
+  float m = -INFINITY, l = 0.f;
+  bool dead = false;
+  constexpr int kRun = Cfg::kHd > 128 ? 16 : 32;     // keys at a time, as registers allow
+  dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
+  const float qs = q_unscale(sh, row);
+  const float rowf = kCap ? qs * (scale / cap) : qs * scale * kLog2e;
+  uint32_t ph = 0;
+#pragma unroll 1
+  for (int j = first; j < n; j += 2, ph ^= 1u) {
+    const bool masked = (j + 1) * kTileKeys > all_vis;
+    const int left = vis - j * kTileKeys;       // of the tile's keys, how many the row sees
+    const int slot = j % Cfg::kMetas;
+    const float* ks = sh.meta[slot].kscale;
+    wait2(&sh.meta_full[slot], static_cast<uint32_t>(j / Cfg::kMetas) & 1u, &sh.s_full[first], ph,
+          dead);
+    tc_fence_after();
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < kTileKeys; h += kRun) {
+      uint32_t v[kRun];
+      float x[kRun];
+      tc_ld<kRun>(t_s + static_cast<uint32_t>(h), v);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kRun; i += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(ks + h + i);
+        const float2 f = make_float2(rowf, rowf);
+        const float2 a = __fmul2_rn(bits2(v[i], v[i + 1]), __fmul2_rn(make_float2(k.x, k.y), f));
+        const float2 b =
+            __fmul2_rn(bits2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(k.z, k.w), f));
+        x[i] = a.x; x[i + 1] = a.y; x[i + 2] = b.x; x[i + 3] = b.y;
+      }
+      if constexpr (kCap) tanh_scaled<kRun>(x, cap * kLog2e);
+      if (masked) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+          if (h + i >= left) x[i] = -INFINITY;     // a select: nothing is multiplied
+      }
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        mx = fmaxf(mx, x[i]);
+        v[i] = __float_as_uint(x[i]);
+      }
+      tc_st<kRun>(t_s + static_cast<uint32_t>(h), v);
+    }
+    tc_wait_st();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.meta_free[slot]);     // the scales are in what was stored
+    const float mn = fmaxf(m, mx);
+    const float base = mn == -INFINITY ? 0.f : mn;
+    l *= ex2(m - base);
+    m = mn;
+    const float sub = static_cast<float>(kPShift) - base;
+    // the buffer's last tile has been multiplied, and its maximum read
+    wait2(&sh.p_free[first], ph ^ 1u, &sh.m_free[first], ph ^ 1u, dead);
+    tc_fence_after();
+    sh.x[0][first][row] = m;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int h = 0; h < kTileKeys; h += kRun) {
+      uint32_t v[kRun], hi[kRun / 2], lo[kRun / 2];
+      tc_ld<kRun>(t_s + static_cast<uint32_t>(h), v);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kRun; i += 2) {
+        float2 a = __fadd2_rn(bits2(v[i], v[i + 1]), make_float2(sub, sub));
+        a.x = ex2(a.x);
+        a.y = ex2(a.y);
+        sum = __fadd2_rn(sum, a);
+        split2(a, hi[i / 2], lo[i / 2]);
+      }
+      tc_st<kRun / 2>(t_p + static_cast<uint32_t>(h / 2), hi);
+      tc_st<kRun / 2>(t_p + 32u + static_cast<uint32_t>(h / 2), lo);
+    }
+    l += sum.x + sum.y;
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.p_ready[first]);
+      mbar_arrive(&sh.s_free[first]);
+    }
+  }
+  sh.x[0][first][row] = m;
+  sh.x[1][first][row] = l;
+  return dead;
+}
+
+// O = sum over tiles of 2^(m_j - m) O_tile(j), in registers: a thread has half a row.
+template <class Cfg>
+__device__ __forceinline__ bool tile_sums(MmaShared<Cfg>& sh, int n, RowState<Cfg>& st) {
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  const int quad = warp & 3, part = warp >> 2, row = 32 * quad + lane;
+  const uint32_t t_o = (static_cast<uint32_t>(32 * quad) << 16) + Cfg::kTmO +
+                       static_cast<uint32_t>(part * Cfg::kOC);
+  st.m = -INFINITY;
+  st.any_left_out = false;
+#pragma unroll
+  for (int c = 0; c < Cfg::kNC; ++c)
+#pragma unroll
+    for (int i = 0; i < Cfg::kOC / 2; ++i) st.o[c][i] = make_float2(0.f, 0.f);
+  bool dead = false;
+  const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+  };
+  RingAt<2> tile, buf;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int b = tile.stage, slot = j % Cfg::kMetas;
+    wait2(&sh.vmeta_full[slot], static_cast<uint32_t>(j / Cfg::kMetas) & 1u, &sh.p_ready[b],
+          tile.phase, dead);
+    tile.next();
+    const float mj = sh.x[0][b][row], vs = sh.meta[slot].vscale;
+    const bool left = (sh.meta[slot].left_out[0] | sh.meta[slot].left_out[1]) != 0;
+    const float mn = fmaxf(st.m, mj), base = mn == -INFINITY ? 0.f : mn;
+    const float alpha = ex2(st.m - base), beta = ex2(mj - base) * vs;
+    st.m = mn;
+    // the arrivals hang on the values read: loads that nothing has used yet may be
+    // scheduled behind them (the vote is true in every lane: vs is a power of two)
+    const uint32_t lefts = __ballot_sync(0xFFFFFFFFu, left && vs > 0.f);
+    const bool read = __all_sync(0xFFFFFFFFu, !(beta < 0.f)) && (vs > 0.f || lefts);
+    st.any_left_out = st.any_left_out || lefts;
+    if (lane == 0 && read) {
+      mbar_arrive(&sh.vmeta_free[slot]);
+      mbar_arrive(&sh.m_free[b]);
+    }
+#pragma unroll
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      wait(&sh.o_full[buf.stage], buf.phase);
+      tc_fence_after();
+#pragma unroll
+      for (int h = 0; h < Cfg::kOC; h += 16) {
+        uint32_t v[16];
+        tc_ld<16>(t_o + static_cast<uint32_t>(buf.stage) * 64u + static_cast<uint32_t>(h), v);
+        tc_wait_ld();
+        if (h + 16 == Cfg::kOC) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_free[buf.stage]);
+          buf.next();
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float2& o = st.o[c][(h + i) / 2];
+          o = __ffma2_rn(o, make_float2(alpha, alpha),
+                         __fmul2_rn(bits2(v[i], v[i + 1]), make_float2(beta, beta)));
+        }
+      }
+    }
+  }
+  return dead;
+}
 
 // Key tiles of every sequence and kv head, split and laid out once (they are
 // read by all of the sequence's query tiles).  grid (key tiles, n_kv).
@@ -208,7 +402,8 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   using Cfg = PromptCfg<kHd>;
   extern __shared__ uint8_t raw[];
   uint8_t* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  auto& sh = *reinterpret_cast<MmaShared<Cfg>*>(stages + Cfg::kRing);
+  uint8_t* q_lo = stages + Cfg::kRing;
+  auto& sh = *reinterpret_cast<MmaShared<Cfg>*>(stages + Cfg::kSmem);
   const int item = blockIdx.x / p.n_kv, g = blockIdx.x - item * p.n_kv;
   const PromptItem it = prompt_item(p, item);
   pdl_launch_dependents();
@@ -227,16 +422,23 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   pdl_wait();
   uint8_t* k_ring = stages;
   uint8_t* v_ring = stages + Cfg::kStages * Cfg::kUnit;
-  if (warp >= Cfg::kRowsWarps) {
-    regs_few<Cfg>();
+  // this thread's row, as output or as softmax warp
+  const int row = 32 * (warp & 3) + lane;
+  const int live = it.n_tok * p.group;
+  const int r = min(row, live - 1);
+  const int i = it.i0 + r / p.group, h = g * p.group + r % p.group;
+  const int vis = visible(i, it.n_q, it.n_k) - ka;
+  if (warp >= Cfg::kLoadK) {
+    regs_dec<kRegsHelp<kHd>>();
     const auto packed = [&](int j) { return p.packed + ((tile0 + j) * p.n_kv + g) * Cfg::kTile; };
     if (warp == Cfg::kLoadK && lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
       mma_load<Cfg>(
           sh.k_full, sh.k_empty, n,
           [&](int j) {
-            const int s = j & 1;
-            if (!mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
+            const int s = j % Cfg::kMetas;
+            if (!mbar_wait(&sh.meta_free[s], (static_cast<uint32_t>(j / Cfg::kMetas) & 1u) ^ 1u))
+              return false;
             mbar_arrive_expect_tx(&sh.meta_full[s], sizeof(TileMeta::kscale));
             bulk_copy_g2s(&sh.meta[s], p.meta + (tile0 + j) * p.n_kv + g,
                           sizeof(TileMeta::kscale), &sh.meta_full[s], pol);
@@ -256,8 +458,9 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
           [&](int j) {
             // the ring is the softmax warps' scratch until Q is stored
             if (j == 0 && !mbar_wait(&sh.q_ready, 0)) return false;
-            const int s = j & 1;
-            if (!mbar_wait(&sh.vmeta_free[s], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u)) return false;
+            const int s = j % Cfg::kMetas;
+            if (!mbar_wait(&sh.vmeta_free[s], (static_cast<uint32_t>(j / Cfg::kMetas) & 1u) ^ 1u))
+              return false;
             mbar_arrive_expect_tx(&sh.vmeta_full[s], 16);
             bulk_copy_g2s(&sh.meta[s].vscale, &p.meta[(tile0 + j) * p.n_kv + g].vscale, 16,
                           &sh.vmeta_full[s], pol);
@@ -270,23 +473,32 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
           },
           &g_err_prompt);
     }
-    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh, k_ring, n, &g_err_prompt);
+    if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh, k_ring, q_lo, n, &g_err_prompt);
     if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh, v_ring, n, &g_err_prompt);
+  } else if (warp >= Cfg::kRowsWarps) {
+    if constexpr (kHd > 128) regs_dec<kRegsSoft<kHd>>();
+    else regs_inc<kRegsSoft<kHd>>();
+    const bool dead = tile_weights<Cfg, kCap>(sh, (warp - Cfg::kRowsWarps) >> 2, n, vis,
+                                              visible(it.i0, it.n_q, it.n_k) - ka, p.scale, p.cap);
+    if (dead) sh.dead = 1;
+    bar_sync(5, 32 * 16);
   } else {
-    regs_many<Cfg>();
-    const int row = 32 * (warp & 3) + lane, part = warp >> 2;
-    const int live = it.n_tok * p.group;
+    regs_inc<kRegsOut<kHd>>();
+    const int part = warp >> 2;
     const bool alive = row < live;
-    const int r = min(row, live - 1);
-    const int i = it.i0 + r / p.group, h = g * p.group + r % p.group;
     const int64_t token = p.seqs.q0[it.s] + i;
     const float* q = p.q.data + token * p.q.token_stride + h * p.q.head_stride;
-    const int vis = visible(i, it.n_q, it.n_k) - ka;
     RowState<Cfg> st;
-    bool dead;
     float* scratch = reinterpret_cast<float*>(v_ring);
-    mma_rows<Cfg, kCap, true>(sh, scratch, alive ? q : nullptr, n, vis, visible(it.i0, it.n_q, it.n_k) - ka,
-                  p.scale, p.cap, st, dead);
+    store_q<Cfg>(sh, scratch, q_lo, alive ? q : nullptr);
+    if (tile_sums<Cfg>(sh, n, st)) sh.dead = 1;
+    bar_sync(5, 32 * 16);
+    const bool dead = *reinterpret_cast<volatile uint32_t*>(&sh.dead) != 0;
+    {
+      const float base = st.m == -INFINITY ? 0.f : st.m;
+      st.l = sh.x[1][0][row] * ex2(sh.x[0][0][row] - base) +
+             sh.x[1][1][row] * ex2(sh.x[0][1][row] - base);
+    }
     if (dead && lane == 0) atomicOr(&g_err_prompt, kErrAttRows);
     if (st.any_left_out && alive) {
       for (int j = 0; j < n; ++j) {
@@ -458,7 +670,7 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
   cudaError_t e;
   if (pl.mma) {
     using Cfg = PromptCfg<kHd>;
-    constexpr size_t kSmem = 1024 + Cfg::kRing + sizeof(MmaShared<Cfg>);
+    constexpr size_t kSmem = 1024 + Cfg::kSmem + sizeof(MmaShared<Cfg>);
     static_assert(kSmem <= 227 * 1024, "shared memory");
     if (ktiles > 0) {
       e = pdl_launch(prompt_pack_kernel<kHd>,

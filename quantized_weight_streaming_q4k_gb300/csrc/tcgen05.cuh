@@ -69,19 +69,10 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tc_ld8(uint32_t taddr, uint32_t (&v)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
-        "=r"(v[7])
-      : "r"(taddr)
-      : "memory");
-}
 template <int kN>
 __device__ __forceinline__ void tc_ld(uint32_t taddr, uint32_t (&v)[kN]) {
-  static_assert(kN == 8 || kN == 16 || kN == 32, "widths in use");
-  if constexpr (kN == 8) tc_ld8(taddr, v);
-  else if constexpr (kN == 16) tc_ld16(taddr, v);
+  static_assert(kN == 16 || kN == 32, "widths in use");
+  if constexpr (kN == 16) tc_ld16(taddr, v);
   else tc_ld32(taddr, v);
 }
 __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -93,12 +84,6 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
       "r"(v[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c,
-                                       uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-               "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
 __device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
@@ -106,11 +91,25 @@ __device__ __forceinline__ void tc_st8(uint32_t taddr, const uint32_t (&v)[8]) {
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
       : "memory");
 }
+__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 template <int kN>
 __device__ __forceinline__ void tc_st(uint32_t taddr, const uint32_t (&v)[kN]) {
-  static_assert(kN == 8 || kN == 16, "widths in use");
+  static_assert(kN == 8 || kN == 16 || kN == 32, "widths in use");
   if constexpr (kN == 8) tc_st8(taddr, v);
-  else tc_st16(taddr, v);
+  else if constexpr (kN == 16) tc_st16(taddr, v);
+  else tc_st32(taddr, v);
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -144,6 +143,19 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       "setp.ne.b32 q, %5, 0;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], d, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(kSw128Hi)
+      : "memory");
+}
+// the same with A from shared memory too, a = sw128_lo of its start
+__device__ __forceinline__ void tc_mma_f16_ss(uint32_t d_tmem, uint32_t a, uint32_t b,
+                                              uint32_t idesc, uint32_t accumulate, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 d, e;\n\t"
+      "mov.b64 e, {%1, %6};\n\t"
+      "mov.b64 d, {%2, %6};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], e, d, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(one), "n"(kSw128Hi)
       : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar, uint32_t one) {
