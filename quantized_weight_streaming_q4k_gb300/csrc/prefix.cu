@@ -409,7 +409,6 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   uint8_t* v_ring = k_ring + Cfg::kStages * Cfg::kUnit;
   uint8_t* staging = v_ring + Cfg::kStages * Cfg::kUnit;
   auto& sh = *reinterpret_cast<PrefixShared<kHd>*>(staging + Cfg::kStaging * Cfg::kRunBytes);
-  pdl_launch_dependents();
   const int piece = blockIdx.x / p.row_tiles, rt = blockIdx.x - piece * p.row_tiles;
   const int g = blockIdx.y;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -431,6 +430,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  // only now: own_part_kernel starts with this and reads what the call was given
   pdl_launch_dependents();
   const int64_t at = (static_cast<int64_t>(g) * p.max_prefix + ka) * kHd;
   if (warp >= Cfg::kConv) {
