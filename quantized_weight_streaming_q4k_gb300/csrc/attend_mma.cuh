@@ -7,10 +7,10 @@
 // a key row are each scaled by a power of two that puts their largest value in
 // [2^14, 2^15), the values of a tile by one for the whole tile; the weights
 // are at most 2^14.  So a value keeps 22 bits, or 2^-40 of the largest it
-// is scaled with.  A key whose values would spoil its tile's scale (one that is
-// not finite, or over 2^16 times the tile's smallest: such a key may be one
-// that most rows do not even see) is left out of the tile and added at the end,
-// in f32, by the rows that see it.
+// is scaled with.  A key whose values would spoil its tile's scale or be spoilt by it (one
+// that is not finite, or further than 2^16 from the tile's others, which may be keys that
+// most rows do not even see) is left out of the tile and added at the end, in f32, by the
+// rows that see it.
 //
 // Per tile of 64 keys, S = Q K^T (128 x 64) and O_tile = P V (128 x head_dim).
 // Q and P are A operands in tensor memory; K and V come through rings in shared
@@ -633,13 +633,22 @@ __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_
     }
   }
   __syncthreads();
-  // the smallest non-zero row maximum; rows above 2^16 times it stay out
+  // the rows within 2^16 of the smallest non-zero row, or within 2^16 of the largest that
+  // is finite: whichever leaves out fewer
   const float a = vmax[lane], b = vmax[lane + 32];
   float lo = fminf(a > 0.f ? a : INFINITY, b > 0.f ? b : INFINITY);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-  const float top = lo * 65536.0f;                 // infinity: only what is not finite
-  const bool out_a = !(a <= top) || a == INFINITY, out_b = !(b <= top) || b == INFINITY;
+  const float hi = warp_max(fmaxf(a == INFINITY ? 0.f : a, b == INFINITY ? 0.f : b));
+  const float top = lo * 65536.0f, low = hi * (1.0f / 65536.0f);     // top: may be infinite
+  const auto count = [](bool x, bool y) {
+    return __popc(__ballot_sync(0xFFFFFFFFu, x)) + __popc(__ballot_sync(0xFFFFFFFFu, y));
+  };
+  const bool big_a = a == INFINITY || a > top, big_b = b == INFINITY || b > top;
+  const bool few_a = a == INFINITY || (a > 0.f && a < low);
+  const bool few_b = b == INFINITY || (b > 0.f && b < low);
+  const bool large = count(big_a, big_b) <= count(few_a, few_b);      // the same in all warps
+  const bool out_a = large ? big_a : few_a, out_b = large ? big_b : few_b;
   const uint32_t ma = __ballot_sync(0xFFFFFFFFu, out_a), mb = __ballot_sync(0xFFFFFFFFu, out_b);
   const int e = split_exp(warp_max(fmaxf(out_a ? 0.f : a, out_b ? 0.f : b)));
   if (threadIdx.x == 0) {

@@ -354,6 +354,156 @@ def test_prompt_outlier_tokens():
     check_prompt(q, k, v, [0, 200], out, 0.125)
 
 
+# the same again with enough (query, key) pairs for the tensor cores (2^18)
+@pytest.mark.parametrize("nq,nkv,hd", [(1, 1, 32), (4, 4, 128), (8, 2, 64), (6, 3, 32), (16, 4, 128),
+                                       (3, 1, 256), (2, 1, 64), (4, 1, 256), (3, 1, 128)])
+@pytest.mark.parametrize("lens", [[777], [640, 1, 333], [65, 2, 900, 64]])
+def test_prompt_large_head_layouts(nq, nkv, hd, lens):
+    run_prompt(gen(60 + nq * hd), lens, nq, nkv, hd)
+
+
+@pytest.mark.parametrize("hd", [32, 128, 256])
+@pytest.mark.parametrize("cap,scale", [(50.0, 0.08), (50.0, 1.5), (1.5, 0.3), (0.05, 0.3)])
+def test_prompt_large_softcap(cap, scale, hd):
+    # scores well within the cap, about it, and far beyond
+    run_prompt(gen(61), [700, 65], 8, 4, hd, cap=cap, scale=scale)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
+def test_prompt_large_scales(scale):
+    run_prompt(gen(62), [600], 4, 2, 128, scale=scale)
+
+
+@pytest.mark.parametrize("lens,ctx", [([130], [4000]), ([512, 3], [1111, 3]), ([1, 400], [3000, 777]),
+                                      ([300], [2368])])
+def test_prompt_large_continued(lens, ctx):
+    run_prompt(gen(63), lens, 8, 4, 256, ctx=ctx)
+    run_prompt(gen(64), lens, 4, 1, 64, ctx=ctx)
+
+
+def test_prompt_large_rows_without_a_key_are_zero():
+    q, k, v, cu, out = run_prompt(gen(65), [700, 300, 129], 4, 2, 64, ctx=[520, 0, 64])
+    assert not out[:180].any() and not out[700:1000].any() and not out[1000:1065].any()
+    assert out[180:700].abs().sum(-1).min() > 0
+
+
+def test_prompt_large_many_sequences():
+    lens = [(i * 29) % 97 for i in range(300)]            # more than one launch's table
+    run_prompt(gen(66), lens, 4, 2, 64)
+
+
+def test_prompt_large_strided_views_and_rows_behind_the_end():
+    g = gen(67)
+    n, nq, nkv, hd = 900, 8, 4, 128
+    qkv = normal(g, n + 9, nq + 2 * nkv, hd)
+    q, k, v = qkv[:, :nq], qkv[:, nq:nq + nkv], qkv[:, nq + nkv:]
+    wide = torch.full((n + 9, nq + 3, hd), 5.0, device="cuda")
+    cu = [4, 370, 900]
+    out = wide[:, 1:1 + nq]
+    assert ops.prompt_attention(q, k, v, cu, 0.09, out=out) is out
+    check_prompt(q, k, v, cu, out, 0.09)
+    assert torch.all(wide[:4] == 5.0) and torch.all(wide[900:] == 5.0)
+    assert torch.all(wide[:, 0] == 5.0) and torch.all(wide[:, 1 + nq:] == 5.0)
+    kc = k.transpose(0, 1).contiguous().transpose(0, 1)
+    vc = v.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(ops.prompt_attention(q, kc, vc, cu, 0.09)[4:900], out[4:900])
+    # one key and value head for all (stride 0)
+    k1, v1 = k[:, :1].expand(-1, nkv, -1), v[:, :1].expand(-1, nkv, -1)
+    check_prompt(q, k1, v1, cu, ops.prompt_attention(q, k1, v1, cu, 0.09), 0.09)
+
+
+@pytest.mark.parametrize("hd", [32, 64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3.0e38])
+def test_prompt_large_masked_places_may_hold_anything(bad, hd):
+    g = gen(68)
+    n, nq, nkv = 1100, 4, 2
+    q, k, v = normal(g, n, nq, hd), normal(g, n, nkv, hd), normal(g, n, nkv, hd)
+    cu = [0, 450, 1000]
+    want = ops.prompt_attention(q, k, v, cu, 0.1)
+    k2, v2 = k.clone(), v.clone()
+    for t in (k2, v2):
+        t[1000:] = bad
+        t[440:450] = bad
+        t[991:1000, :, ::3] = bad
+    got = ops.prompt_attention(q, k2, v2, cu, 0.1)
+    clean = list(range(440)) + list(range(450, 991))
+    assert torch.all((got[clean] - want[clean]).abs() <= 2e-5)
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prompt_large_seen_infinities_show(bad, hd):
+    g = gen(69)
+    q, k, v = normal(g, 700, 2, hd), normal(g, 700, 1, hd), normal(g, 700, 1, hd)
+    want = ops.prompt_attention(q, k, v, [0, 700], 0.1)
+    v[333, 0, 5] = bad
+    got = ops.prompt_attention(q, k, v, [0, 700], 0.1)
+    assert not torch.isfinite(got[333:, :, 5]).any()
+    assert torch.isfinite(got[:333]).all()
+    keep = [i for i in range(hd) if i != 5]
+    assert torch.all((got[333:][..., keep] - want[333:][..., keep]).abs() <= 2e-5)
+    k[600, 0, 3] = float("nan")
+    got = ops.prompt_attention(q, k, v, [0, 700], 0.1)
+    assert torch.isnan(got[600:]).all() and torch.isfinite(got[:333]).all()
+    q[650, 0, 1] = float("nan")                            # a row's own, and no other row's
+    k[600, 0, 3] = v[333, 0, 5] = 0.0
+    got = ops.prompt_attention(q, k, v, [0, 700], 0.1)
+    assert torch.isnan(got[650, 0]).all()
+    got[650, 0] = 0.0
+    assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("hd", [32, 256])
+@pytest.mark.parametrize("mag", [1e-20, 1e-6, 1e4, 1e15])
+def test_prompt_large_magnitudes(mag, hd):
+    g = gen(70)
+    q, k, v = normal(g, 640, 4, hd), normal(g, 640, 2, hd), normal(g, 640, 2, hd)
+    s = hd ** -0.5
+    out = ops.prompt_attention(q * mag, k / mag, v * mag, [0, 640], s)
+    check_prompt(q * mag, k / mag, v * mag, [0, 640], out, s)
+
+
+def test_prompt_large_rows_of_very_different_size():
+    g = gen(71)
+    q, k, v = normal(g, 800, 4, 64), normal(g, 800, 2, 64), normal(g, 800, 2, 64)
+    k[..., 7] *= 300.0
+    q[..., 7] *= 0.01
+    k[100:110] *= 1e-6
+    v[33] *= 1e7
+    v[0:3] *= 1e-9                   # the first rows see nothing else
+    v[200:205] *= 1e-7
+    v[400:440] *= 1e8                # more than half of a tile
+    v[640:704] = 0.0
+    out = ops.prompt_attention(q, k, v, [0, 800], 0.125)
+    check_prompt(q, k, v, [0, 800], out, 0.125)
+
+
+def test_prompt_large_in_graphs_and_beside_another_call():
+    g = gen(72)
+    a = [normal(g, 700, h, 256) for h in (8, 4, 4)]
+    b = [normal(g, 900, h, 64) for h in (8, 2, 2)]
+    want = [ops.prompt_attention(*a, [0, 100, 700], 0.06), ops.prompt_attention(*b, [0, 900], 0.1, 30.0)]
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):                                    # both at once, each its workspace
+        with torch.cuda.stream(side[0]):
+            outs.append(ops.prompt_attention(*a, [0, 100, 700], 0.06))
+        outs.append(ops.prompt_attention(*b, [0, 900], 0.1, 30.0, stream=side[1]))
+    torch.cuda.synchronize()
+    for i, t in enumerate(outs):
+        assert torch.equal(t, want[i % 2]), i
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x = ops.prompt_attention(*a, [0, 100, 700], 0.06)
+        y = ops.prompt_attention(*b, [0, 900], 0.1, 30.0)
+    a[2].mul_(-2.0)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want[0] * -2.0) and torch.equal(y, want[1])
+
+
 # ------------------------------------------------------------------ prefix attention
 def check_prefix(q, kp, vp, n_prefix, kc, vc, n_ctx, scale, cap, out):
     nq, nkv = q.shape[1], kp.shape[0]
