@@ -293,10 +293,15 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *     s_j = scale * q_ih . k_j, softcap as in qws_kv_attention, out_ih = sum_j
  *     softmax(s)_j v_j, head h reading kv head h / (n_q / n_kv); a row without
  *     a key is zero.  Rows that belong to no sequence are not touched.
- *   cu_q, cu_k: host, n_seqs + 1 non-decreasing offsets from 0 up, below 2^31.
+ *   cu_q, cu_k: host, n_seqs + 1 non-decreasing offsets, 0 <= offset <= 2^30.
+ *   out overlaps none of q, k and v.
  *   ws: device, 16-byte aligned, >= qws_prompt_attention_workspace_bytes of
  *   the same arguments (0: may be NULL).  Keys that a row does not see may
  *   hold anything, infinities and NaN included.
+ *   Accuracy, here and in qws_prefix_attention: f32 sums; a score is within
+ *   (head_dim + 32) 2^-24 max_t sum_i |scale q_i k_ti|, whichever kernel runs (on
+ *   the tensor cores every f32 is two f16 and every product three).  Beside value
+ *   rows within a factor of 2^16 of one another, rows far off cost time, not bits.
  *
  * qws_prefix_attention: one decode step of a batch over a shared prefix.  Row
  *   b of q attends to positions 0 .. n_prefix-1 of the shared caches k_prefix,
@@ -305,8 +310,8 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   qws_kv_attention over the two one after the other; a row without any
  *   position is zero.  Caches 16-byte aligned; k_prefix and v_prefix may be
  *   NULL when n_prefix is 0, the own caches when every n_ctx is 0.
- *   0 <= n_prefix <= max_prefix < 2^31, 0 <= n_ctx[b] <= max_seq < 2^31 (host
- *   array), batch >= 0.  ws as above, qws_prefix_attention_workspace_bytes.
+ *   0 <= n_prefix <= max_prefix <= 2^30, 0 <= n_ctx[b] <= max_seq <= 2^30 (host
+ *   array), batch >= 0.  out overlaps neither q nor a cache.  ws as above, qws_prefix_attention_workspace_bytes.
  *   Positions from the lengths on may hold anything.
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -528,8 +533,10 @@ qws_status qws_decode_kv(const qws_layer* layers, int n_layers, float* h, const 
  *   for data, 2 = a producer gave up waiting for a free stage, 4 = a grid
  *   barrier gave up, 8 = a producer gave up draining its copies; 16..128 the
  *   prefill kernel's waits; 256 = a prefill weight outside the f16 split's
- *   range; 512 = a token outside the embedding table) and clears them.  Returns QWS_ERR_TIMEOUT when the code is
- *   non-zero.
+ *   range; 512 = a token outside the embedding table; 1024, 2048, 4096 = the
+ *   loaders, the MMA issuers, the softmax and output warps of prompt_attention
+ *   or prefix_attention gave up waiting) and clears them.  Returns
+ *   QWS_ERR_TIMEOUT when the code is non-zero.
  * qws_version: library version string.
  * ---------------------------------------------------------------------- */
 size_t qws_workspace_bytes(qws_op op, int64_t rows, int64_t hidden, int64_t inter, int batch,

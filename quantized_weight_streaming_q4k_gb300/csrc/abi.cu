@@ -418,12 +418,14 @@ qws_status check_head_counts(const char* fn, int n_q, int n_kv, int head_dim) {
 }
 
 constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+// positions of an attention call: sums of two, and of one and a tile, stay in 32 bits
+constexpr int64_t kMaxPositions = int64_t(1) << 30;
 
 qws_status check_offsets(const char* fn, const char* name, const int64_t* cu, int n_seqs) {
   if (cu[0] < 0) return fail(QWS_ERR_SHAPE, "%s: %s[0] < 0", fn, name);
   for (int s = 0; s < n_seqs; ++s)
     if (cu[s + 1] < cu[s]) return fail(QWS_ERR_SHAPE, "%s: %s decreases at %d", fn, name, s);
-  if (cu[n_seqs] > kMaxTokens) return fail(QWS_ERR_SHAPE, "%s: %s passes 2^31", fn, name);
+  if (cu[n_seqs] > kMaxPositions) return fail(QWS_ERR_SHAPE, "%s: %s passes 2^30", fn, name);
   return QWS_OK;
 }
 
@@ -572,11 +574,11 @@ qws_status check_prefix_lengths(const char* fn, int64_t n_prefix, int64_t max_pr
                                 const int64_t* n_ctx, int batch, int64_t max_seq) {
   if (batch < 0 || batch > (1 << 20))
     return fail(QWS_ERR_SHAPE, "%s: batch = %d out of range", fn, batch);
-  if (n_prefix < 0 || n_prefix > max_prefix || max_prefix > kMaxTokens)
-    return fail(QWS_ERR_SHAPE, "%s: need 0 <= n_prefix <= max_prefix < 2^31", fn);
+  if (n_prefix < 0 || n_prefix > max_prefix || max_prefix > kMaxPositions)
+    return fail(QWS_ERR_SHAPE, "%s: need 0 <= n_prefix <= max_prefix <= 2^30", fn);
   if (batch && !n_ctx) return fail(QWS_ERR_NULL, "%s: n_ctx is NULL", fn);
-  if (max_seq < 0 || max_seq > kMaxTokens)
-    return fail(QWS_ERR_SHAPE, "%s: need 0 <= max_seq < 2^31", fn);
+  if (max_seq < 0 || max_seq > kMaxPositions)
+    return fail(QWS_ERR_SHAPE, "%s: need 0 <= max_seq <= 2^30", fn);
   for (int b = 0; b < batch; ++b)
     if (n_ctx[b] < 0 || n_ctx[b] > max_seq)
       return fail(QWS_ERR_SHAPE, "%s: need 0 <= n_ctx[%d] <= max_seq", fn, b);
@@ -589,7 +591,7 @@ size_t qws_prefix_attention_workspace_bytes(int64_t n_prefix, const int64_t* n_c
                                             int n_q_heads, int n_kv_heads, int head_dim) {
   const char* fn = "qws_prefix_attention_workspace_bytes";
   if (batch < 1 || check_head_counts(fn, n_q_heads, n_kv_heads, head_dim) != QWS_OK ||
-      check_prefix_lengths(fn, n_prefix, n_prefix, n_ctx, batch, kMaxTokens) != QWS_OK)
+      check_prefix_lengths(fn, n_prefix, n_prefix, n_ctx, batch, kMaxPositions) != QWS_OK)
     return 0;
   return round256(qws::prefix_attention_workspace_bytes(n_prefix, n_ctx, batch, n_q_heads,
                                                         n_kv_heads, head_dim));

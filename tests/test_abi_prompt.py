@@ -153,3 +153,18 @@ def test_prefix_attention(lib):
     assert lib.qws_prefix_attention_workspace_bytes(1000, ints(1, -1), 2, 4, 2, 64) == 0
     # few positions in all: one kernel, no workspace
     assert lib.qws_prefix_attention_workspace_bytes(100, ints(1, 50, 0), 3, 4, 2, 64) == 0
+
+
+def test_attention_positions_end_at_2_to_the_30(lib):
+    # sums of positions are kept in 32 bits on the device
+    over = 2 ** 30 + 1
+    assert prompt(lib, cu=ints(0, 8), ck=ints(0, over)) == SHAPE
+    assert prompt(lib, cu=ints(over - 2, over)) == SHAPE
+    f = lib.qws_prefix_attention_workspace_bytes
+    assert f(over, ints(0), 1, 4, 2, 64) == 0 and f(0, ints(over), 1, 4, 2, 64) == 0
+    assert f(2 ** 30, ints(0), 1, 4, 2, 64) > 0
+    call = lib.qws_prefix_attention
+    assert call(heads(A), B, D, over, 5, B, D, 50, ints(1), heads(E), 1, 4, 2, 64, 1.0, 0.0, A,
+                1 << 40, None) == SHAPE
+    assert call(heads(A), B, D, 100, 5, B, D, over, ints(1), heads(E), 1, 4, 2, 64, 1.0, 0.0, A,
+                1 << 40, None) == SHAPE
