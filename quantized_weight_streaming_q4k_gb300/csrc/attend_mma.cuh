@@ -247,6 +247,13 @@ struct RingAt {
   }
 };
 
+// Both phases are over, or dead: asked together, as a wait costs some 200 cycles even so.
+__device__ __forceinline__ void wait2(uint64_t* a, uint32_t a_par, uint64_t* b, uint32_t b_par,
+                                      bool& dead) {
+  if (!__all_sync(0xFFFFFFFFu, mbar_test(a, a_par) & mbar_test(b, b_par)) && !dead)
+    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(a, a_par) && mbar_wait(b, b_par));
+}
+
 // ------------------------------------------------------------ the MMA issuers
 // Each a whole warp.  A wait costs some 200 cycles here even if it is over, so the barriers
 // of a chunk are asked together, and waited for one by one only after a no.

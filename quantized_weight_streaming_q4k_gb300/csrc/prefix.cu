@@ -145,10 +145,10 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     const uint32_t free_par = (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u;
     const int stage = (j % Cfg::kDepth) * kNC;
     uint64_t* empty = is_v ? sh.mma.v_empty : sh.mma.k_empty;
-    wait(is_v ? &sh.mma.vmeta_free[slot] : &sh.mma.meta_free[slot], free_par);
     // the V ring is the softmax warps' scratch until Q is stored
     if (jh == 1) wait(&sh.mma.q_ready, 0);
-    wait(&empty[stage], (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u);
+    wait2(is_v ? &sh.mma.vmeta_free[slot] : &sh.mma.meta_free[slot], free_par, &empty[stage],
+          (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u, dead);
     uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
     TileMeta& meta = sh.mma.meta[slot];
     uint32_t out_lo = 0, out_hi = 0;              // rows of the tile this warp leaves out
@@ -234,8 +234,6 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     }
     if (is_v) {
       if ((out_lo | out_hi) && lane < 2) atomicOr(&sh.left_out[j][lane], lane ? out_hi : out_lo);
-      bar_sync(5, 32 * Cfg::kConvWarps);          // every warp's left_out is in
-      if (cw == 0 && lane < 2) meta.left_out[lane] = sh.left_out[j][lane];
       if (cw == 0 && lane == 0) meta.vscale = 1.0f / v_scale;
     }
     fence_proxy_async_smem();                     // generic stores -> visible to the MMAs
@@ -251,8 +249,9 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
 // Softmax and output of a row's half: two threads share a query row, each has half of a
 // tile's keys and, of each chunk of head_dim, half of the output columns.
 template <class Cfg, bool kCap>
-__device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, int n, int keys, float scale,
-                                            float cap, RowState<Cfg>& st, bool& dead) {
+__device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (*left_out)[2],
+                                            int n, int keys, float scale, float cap,
+                                            RowState<Cfg>& st, bool& dead) {
   constexpr int kKeys = kTileKeys / 2;
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int quad = warp & 3, part = warp >> 2;
@@ -362,7 +361,7 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, int n, int keys,
         dead = !__all_sync(0xFFFFFFFFu,
                            mbar_wait(&sh.vmeta_full[ph], static_cast<uint32_t>(j >> 1) & 1u));
       vs = sh.meta[ph].vscale;
-      const bool left = (sh.meta[ph].left_out[0] | sh.meta[ph].left_out[1]) != 0;
+      const bool left = (left_out[j][0] | left_out[j][1]) != 0;
       // the arrival hangs on the values read: loads that nothing has used yet may be
       // scheduled behind it (vs is a power of two; left is the same in all lanes)
       const uint32_t lefts = __ballot_sync(0xFFFFFFFFu, left && vs > 0.f);
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
     bool dead;
     float* scratch = reinterpret_cast<float*>(v_ring);
     store_q<Cfg>(sh.mma, scratch, nullptr, alive ? q : nullptr);
-    prefix_rows<Cfg, kCap>(sh.mma, n, keys, p.scale, p.cap, st, dead);
+    prefix_rows<Cfg, kCap>(sh.mma, sh.left_out, n, keys, p.scale, p.cap, st, dead);
     if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttRows);
     if (st.any_left_out && alive) {
       for (int t = 0; t < keys; ++t)

@@ -205,13 +205,6 @@ constexpr int kRegsSoft = kHd > 128 ? 64 : 104;
 template <int kHd>
 constexpr int kRegsHelp = kHd > 128 ? 32 : 64;
 
-// Both phases are over, or dead: asked together, as a wait costs some 200 cycles even so.
-__device__ __forceinline__ void wait2(uint64_t* a, uint32_t a_par, uint64_t* b, uint32_t b_par,
-                                      bool& dead) {
-  if (!__all_sync(0xFFFFFFFFu, mbar_test(a, a_par) & mbar_test(b, b_par)) && !dead)
-    dead = !__all_sync(0xFFFFFFFFu, mbar_wait(a, a_par) && mbar_wait(b, b_par));
-}
-
 // The weights of the tiles first, first + 2, ... of a row: a thread has the whole row, so
 // nothing is exchanged.  The scaled scores go back to S for the second pass, because 64 of
 // them and the packed weights do not fit the registers.  Each of the two groups of warps
