@@ -532,10 +532,19 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
 // ------------------------------------------------------------ host side
 namespace {
 
-constexpr int64_t kMmaFrom = 1 << 18;
+// (query row, key) pairs of all heads above which the tensor cores, whose two or three
+// launches and packing take 13 us at least, take a call; device time on CUDA cores / tensor
+// cores: 128 tokens of 8 q / 4 kv heads of 256 (2^16 pairs) 21.5 / 19.2 us, of 16 / 4 heads of
+// 128 (2^17) 23.5 / 13.3 us, 64 tokens of 8 / 4 heads of 256 (2^14) 11.3 us / not less than 13.
+constexpr int64_t kMmaFrom = 1 << 16;
+// Up to this many tiles of four rows a warp, one row a warp: each then still has its SM.
+// 37 tokens of 8 q / 4 kv heads of 256: 16.7 -> 9.4 us; 300 tokens of 4 / 1 heads of 64, which
+// fill the SMs either way: 17.9 us with four rows, 20.4 with one.
+constexpr int64_t kOneRowTiles = 38;
 
 struct PromptPlan {
   bool mma;             // on the tensor cores
+  bool one;             // if not: one row a warp in place of four
   int rows, tok, chunk;
   bool split;           // some tile has several pieces
   int64_t items, ktiles;        // per kv head, of the largest launch
@@ -605,7 +614,11 @@ PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int
     if (nq) longest = std::max(longest, nk);
   }
   pl.mma = pairs * n_kv > kMmaFrom;
-  pl.rows = pl.mma ? kTileRows : 4 * kRowWarps;
+  int64_t tiles = 0;           // of 4 rows a warp
+  for (int s = 0; s < n_seqs; ++s)
+    tiles += ceil_div(cu_q[s + 1] - cu_q[s], 4 * kRowWarps / group) * n_kv;
+  pl.one = tiles <= kOneRowTiles;
+  pl.rows = pl.mma ? kTileRows : pl.one ? kRowWarps : 4 * kRowWarps;
   pl.tok = pl.rows / group;
   const int unit = pl.mma ? kTileKeys : 32;         // keys of a step
   const int slots = pl.mma ? 152 : 304;             // items that run at once
@@ -677,12 +690,12 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
     if (e != cudaSuccess) return e;
     e = pdl_launch(kernel, grid, Cfg::kThreads, kSmem, st, p);
   } else {
-    using Tile = RowTile<kPL, 4>;
-    e = cudaFuncSetAttribute(prompt_rows_kernel<kPL, 4>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(Tile::kSmem));
+    const auto kernel = pl.one ? prompt_rows_kernel<kPL, 1> : prompt_rows_kernel<kPL, 4>;
+    const size_t smem = pl.one ? RowTile<kPL, 1>::kSmem : RowTile<kPL, 4>::kSmem;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    e = pdl_launch(prompt_rows_kernel<kPL, 4>, grid, kRowThreads, Tile::kSmem, st, p);
+    e = pdl_launch(kernel, grid, kRowThreads, smem, st, p);
   }
   if (e != cudaSuccess || !pl.split) return e;
   const int64_t rows = static_cast<int64_t>(p.seqs.q0[p.seqs.n] - p.seqs.q0[0]) * p.n_q;
