@@ -74,7 +74,8 @@ struct MmaCfg {
   static constexpr uint32_t kUnit = 2 * kPart;
   static constexpr uint32_t kHalfTile = kNC * kUnit;    // K, or V, of a tile
   static constexpr uint32_t kTile = 2 * kHalfTile;      // a packed key tile
-  // units of each of the two rings: 6, or kDepth whole tiles
+  // units of each of the two rings: 6, or kDepth whole tiles (a fifth unit for K at head_dim
+  // 256 gained nothing)
   static constexpr int kStages = kDepthT ? kDepthT * kNC : 6;
   static constexpr uint32_t kRing = 2 * kStages * kUnit;
   // 8 warps keep the output (thread = row 32 (w % 4) + lane, w / 4 = which half of the
@@ -257,8 +258,11 @@ __device__ __forceinline__ void wait2(uint64_t* a, uint32_t a_par, uint64_t* b, 
 // ------------------------------------------------------------ the MMA issuers
 // Each a whole warp.  A wait costs some 200 cycles here even if it is over, so the barriers
 // of a chunk are asked together, and waited for one by one only after a no.
-// S(j) = Q K(j)^T, chunk after chunk of head_dim, once what was in its buffer has been
-// read; of each chunk the small cross terms first.
+// S(j) = Q K(j)^T, once what was in its buffer has been read, chunk after chunk of
+// head_dim: the small cross terms of all chunks, then hi * hi of all.  The tensor cores
+// round each step's sum towards zero, so the fewer steps at the sum's full size the better:
+// with both in one pass over the chunks the outputs' error at head_dim 256 was twice as
+// large (9.8e-7 for 5.1e-7; plain f32 5.2e-7), and the second pass costs 2 %.
 template <class Cfg>
 __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring,
                                              const uint8_t* q_lo, int n, unsigned* err) {
@@ -272,7 +276,7 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
   bool ok = n <= 0 || __all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
   for (int j = 0; j < n && ok; ++j) {
     const uint32_t d = Cfg::kTmS + static_cast<uint32_t>(buf.stage) * 64u;
-    uint32_t acc = 0;
+    const RingAt<Cfg::kStages> start = at;
 #pragma unroll 1
     for (int c = 0; c < Cfg::kNC; ++c) {
       const bool unit = !(Cfg::kWhole && c > 0), tile = c == 0 && j >= Cfg::kBufs;
@@ -286,14 +290,13 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
       tc_fence_after();
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
-      uint64_t* empty = &sh.k_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
 #pragma unroll
-      for (int t = 0; t < 3; ++t) {
+      for (int t = 0; t < 2; ++t) {
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
           const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 32u;
-          const uint32_t add = (t | k) != 0 ? 1u : acc;
+          const uint32_t add = (t | k) != 0 || c > 0 ? 1u : 0u;
           if constexpr (Cfg::kQLoSmem) {
             if (t == 1) {
               tc_mma_f16_ss(d, lo_base + static_cast<uint32_t>(c * kTileRows * 8 + k * 2),
@@ -306,10 +309,21 @@ __device__ __forceinline__ void mma_issue_qk(MmaShared<Cfg>& sh, uint8_t* k_ring
           tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, add, one);
         }
       }
-      acc = 1;
-      if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
-      if (c == Cfg::kNC - 1) tc_commit(&sh.s_full[buf.stage], one);
     }
+    if (!ok) break;
+    at = start;
+#pragma unroll 1
+    for (int c = 0; c < Cfg::kNC; ++c) {
+      const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
+      uint64_t* empty = &sh.k_empty[Cfg::kWhole ? at.stage - c : at.stage];
+      at.next();
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        tc_mma_f16_ts(d, Cfg::kTmQhi + static_cast<uint32_t>(c * kSteps + k) * 8u,
+                      b + static_cast<uint32_t>(k) * 2u, kIdesc, 1u, one);
+      if (!Cfg::kWhole || c == Cfg::kNC - 1) tc_commit(empty, one);
+    }
+    tc_commit(&sh.s_full[buf.stage], one);
     buf.next();
   }
   if (!ok && one) atomicOr(err, kErrAttMma);

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(256)
 // softcap) where its MMAs take 3330 (1540).  S and P have two buffers, so that Q K(j+2)^T
 // and P V(j+1) do not wait for one tile's softmax.  8192 positions, 8 q / 4 kv heads of 256:
 // 616 -> 525 us; 16 q / 4 kv heads of 128: 619 -> 572 us, with a softcap 785 -> 683 us (the
-// MMAs at the measured rate: 428 us).  Bound by the MMAs and the waits between them at
+// MMAs at the measured rate: 428 us; 544, 575 and 677 us since Q K^T takes two passes).  Bound by the MMAs and the waits between them at
 // head_dim 256, and by the softmax's instructions below (1400 a scheduler and tile).
 template <int kHd>
 struct PromptCfg : MmaCfg<kHd, (kHd > 128 ? 1 : 0), false, 2> {
@@ -538,8 +538,9 @@ namespace {
 // 128 (2^17) 23.5 / 13.3 us, 64 tokens of 8 / 4 heads of 256 (2^14) 11.3 us / not less than 13.
 constexpr int64_t kMmaFrom = 1 << 16;
 // Up to this many tiles of four rows a warp, one row a warp: each then still has its SM.
-// 37 tokens of 8 q / 4 kv heads of 256: 16.7 -> 9.4 us; 300 tokens of 4 / 1 heads of 64, which
-// fill the SMs either way: 17.9 us with four rows, 20.4 with one.
+// 37 tokens of 8 q / 4 kv heads of 256: 16.7 -> 9.4 us.  Longer prompts read the keys more
+// often for it (300 tokens of 4 / 1 heads of 64, 38 tiles: 17.9 us with four rows, 20.4 with
+// one), but most of those are the tensor cores'.
 constexpr int64_t kOneRowTiles = 38;
 
 struct PromptPlan {
