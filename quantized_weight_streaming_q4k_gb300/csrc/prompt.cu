@@ -220,7 +220,10 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
   const uint32_t t_p = lanes + Cfg::kTmP + static_cast<uint32_t>(first) * 64u;
   float m = -INFINITY, l = 0.f;
   bool dead = false;
-  constexpr int kRun = Cfg::kHd > 128 ? 16 : 32;     // keys at a time, as registers allow
+  // As registers allow: the tile's scores are held from one pass to the next, or go back to
+  // S, a run of keys at a time.
+  constexpr bool kHold = Cfg::kHd <= 128;
+  constexpr int kRun = kHold ? 32 : 16, kHeld = kHold ? kTileKeys / kRun : 1;
   dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
   const float qs = q_unscale(sh, row);
   const float rowf = kCap ? qs * (scale / cap) : qs * scale * kLog2e;
@@ -234,20 +237,32 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
     wait2(&sh.meta_full[slot], static_cast<uint32_t>(j / Cfg::kMetas) & 1u, &sh.s_full[first], ph,
           dead);
     tc_fence_after();
-    float mx = -INFINITY;
-#pragma unroll 1
-    for (int h = 0; h < kTileKeys; h += kRun) {
-      uint32_t v[kRun];
-      float x[kRun];
-      tc_ld<kRun>(t_s + static_cast<uint32_t>(h), v);
+    uint32_t v[kHeld][kRun];
+    if constexpr (kHold) {
+#pragma unroll
+      for (int r = 0; r < kHeld; ++r) tc_ld<kRun>(t_s + static_cast<uint32_t>(r * kRun), v[r]);
       tc_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.s_free[first]);
+    }
+    float mx = -INFINITY;
+#pragma unroll kHeld
+    for (int r = 0; r < kTileKeys / kRun; ++r) {
+      const int h = r * kRun;
+      uint32_t(&vr)[kRun] = v[kHold ? r : 0];
+      float x[kRun];
+      if constexpr (!kHold) {
+        tc_ld<kRun>(t_s + static_cast<uint32_t>(h), vr);
+        tc_wait_ld();
+      }
 #pragma unroll
       for (int i = 0; i < kRun; i += 4) {
         const float4 k = *reinterpret_cast<const float4*>(ks + h + i);
         const float2 f = make_float2(rowf, rowf);
-        const float2 a = __fmul2_rn(bits2(v[i], v[i + 1]), __fmul2_rn(make_float2(k.x, k.y), f));
+        const float2 a = __fmul2_rn(bits2(vr[i], vr[i + 1]), __fmul2_rn(make_float2(k.x, k.y), f));
         const float2 b =
-            __fmul2_rn(bits2(v[i + 2], v[i + 3]), __fmul2_rn(make_float2(k.z, k.w), f));
+            __fmul2_rn(bits2(vr[i + 2], vr[i + 3]), __fmul2_rn(make_float2(k.z, k.w), f));
         x[i] = a.x; x[i + 1] = a.y; x[i + 2] = b.x; x[i + 3] = b.y;
       }
       if constexpr (kCap) tanh_scaled<kRun>(x, cap * kLog2e);
@@ -259,13 +274,14 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         mx = fmaxf(mx, x[i]);
-        v[i] = __float_as_uint(x[i]);
+        vr[i] = __float_as_uint(x[i]);
       }
-      tc_st<kRun>(t_s + static_cast<uint32_t>(h), v);
+      if constexpr (!kHold) tc_st<kRun>(t_s + static_cast<uint32_t>(h), vr);
     }
-    tc_wait_st();
+    if constexpr (!kHold) tc_wait_st();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.meta_free[slot]);     // the scales are in what was stored
+    // the scales are in what was stored, or in the maximum
+    if (lane == 0 && (!kHold || !(mx > INFINITY))) mbar_arrive(&sh.meta_free[slot]);
     const float mn = fmaxf(m, mx);
     const float base = mn == -INFINITY ? 0.f : mn;
     l *= ex2(m - base);
@@ -276,21 +292,28 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
     tc_fence_after();
     sh.x[0][first][row] = m;
     float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int h = 0; h < kTileKeys; h += kRun) {
-      uint32_t v[kRun], hi[kRun / 2], lo[kRun / 2];
-      tc_ld<kRun>(t_s + static_cast<uint32_t>(h), v);
-      tc_wait_ld();
-#pragma unroll
-      for (int i = 0; i < kRun; i += 2) {
-        float2 a = __fadd2_rn(bits2(v[i], v[i + 1]), make_float2(sub, sub));
-        a.x = ex2(a.x);
-        a.y = ex2(a.y);
-        sum = __fadd2_rn(sum, a);
-        split2(a, hi[i / 2], lo[i / 2]);
+#pragma unroll kHeld
+    for (int r = 0; r < kTileKeys / kRun; ++r) {
+      uint32_t(&vr)[kRun] = v[kHold ? r : 0];
+      if constexpr (!kHold) {
+        tc_ld<kRun>(t_s + static_cast<uint32_t>(r * kRun), vr);
+        tc_wait_ld();
       }
-      tc_st<kRun / 2>(t_p + static_cast<uint32_t>(h / 2), hi);
-      tc_st<kRun / 2>(t_p + 32u + static_cast<uint32_t>(h / 2), lo);
+#pragma unroll
+      for (int e = 0; e < kRun; e += 16) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          float2 a = __fadd2_rn(bits2(vr[e + i], vr[e + i + 1]), make_float2(sub, sub));
+          a.x = ex2(a.x);
+          a.y = ex2(a.y);
+          sum = __fadd2_rn(sum, a);
+          split2(a, hi[i / 2], lo[i / 2]);
+        }
+        const uint32_t at = t_p + static_cast<uint32_t>((r * kRun + e) / 2);
+        tc_st<8>(at, hi);
+        tc_st<8>(at + 32u, lo);
+      }
     }
     l += sum.x + sum.y;
     tc_wait_st();
@@ -298,7 +321,7 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(&sh.p_ready[first]);
-      mbar_arrive(&sh.s_free[first]);
+      if (!kHold) mbar_arrive(&sh.s_free[first]);
     }
   }
   sh.x[0][first][row] = m;
