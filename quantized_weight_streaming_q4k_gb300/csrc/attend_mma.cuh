@@ -443,14 +443,21 @@ __device__ __forceinline__ void store_q(MmaShared<Cfg>& sh, float* scratch, uint
   }
 #pragma unroll
   for (int k = 0; k < kLoads; ++k) {
+    // the largest finite magnitude: an infinity makes a itself one, which is rare
     float a = 0.f;
+    const auto take = [&](bool all) {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) {
-      const float4 y = v[r][k];
-      const float o[4] = {y.x, y.y, y.z, y.w};
+      for (int r = 0; r < kRuns; ++r) {
+        const float o[4] = {v[r][k].x, v[r][k].y, v[r][k].z, v[r][k].w};
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
+        for (int c = 0; c < 4; ++c)
+          if (all || finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
+      }
+    };
+    take(true);
+    if (__any_sync(0xFFFFFFFFu, a == INFINITY)) {
+      a = 0.f;
+      take(false);
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));

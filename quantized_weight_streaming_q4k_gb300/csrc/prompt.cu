@@ -420,18 +420,19 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   uint8_t* stages = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   uint8_t* q_lo = stages + Cfg::kRing;
   auto& sh = *reinterpret_cast<MmaShared<Cfg>*>(stages + Cfg::kSmem);
-  const int item = blockIdx.x / p.n_kv, g = blockIdx.x - item * p.n_kv;
-  const PromptItem it = prompt_item(p, item);
   pdl_launch_dependents();
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
-  const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
-  const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
-  const int64_t tile0 = p.seqs.ktile[it.s] + ka / kTileKeys;    // its packed tiles
-  if (threadIdx.x == 0) mma_init_barriers<Cfg>(sh, 1);
+  // before the item is looked up, which takes the other warps as long
+  if (warp == Cfg::kMmaPv && lane == 0) mma_init_barriers<Cfg>(sh, 1);
   if (warp == Cfg::kMmaQk) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  const int item = blockIdx.x / p.n_kv, g = blockIdx.x - item * p.n_kv;
+  const PromptItem it = prompt_item(p, item);
+  const int ka = it.piece * p.chunk, kb = min(it.vis, ka + p.chunk);
+  const int n = kb > ka ? (kb - ka + kTileKeys - 1) / kTileKeys : 0;
+  const int64_t tile0 = p.seqs.ktile[it.s] + ka / kTileKeys;    // its packed tiles
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
