@@ -632,11 +632,35 @@ __device__ __forceinline__ float row_amax(const float (&x)[kPL], bool& all) {
   return __uint_as_float(a);
 }
 
-// 64 keys of one kv head, n of them there (the rest zero), by a CTA of 256
-// threads, into dst: the units of K, then those of V, and the meta record.
+// 64 keys of one kv head, n of them there (the rest zero), by a CTA of 256 threads: K as
+// units at dst and the keys' scales.
 template <class Cfg>
-__device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_t k_stride,
-                                          int64_t v_stride, int n, uint8_t* dst, TileMeta* meta) {
+__device__ __forceinline__ void pack_keys(const float* K, int64_t stride, int n, uint8_t* dst,
+                                          TileMeta* meta) {
+  constexpr int kPL = Cfg::kHd / 32, kRows = kTileKeys / 8;
+  const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
+  float x[kRows][kPL];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + 8 * i;
+#pragma unroll
+    for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
+    if (r < n) load_row<kPL>(K + r * stride, lane, x[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = warp + 8 * i;
+    bool fin;
+    const int e = split_exp(row_amax<kPL>(x[i], fin));
+    store_split_row<Cfg>(x[i], exp2i(e), r, lane, dst);
+    if (lane == 0) meta->kscale[r] = exp2i(-e);
+  }
+}
+
+// Their values, likewise, with one scale for the tile.
+template <class Cfg>
+__device__ __forceinline__ void pack_values(const float* V, int64_t stride, int n, uint8_t* dst,
+                                            TileMeta* meta) {
   constexpr int kPL = Cfg::kHd / 32, kRows = kTileKeys / 8;
   __shared__ float vmax[kTileKeys];
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
@@ -644,21 +668,15 @@ __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = warp + 8 * i;
-    float x[kPL];
 #pragma unroll
-    for (int c = 0; c < kPL; ++c) x[c] = y[i][c] = 0.f;
-    if (r < n) {
-      load_row<kPL>(K + r * k_stride, lane, x);
-      load_row<kPL>(V + r * v_stride, lane, y[i]);
-    }
+    for (int c = 0; c < kPL; ++c) y[i][c] = 0.f;
+    if (r < n) load_row<kPL>(V + r * stride, lane, y[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
     bool fin;
-    const int e = split_exp(row_amax<kPL>(x, fin));
-    store_split_row<Cfg>(x, exp2i(e), r, lane, dst);
     const float b = row_amax<kPL>(y[i], fin);
-    if (lane == 0) {
-      meta->kscale[r] = exp2i(-e);
-      vmax[r] = fin ? b : INFINITY;
-    }
+    if (lane == 0) vmax[warp + 8 * i] = fin ? b : INFINITY;
   }
   __syncthreads();
   // the rows within 2^16 of the smallest non-zero row, or within 2^16 of the largest that
@@ -691,7 +709,7 @@ __device__ __forceinline__ void pack_tile(const float* K, const float* V, int64_
     const bool out = ((r < 32 ? ma : mb) >> (r & 31)) & 1u;
 #pragma unroll
     for (int c = 0; c < kPL; ++c) y[i][c] = out ? 0.f : y[i][c];
-    store_split_row<Cfg>(y[i], exp2i(e), r, lane, dst + Cfg::kHalfTile);
+    store_split_row<Cfg>(y[i], exp2i(e), r, lane, dst);
   }
 }
 

@@ -395,7 +395,8 @@ __device__ __forceinline__ bool tile_sums(MmaShared<Cfg>& sh, int n, RowState<Cf
 }
 
 // Key tiles of every sequence and kv head, split and laid out once (they are
-// read by all of the sequence's query tiles).  grid (key tiles, n_kv).
+// read by all of the sequence's query tiles).  grid (key tiles, n_kv, 2): K, then V, apart,
+// as a CTA is one chain of a read, a reduction and a write.
 template <int kHd>
 __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant__ PromptParams p) {
   using Cfg = PromptCfg<kHd>;
@@ -406,9 +407,13 @@ __global__ void __launch_bounds__(256) prompt_pack_kernel(const __grid_constant_
   const int64_t key = p.seqs.k0[s] + static_cast<int64_t>(tile - p.seqs.ktile[s]) * kTileKeys;
   const int n = static_cast<int>(min(static_cast<int64_t>(kTileKeys), p.seqs.k0[s + 1] - key));
   const int64_t at = static_cast<int64_t>(tile) * p.n_kv + g;
-  pack_tile<Cfg>(p.k.data + key * p.k.token_stride + g * p.k.head_stride,
-                 p.v.data + key * p.v.token_stride + g * p.v.head_stride, p.k.token_stride,
-                 p.v.token_stride, n, p.packed + at * Cfg::kTile, p.meta + at);
+  uint8_t* dst = p.packed + at * Cfg::kTile;
+  if (blockIdx.z == 0)
+    pack_keys<Cfg>(p.k.data + key * p.k.token_stride + g * p.k.head_stride, p.k.token_stride, n,
+                   dst, p.meta + at);
+  else
+    pack_values<Cfg>(p.v.data + key * p.v.token_stride + g * p.v.head_stride, p.v.token_stride,
+                     n, dst + Cfg::kHalfTile, p.meta + at);
 }
 
 // One item per CTA: 128 rows of one kv head against its piece of the keys.
@@ -705,7 +710,7 @@ cudaError_t run_prompt(PromptParams& p, const PromptPlan& pl, int64_t items, int
     static_assert(kSmem <= 227 * 1024, "shared memory");
     if (ktiles > 0) {
       e = pdl_launch(prompt_pack_kernel<kHd>,
-                     dim3(static_cast<unsigned>(ktiles), static_cast<unsigned>(p.n_kv)), 256, 0,
+                     dim3(static_cast<unsigned>(ktiles), static_cast<unsigned>(p.n_kv), 2), 256, 0,
                      st, p);
       if (e != cudaSuccess) return e;
     }
