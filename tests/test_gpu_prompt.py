@@ -586,6 +586,18 @@ def test_prefix_rows_of_very_different_size(hd):
     check_prefix(q, kp, vp, 700, kc, vc, [5, 0, 2], hd ** -0.5, 0.0, out)
 
 
+@pytest.mark.parametrize("first", [0.0, 1e-3, 0.02, 60.0])
+def test_prefix_first_rows_unlike_the_rest(first):
+    # the rows that a piece takes its scale from
+    g = gen(44)
+    q, kp, vp = normal(g, 3, 4, 128), normal(g, 2, 900, 128), normal(g, 2, 900, 128)
+    kp[:, :64] *= first
+    vp[:, :64] *= first
+    kc, vc = normal(g, 3, 2, 5, 128), normal(g, 3, 2, 5, 128)
+    out = ops.prefix_attention(q, kp, vp, 900, kc, vc, [5, 0, 2], 0.09)
+    check_prefix(q, kp, vp, 900, kc, vc, [5, 0, 2], 0.09, 0.0, out)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_prefix_seen_infinities_show(bad):
     g = gen(42)
