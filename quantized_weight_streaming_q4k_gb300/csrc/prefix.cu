@@ -54,7 +54,7 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
 // a loader copies runs of rows into a staging ring, eight converter warps scale, split
 // and lay them out for the tensor cores.  Bound by that read (8 * head_dim bytes a key
 // and kv head; at head_dim 256 a tile of 64 keys is 128 KB, about 5800 cycles of an
-// SM's share of the memory, against 3072 cycles of MMAs).
+// SM's share of the memory, against 3100 cycles of MMAs).
 //
 // The converters bound it next (with a maximum over every row and a scale of its own
 // they took 12200 cycles a tile).  So a piece has one scale for its keys and one for its
