@@ -426,7 +426,7 @@ __device__ __forceinline__ void store_q(MmaShared<Cfg>& sh, float* scratch, uint
                                         const float* q) {
   constexpr int kQC = Cfg::kHd / 2, kRun = kQC < 32 ? kQC : 32, kLanes = kRun / 4;
   constexpr int kAt = 32 / kLanes, kLoads = 32 / kAt, kRuns = kQC / kRun;
-  constexpr int kPitch = kRun / 2 + 4;
+  constexpr int kPitch = kRun + 4;         // hi, lo of a row
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   const int quad = warp & 3, part = warp >> 2;
   const int r0 = 32 * quad + lane / kLanes, at = lane % kLanes;
@@ -441,64 +441,66 @@ __device__ __forceinline__ void store_q(MmaShared<Cfg>& sh, float* scratch, uint
       if (src) v[r][k] = *reinterpret_cast<const float4*>(src + part * kQC + r * kRun + at * 4);
     }
   }
+  // the largest finite magnitude of each row; infinities, which are rare, in a second pass
+  float a[kLoads];
+  const auto largest = [&](bool all) {
 #pragma unroll
-  for (int k = 0; k < kLoads; ++k) {
-    // the largest finite magnitude: an infinity makes a itself one, which is rare
-    float a = 0.f;
-    const auto take = [&](bool all) {
+    for (int k = 0; k < kLoads; ++k) {
+      a[k] = 0.f;
 #pragma unroll
       for (int r = 0; r < kRuns; ++r) {
         const float o[4] = {v[r][k].x, v[r][k].y, v[r][k].z, v[r][k].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (all || finite_bits(o[c])) a = fmaxf(a, fabsf(o[c]));
+          if (all || finite_bits(o[c])) a[k] = fmaxf(a[k], fabsf(o[c]));
       }
-    };
-    take(true);
-    if (__any_sync(0xFFFFFFFFu, a == INFINITY)) {
-      a = 0.f;
-      take(false);
     }
+  };
+  largest(true);
+  float top = a[0];
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    if (at == 0) sh.qmax[part][r0 + k * kAt] = a;
-  }
-  bar_sync(1 + quad, 64);
-  float sc[kLoads];
+  for (int k = 1; k < kLoads; ++k) top = fmaxf(top, a[k]);
+  if (__any_sync(0xFFFFFFFFu, top == INFINITY)) largest(false);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) a[k] = fmaxf(a[k], __shfl_xor_sync(0xFFFFFFFFu, a[k], o));
 #pragma unroll
   for (int k = 0; k < kLoads; ++k)
-    sc[k] = exp2i(split_exp(fmaxf(sh.qmax[0][r0 + k * kAt], sh.qmax[1][r0 + k * kAt])));
+    if (at == 0) sh.qmax[part][r0 + k * kAt] = a[k];
+  bar_sync(1 + quad, 64);
   uint32_t* mine = reinterpret_cast<uint32_t*>(scratch) + warp * 32 * kPitch;
   const uint32_t lanes = static_cast<uint32_t>(32 * quad) << 16;
 #pragma unroll
+  for (int k = 0; k < kLoads; ++k)
+    a[k] = exp2i(split_exp(fmaxf(a[k], sh.qmax[part ^ 1][r0 + k * kAt])));
+#pragma unroll
   for (int r = 0; r < kRuns; ++r) {
-    uint2 lo[kLoads];
+    if (r > 0) __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      const float2 f = make_float2(a[k], a[k]);
+      uint2 hi, lo;
+      split2(__fmul2_rn(make_float2(v[r][k].x, v[r][k].y), f), hi.x, lo.x);
+      split2(__fmul2_rn(make_float2(v[r][k].z, v[r][k].w), f), hi.y, lo.y);
+      uint32_t* to = mine + (k * kAt + lane / kLanes) * kPitch + at * 2;
+      *reinterpret_cast<uint2*>(to) = hi;
+      if constexpr (Cfg::kQLoSmem) {
+        const uint32_t col = static_cast<uint32_t>(part * kQC + r * kRun + at * 4);
+        *reinterpret_cast<uint2*>(
+            q_lo + (col / 64) * (kTileRows * 128) +
+            sw128_off(static_cast<uint32_t>(r0 + k * kAt), (col % 64) / 8) + (col % 8) * 2) = lo;
+      } else {
+        *reinterpret_cast<uint2*>(to + kRun / 2) = lo;
+      }
+    }
+    __syncwarp();
 #pragma unroll
     for (int t = 0; t < (Cfg::kQLoSmem ? 1 : 2); ++t) {
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        uint2 hi;
-        if (t == 0) {
-          const float4 y = v[r][k];
-          split_f16x2(y.x * sc[k], y.y * sc[k], hi.x, lo[k].x);
-          split_f16x2(y.z * sc[k], y.w * sc[k], hi.y, lo[k].y);
-        }
-        *reinterpret_cast<uint2*>(mine + (k * kAt + lane / kLanes) * kPitch + at * 2) =
-            t == 0 ? hi : lo[k];
-        if constexpr (Cfg::kQLoSmem) {
-          const uint32_t col = static_cast<uint32_t>(part * kQC + r * kRun + at * 4);
-          *reinterpret_cast<uint2*>(
-              q_lo + (col / 64) * (kTileRows * 128) +
-              sw128_off(static_cast<uint32_t>(r0 + k * kAt), (col % 64) / 8) + (col % 8) * 2) =
-              lo[k];
-        }
-      }
-      __syncwarp();
       uint32_t w[kRun / 2];
 #pragma unroll
       for (int i = 0; i < kRun / 2; i += 4) {
-        const uint4 y = *reinterpret_cast<const uint4*>(mine + lane * kPitch + i);
+        const uint4 y = *reinterpret_cast<const uint4*>(mine + lane * kPitch + t * (kRun / 2) + i);
         w[i] = y.x; w[i + 1] = y.y; w[i + 2] = y.z; w[i + 3] = y.w;
       }
       tc_st<kRun / 2>(lanes + (t == 0 ? Cfg::kTmQhi : Cfg::kTmQlo) +
