@@ -198,20 +198,21 @@ __device__ __forceinline__ void store_partial(float* dst, int lane, const float 
   }
 }
 
-// Joins the n partial results of a row in order, by one warp, for its columns, kV
+// Joins the partial results from .. n - 1 of a row in order, by one warp, for its columns, kV
 // neighbours a lane from column col on.  part(c) is piece c's row, called by the whole
-// warp with one c; mine(c) the same, called by some lanes, lane i with c = i modulo 32
+// warp with one c; mine(c) the same, called by some lanes, lane i with c = from + i modulo 32
 // (so neither may exchange values between lanes there).  The columns of a
 // batch of pieces are fetched together with, not after, the maxima that weigh them: one
-// trip to memory and not three.  Returns the row's sum.
+// trip to memory and not three.  Returns the row's sum, and its maximum in M.
 template <int kHd, int kV, class Mine, class Part>
-__device__ __forceinline__ float join_parts(int n, int lane, int col, Mine&& mine, Part&& part,
-                                            float (&acc)[kV]) {
+__device__ __forceinline__ float join_parts(int from, int n, int lane, int col, Mine&& mine,
+                                            Part&& part, float (&acc)[kV], float& M) {
   constexpr int kBatch = 32 / kV;
-  float M = -INFINITY, L = 0.f;
+  float L = 0.f;
+  M = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kV; ++i) acc[i] = 0.f;
-  for (int c0 = 0; c0 < n; c0 += 32) {
+  for (int c0 = from; c0 < n; c0 += 32) {
     const int m = min(32, n - c0);
     float mc = -INFINITY, lc = 0.f;
     if (lane < m) {

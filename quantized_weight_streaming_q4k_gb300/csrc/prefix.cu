@@ -672,18 +672,19 @@ __global__ void __launch_bounds__(kOwnWarps * 32)
   }
 }
 
-// One warp per (sequence, query head, 64 columns): the prefix pieces, then the own ones.
+// One CTA per (sequence, query head, 64 columns): the prefix pieces, then the own ones, a
+// quarter of them a warp (at least 8), and the warps in order.  By one warp, 37 pieces and
+// up to 32 own ones were six trips to memory in turn, 10 us.
+constexpr int kJoinWarps = 4;
 template <int kPL>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     prefix_merge_kernel(const __grid_constant__ PrefixParams p) {
   constexpr int kHd = kPL * 32, kV = kPL >= 2 ? 2 : 1, kWide = kHd / (32 * kV);
+  __shared__ float sacc[kJoinWarps][32 * kV], sm[kJoinWarps], sl[kJoinWarps];
   pdl_launch_dependents();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int rh = w / kWide, c0 = (w - rh * kWide) * 32 * kV;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rh = blockIdx.x / kWide, c0 = (blockIdx.x - rh * kWide) * 32 * kV;
   const int b = rh / p.n_q, h = rh - b * p.n_q, g = h / p.group;
-  if (b >= p.batch) return;
   const int row = b * p.group + (h - g * p.group);
   const auto part = [&](int c) {
     return c < p.pieces
@@ -691,12 +692,36 @@ __global__ void __launch_bounds__(128)
                : p.own + ((static_cast<int64_t>(p.first[b] + c - p.pieces) * p.n_kv + g) * p.group +
                           (h - g * p.group)) * (kHd + kPartPad);
   };
-  float acc[kV];
-  const float l = join_parts<kHd, kV>(p.pieces + p.first[b + 1] - p.first[b], lane,
-                                      c0 + lane * kV, part, part, acc);
+  const int n = p.pieces + p.first[b + 1] - p.first[b];
+  const int each = max(8, (n + kJoinWarps - 1) / kJoinWarps), from = warp * each;
+  pdl_wait();
+  float acc[kV], m;
+  const float l = join_parts<kHd, kV>(from, min(n, from + each), lane, c0 + lane * kV, part, part,
+                                      acc, m);
+#pragma unroll
+  for (int i = 0; i < kV; ++i) sacc[warp][lane * kV + i] = acc[i];
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
+  __syncthreads();
+  if (warp > 0) return;
+  float M = sm[0], L = 0.f;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) M = fmaxf(M, sm[w]);
+  const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float f = exp2f(sm[w] - base);
+    L = fmaf(sl[w], f, L);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = fmaf(sacc[w][lane * kV + i], f, acc[i]);
+  }
   store_final<kV>(p.out.data + static_cast<int64_t>(p.b0 + b) * p.out.token_stride +
                       h * p.out.head_stride + c0,
-                  lane, acc, l);
+                  lane, acc, L);
 }
 
 // ------------------------------------------------------------ host side
@@ -781,10 +806,9 @@ cudaError_t run_prefix(const PrefixParams& p, const PrefixPlan& pl, cudaStream_t
     }
     if (e != cudaSuccess) return e;
   }
-  constexpr int kWide = kPL > 2 ? kPL / 2 : 1;          // warps of a row
-  const int warps = p.batch * p.n_q * kWide;
-  return pdl_launch(prefix_merge_kernel<kPL>, dim3(static_cast<unsigned>((warps + 3) / 4)), 128,
-                    0, st, p);
+  constexpr int kWide = kPL > 2 ? kPL / 2 : 1;          // CTAs of a row
+  return pdl_launch(prefix_merge_kernel<kPL>, dim3(static_cast<unsigned>(p.batch * p.n_q * kWide)),
+                    kJoinWarps * 32, 0, st, p);
 }
 
 }  // namespace

@@ -145,12 +145,16 @@ __global__ void __launch_bounds__(256)
     prompt_merge_kernel(const __grid_constant__ PromptParams p) {
   constexpr int kHd = kPL * 32;
   pdl_launch_dependents();
-  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int total = p.seqs.q0[p.seqs.n] - p.seqs.q0[0];
   const int64_t t = w / p.n_q;
-  if (t >= total) return;
+  // every warp waits, also one with nothing to do: who comes behind this kernel counts on
+  // the one before it to be done
+  if (t >= total) {
+    pdl_wait();
+    return;
+  }
   const int h = static_cast<int>(w - t * p.n_q), g = h / p.group;
   const int token = p.seqs.q0[0] + static_cast<int>(t);
   PromptItem it;
@@ -161,12 +165,16 @@ __global__ void __launch_bounds__(256)
   const int i = token - p.seqs.q0[it.s];
   it.tile = i / p.tok;
   tile_span(p, it);
-  if (it.pieces < 2) return;
+  if (it.pieces < 2) {
+    pdl_wait();
+    return;
+  }
   const int row = (i - it.i0) * p.group + (h - g * p.group);
   // lane c holds where piece c is (a tile has at most 32: the plan sees to it)
   int64_t where = first_item(p, it);
   for (int c = 1; c <= lane && c < it.pieces; ++c) where += next_piece(p, it, c - 1);
   where = ((where * p.n_kv + g) * p.rows + row) * (kHd + kPartPad);
+  pdl_wait();
   const auto mine = [&](int) { return p.part + where; };
   const auto part = [&](int c) { return p.part + __shfl_sync(0xFFFFFFFFu, where, c); };
   constexpr int kV = kPL >= 4 ? 4 : kPL;
@@ -174,8 +182,8 @@ __global__ void __launch_bounds__(256)
                h * p.out.head_stride;
 #pragma unroll
   for (int c = 0; c < kHd; c += 32 * kV) {
-    float acc[kV];
-    const float l = join_parts<kHd, kV>(it.pieces, lane, c + lane * kV, mine, part, acc);
+    float acc[kV], m;
+    const float l = join_parts<kHd, kV>(0, it.pieces, lane, c + lane * kV, mine, part, acc, m);
     store_final<kV>(dst + c, lane, acc, l);
   }
 }
