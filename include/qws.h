@@ -294,7 +294,8 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *     softmax(s)_j v_j, head h reading kv head h / (n_q / n_kv); a row without
  *     a key is zero.  Rows that belong to no sequence are not touched.
  *   cu_q, cu_k: host, n_seqs + 1 non-decreasing offsets, 0 <= offset <= 2^30.
- *   out overlaps none of q, k and v.
+ *   out overlaps none of q, k and v.  scale and, with a softcap, scale / softcap
+ *   finite (in qws_prefix_attention too).
  *   ws: device, 16-byte aligned, >= qws_prompt_attention_workspace_bytes of
  *   the same arguments (0: may be NULL).  Keys that a row does not see may
  *   hold anything, infinities and NaN included.

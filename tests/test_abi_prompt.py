@@ -168,3 +168,11 @@ def test_attention_positions_end_at_2_to_the_30(lib):
                 1 << 40, None) == SHAPE
     assert call(heads(A), B, D, 100, 5, B, D, over, ints(1), heads(E), 1, 4, 2, 64, 1.0, 0.0, A,
                 1 << 40, None) == SHAPE
+
+
+def test_attention_scale_over_softcap_is_finite(lib):
+    assert prompt(lib, scale=1.0, cap=1e-39) == SHAPE
+    assert prompt(lib, scale=1e20, cap=1e-20) == SHAPE
+    assert lib.qws_prefix_attention(heads(A), B, D, 100, 5, B, D, 50, ints(1), heads(E), 1, 4, 2, 64,
+                                    1.0, 1e-39, A, 1 << 40, None) == SHAPE
+    assert prompt(lib, cu=ints(0, 5000), scale=1.0, cap=1e-20, ws=None, ws_bytes=0) == WORKSPACE
