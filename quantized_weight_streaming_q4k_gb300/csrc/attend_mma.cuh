@@ -87,7 +87,8 @@ struct MmaCfg {
   static constexpr int kLoadK = kRowsWarps + (kBufs > 1 ? 8 : 0), kLoadV = kLoadK + 1;
   static constexpr int kMmaQk = kLoadK + 2, kMmaPv = kLoadK + 3;
   // Tensor memory columns (all 512 are allocated, so they start at 0): Q hi, Q lo, the
-  // buffers of S, those of P (hi, lo), and two of O_tile.  Where that is too much, Q lo
+  // buffers of S, those of P (of every 16 keys hi, then lo: 16 columns, as many as their
+  // scores take), and two of O_tile.  Where that is too much, Q lo
   // is in shared memory (its MMAs take 48 cycles a step in place of 32).
   static constexpr bool kQLoSmem = kBufs > 1 && kHd > 128;
   static constexpr uint32_t kQLoBytes = kQLoSmem ? kNC * kTileRows * 128 : 0;
@@ -359,7 +360,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
       if (!ok) break;
       const uint32_t b = base + static_cast<uint32_t>(at.stage) * (Cfg::kUnit >> 4);
       const uint32_t d = Cfg::kTmO + static_cast<uint32_t>(buf.stage) * 64u;
-      const uint32_t hi = Cfg::kTmP + static_cast<uint32_t>(pb.stage) * 64u, lo = hi + 32u;
+      const uint32_t hi = Cfg::kTmP + static_cast<uint32_t>(pb.stage) * 64u, lo = hi + 8u;
       uint64_t* full = &sh.o_full[buf.stage];
       uint64_t* empty = &sh.v_empty[Cfg::kWhole ? at.stage - c : at.stage];
       at.next();
@@ -368,7 +369,7 @@ __device__ __forceinline__ void mma_issue_pv(MmaShared<Cfg>& sh, uint8_t* v_ring
       for (int t = 0; t < 3; ++t) {
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k) {
-          const uint32_t a = (t == 1 ? lo : hi) + static_cast<uint32_t>(k) * 8u;
+          const uint32_t a = (t == 1 ? lo : hi) + static_cast<uint32_t>(k) * 16u;
           const uint32_t off = (t == 0 ? Cfg::kPart : 0u) + static_cast<uint32_t>(k) * 2048u;
           tc_mma_f16_ts(d, a, b + (off >> 4), kIdesc, (t | k) != 0 ? 1u : 0u, one);
         }

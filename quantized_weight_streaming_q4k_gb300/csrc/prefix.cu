@@ -272,7 +272,7 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (
   const float rowf = kCap ? qscale * (scale / cap) : qscale * scale * kLog2e;
   const uint32_t t_o = lanes + Cfg::kTmO + static_cast<uint32_t>(part * Cfg::kOC);
   float alpha = 1.f, vs = 1.f;
-  uint32_t hi[kKeys / 2], lo[kKeys / 2];
+  uint32_t w[kKeys];           // of every 16 keys hi, then lo
   // waits unless an earlier mbar_test saw the phase over
   auto wait = [&](uint64_t* bar, uint32_t parity, bool seen) {
     if (!__all_sync(0xFFFFFFFFu, seen) && !dead)
@@ -337,7 +337,7 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (
       a.x = ex2(a.x);
       a.y = ex2(a.y);
       sum = __fadd2_rn(sum, a);
-      split2(a, hi[i], lo[i]);
+      split2(a, w[i / 8 * 16 + i % 8], w[i / 8 * 16 + 8 + i % 8]);
     }
     st.l = fmaf(st.l, alpha, sum.x + sum.y);
   };
@@ -346,8 +346,7 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (
     const uint32_t ph = static_cast<uint32_t>(j + 1) & 1u;
     s_seen = mbar_test(&sh.meta_full[ph], static_cast<uint32_t>((j + 1) >> 1) & 1u) &
              mbar_test(&sh.s_full[0], ph);
-    tc_st<kKeys / 2>(lanes + Cfg::kTmP + static_cast<uint32_t>(kKeys / 2 * part), hi);
-    tc_st<kKeys / 2>(lanes + Cfg::kTmP + 32u + static_cast<uint32_t>(kKeys / 2 * part), lo);
+    tc_st<kKeys>(lanes + Cfg::kTmP + static_cast<uint32_t>(kKeys * part), w);
     tc_wait_st();
     tc_fence_before();
     __syncwarp();

@@ -214,8 +214,9 @@ template <int kHd>
 constexpr int kRegsHelp = kHd > 128 ? 32 : 64;
 
 // The weights of the tiles first, first + 2, ... of a row: a thread has the whole row, so
-// nothing is exchanged.  The scaled scores go back to S for the second pass, because 64 of
-// them and the packed weights do not fit the registers.  Each of the two groups of warps
+// nothing is exchanged.  Above head_dim 128, 64 scores and their packed weights do not fit the
+// registers, and the scores wait for the second pass in tensor memory.  Each of the two groups
+// of warps
 // has its own running maximum; the output warps bring the tiles to one.  vis: the row sees
 // the keys below vis; all_vis: below this one, every row of the CTA does.
 template <class Cfg, bool kCap>
@@ -228,8 +229,8 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
   const uint32_t t_p = lanes + Cfg::kTmP + static_cast<uint32_t>(first) * 64u;
   float m = -INFINITY, l = 0.f;
   bool dead = false;
-  // As registers allow: the tile's scores are held from one pass to the next, or go back to
-  // S, a run of keys at a time.
+  // As registers allow: the tile's scores are held from one pass to the next, or go to where
+  // its weights will be, a run of keys at a time; S is free from then on either way.
   constexpr bool kHold = Cfg::kHd <= 128;
   constexpr int kRun = kHold ? 32 : 16, kHeld = kHold ? kTileKeys / kRun : 1;
   dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
@@ -253,6 +254,11 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.s_free[first]);
+    } else {
+      // the buffer's last tile has been multiplied: the scores go there
+      if (!__all_sync(0xFFFFFFFFu, mbar_test(&sh.p_free[first], ph ^ 1u)) && !dead)
+        dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.p_free[first], ph ^ 1u));
+      tc_fence_after();
     }
     float mx = -INFINITY;
 #pragma unroll kHeld
@@ -284,18 +290,24 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
         mx = fmaxf(mx, x[i]);
         vr[i] = __float_as_uint(x[i]);
       }
-      if constexpr (!kHold) tc_st<kRun>(t_s + static_cast<uint32_t>(h), vr);
+      if constexpr (!kHold) tc_st<kRun>(t_p + static_cast<uint32_t>(h), vr);
     }
-    if constexpr (!kHold) tc_wait_st();
+    if constexpr (!kHold) {
+      tc_wait_st();
+      tc_fence_before();
+    }
     __syncwarp();
     // the scales are in what was stored, or in the maximum
-    if (lane == 0 && (!kHold || !(mx > INFINITY))) mbar_arrive(&sh.meta_free[slot]);
+    if (lane == 0 && (!kHold || !(mx > INFINITY))) {
+      mbar_arrive(&sh.meta_free[slot]);
+      if (!kHold) mbar_arrive(&sh.s_free[first]);
+    }
     const float mn = fmaxf(m, mx);
     const float base = mn == -INFINITY ? 0.f : mn;
     l *= ex2(m - base);
     m = mn;
     const float sub = static_cast<float>(kPShift) - base;
-    // the buffer's last tile has been multiplied, and its maximum read
+    // the buffer's last tile has been multiplied (kHold), and its maximum read
     wait2(&sh.p_free[first], ph ^ 1u, &sh.m_free[first], ph ^ 1u, dead);
     tc_fence_after();
     sh.x[0][first][row] = m;
@@ -304,33 +316,28 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
     for (int r = 0; r < kTileKeys / kRun; ++r) {
       uint32_t(&vr)[kRun] = v[kHold ? r : 0];
       if constexpr (!kHold) {
-        tc_ld<kRun>(t_s + static_cast<uint32_t>(r * kRun), vr);
+        tc_ld<kRun>(t_p + static_cast<uint32_t>(r * kRun), vr);
         tc_wait_ld();
       }
 #pragma unroll
       for (int e = 0; e < kRun; e += 16) {
-        uint32_t hi[8], lo[8];
+        uint32_t w[16];              // hi, then lo
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           float2 a = __fadd2_rn(bits2(vr[e + i], vr[e + i + 1]), make_float2(sub, sub));
           a.x = ex2(a.x);
           a.y = ex2(a.y);
           sum = __fadd2_rn(sum, a);
-          split2(a, hi[i / 2], lo[i / 2]);
+          split2(a, w[i / 2], w[8 + i / 2]);
         }
-        const uint32_t at = t_p + static_cast<uint32_t>((r * kRun + e) / 2);
-        tc_st<8>(at, hi);
-        tc_st<8>(at + 32u, lo);
+        tc_st<16>(t_p + static_cast<uint32_t>(r * kRun + e), w);
       }
     }
     l += sum.x + sum.y;
     tc_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh.p_ready[first]);
-      if (!kHold) mbar_arrive(&sh.s_free[first]);
-    }
+    if (lane == 0) mbar_arrive(&sh.p_ready[first]);
   }
   sh.x[0][first][row] = m;
   sh.x[1][first][row] = l;
