@@ -62,8 +62,8 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
 // Rows whose largest scaled value is in [2^-3, 65504] keep their 22 bits with it, which
 // one vote checks; the others, 2^8 times larger or 2^10 times smaller than that run, are
 // rare: such a key gets a scale of its own, such a value row is left out of the tile and
-// added at the end in f32.  32 rows against 32768 keys of 4 heads of 256: 70 us, 3.8 TB/s
-// (268 MB at the copy rate: 40 us), 8300 cycles a tile.
+// added at the end in f32.  64 rows against 32768 keys of 4 heads of 256: 67 us, 4.0 TB/s
+// (268 MB at the copy rate: 40 us), some 8000 cycles a tile.
 template <int kHd>
 struct PrefixCfg : MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1> {
   using Base = MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1>;
@@ -487,9 +487,10 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
 // one costs three trips to memory however long it is: with 128 keys an item, four
 // sequences of up to 130 keys took 10.6 us.
 //
-// This kernel does not need the shared part's results: it runs beside that kernel and
-// waits for it only at its end, so that the joining kernel behind finds both done.  (The
-// shared part lets it start only after everything before the call has completed.)
+// This kernel does not need the shared part's results: it runs beside that kernel, on the
+// SMs that one leaves free or has left, and waits for it only at its end, so that the joining
+// kernel behind finds both done.  (The shared part lets it start only after everything before
+// the call has completed.)
 template <int kPL, int kG>
 __global__ void __launch_bounds__(kOwnWarps * 32)
     own_part_kernel(const __grid_constant__ PrefixParams p) {

@@ -354,7 +354,7 @@ def test_prompt_outlier_tokens():
     check_prompt(q, k, v, [0, 200], out, 0.125)
 
 
-# the same again with enough (query, key) pairs for the tensor cores (2^18)
+# the same again with enough (query, key) pairs for the tensor cores (over 2^16)
 @pytest.mark.parametrize("nq,nkv,hd", [(1, 1, 32), (4, 4, 128), (8, 2, 64), (6, 3, 32), (16, 4, 128),
                                        (3, 1, 256), (2, 1, 64), (4, 1, 256), (3, 1, 128)])
 @pytest.mark.parametrize("lens", [[777], [640, 1, 333], [65, 2, 900, 64]])
