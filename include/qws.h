@@ -297,7 +297,8 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   out overlaps none of q, k and v.  scale and, with a softcap, scale / softcap
  *   finite (in qws_prefix_attention too).
  *   ws: device, 16-byte aligned, >= qws_prompt_attention_workspace_bytes of
- *   the same arguments (0: may be NULL).  Keys that a row does not see may
+ *   the same arguments (0: may be NULL).  Scratch: calls that overlap, or
+ *   captured graphs that do, need one each.  Keys that a row does not see may
  *   hold anything, infinities and NaN included.
  *   Accuracy, here and in qws_prefix_attention: f32 sums; a score is within
  *   (head_dim + 32) 2^-24 max_t sum_i |scale q_i k_ti|, whichever kernel runs (on

@@ -641,6 +641,64 @@ def test_prefix_one_sequence_equals_kv_attention():
         assert torch.all((x - want).abs() <= 2e-5)
 
 
+# ------------------------------------------------------------------ long buffers
+def spread(t, dim, room):
+    """t in a buffer where neighbours along dim are room elements of t's rows apart."""
+    shape = list(t.shape)
+    shape[dim] = room
+    big = torch.empty(shape, device="cuda", dtype=t.dtype)
+    big.narrow(dim, 0, t.shape[dim]).copy_(t)
+    return big
+
+
+def test_offsets_beyond_32_bits():
+    # each operator on buffers of 9 to 12 GB, of which little is used: the same bits as compact
+    g = gen(46)
+    nq, nkv, hd, P = 8, 4, 64, 700
+    room = 2 ** 31 // (3 * hd) + 64
+    kp = normal(g, nkv, P, hd)
+    big = spread(kp, 1, room)
+    assert big.stride(0) * 3 > 2 ** 31
+    q, own = normal(g, 2, nq, hd), normal(g, 2, nkv, 40, hd)
+    want = ops.prefix_attention(q, kp, kp, P, own, own, [40, 9], 0.1)
+    assert torch.equal(ops.prefix_attention(q, big, big, P, own, own, [40, 9], 0.1), want)
+    qp = normal(g, 600, nq, hd)
+    for n in (30, 600):                                    # either form of prompt_attention
+        k = kp[:, :n].transpose(0, 1)
+        want = ops.prompt_attention(qp[:n], k, k, [0, n], 0.1)
+        far = big[:, :n].transpose(0, 1)
+        assert torch.equal(ops.prompt_attention(qp[:n], far, far, [0, n], 0.1), want)
+    del big, far
+    big = spread(own, 2, room // 2)
+    want = ops.prefix_attention(q, kp, kp, P, own, own, [40, 9], 0.1)
+    assert torch.equal(ops.prefix_attention(q, kp, kp, P, big, big, [40, 9], 0.1), want)
+    assert torch.equal(ops.prefix_attention(q, kp, kp, 3, big, big, [40, 9], 0.1),
+                       ops.prefix_attention(q, kp, kp, 3, own, own, [40, 9], 0.1))
+    del big
+    # tokens far apart, in and out
+    wide = torch.empty(600, 2 ** 31 // 590 // 64 * 64, device="cuda")
+    assert wide.stride(0) * 599 > 2 ** 31
+    qw = wide[:, :nq * hd].unflatten(1, (nq, hd))
+    ow = wide[:, 1024:1024 + nq * hd].unflatten(1, (nq, hd))
+    qw.copy_(qp)
+    k = kp[:, :600].transpose(0, 1)
+    want = ops.prompt_attention(qp, k, k, [0, 600], 0.1)
+    assert torch.equal(ops.prompt_attention(qw, k, k, [0, 600], 0.1, out=ow), want)
+    pos = torch.arange(600, device="cuda")
+    a, b = ops.qk_norm_rope(qp, k, pos, hd, 1e4)
+    c, d = ops.qk_norm_rope(qw, k, pos, hd, 1e4, q_out=ow)
+    assert torch.equal(a, c) and torch.equal(b, d)
+    del wide, qw, ow, c
+    rows = torch.from_numpy(synth.q8_0_matrix(synth.rng(W_PROMPT, 47), 3, 2560)).cuda().view(3, -1)
+    table = torch.empty(900000, rows.shape[1], dtype=torch.uint8, device="cuda")
+    tok = torch.tensor([5, 800001, 899999], device="cuda")
+    table[tok] = rows
+    want = ops.embed_tokens(ops.Q8_0, rows, torch.arange(3, device="cuda"), 3, 2560)
+    assert torch.equal(ops.embed_tokens(ops.Q8_0, table, tok, 900000, 2560), want)
+    del table
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ streams, graphs, refusals
 def test_prompt_ops_on_another_stream_and_in_a_graph():
     g = gen(40)
@@ -704,6 +762,32 @@ def test_prefix_right_behind_what_makes_its_input():
         torch.cuda.synchronize()
         same = torch.equal(step(src[i % 2]), want[i % 2])
         assert same, i
+
+
+def test_one_workspace_for_calls_in_a_row_and_two_streams():
+    g = gen(48)
+    ws = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    calls = []
+    for i, (n, nq, nkv, hd) in enumerate([(900, 8, 4, 256), (700, 4, 2, 64), (300, 16, 4, 128)]):
+        q, k, v = normal(g, n, nq, hd), normal(g, n, nkv, hd), normal(g, n, nkv, hd)
+        calls.append(lambda q=q, k=k, v=v, n=n, **kw: ops.prompt_attention(q, k, v, [0, 40, n], 0.1,
+                                                                           **kw))
+        kp, kc = normal(g, nkv, 2000 + i, hd), normal(g, 6, nkv, 300, hd)
+        calls.append(lambda q=q, kp=kp, kc=kc, **kw: ops.prefix_attention(
+            q[:6], kp, kp, kp.shape[1], kc, kc, [300, 0, 31, 200, 1, 64], 0.1, 20.0, **kw))
+    want = [c().clone() for c in calls]
+    torch.cuda.synchronize()
+    got = [c(workspace=ws) for _ in range(5) for c in calls]       # nothing waits in between
+    torch.cuda.synchronize()
+    for i, t in enumerate(got):
+        assert torch.equal(t, want[i % len(calls)]), i
+    side = [torch.cuda.Stream() for _ in range(2)]
+    half = ws.numel() // 2
+    got = [c(workspace=ws[i * half:(i + 1) * half], stream=s)
+           for _ in range(5) for c in calls for i, s in enumerate(side)]
+    torch.cuda.synchronize()
+    for i, t in enumerate(got):
+        assert torch.equal(t, want[i // 2 % len(calls)]), i
 
 
 def test_prompt_refusals():
