@@ -17,7 +17,9 @@ struct SeqTab {
   int n;
   int q0[kMaxSeqs + 1];     // first query token of sequence s
   int k0[kMaxSeqs + 1];     // first key of sequence s
-  int item[kMaxSeqs + 1];   // first work item of sequence s
+  int item[kMaxSeqs + 1];   // first work item of the sequence order[i]
+  int order[kMaxSeqs];      // sequences, those with the most keys first
+  int first[kMaxSeqs];      // first work item of sequence s
   int ktile[kMaxSeqs + 1];  // first 64-key tile of sequence s
 };
 
