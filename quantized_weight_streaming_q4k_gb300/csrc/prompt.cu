@@ -20,9 +20,10 @@ __device__ unsigned g_err_prompt;
 // A tile is `rows` query rows of one kv head: tok = rows / group tokens with
 // the group's heads side by side, row r = token r / group, head r % group.  Its
 // keys are cut into pieces of `chunk`; an item is one piece.  The sequences with the most
-// keys come first (a ragged batch of 12, heads of 256: 88 -> 79 us).  A sequence's items come by piece, first every tile's piece 0, the longest tile first, then
-// piece 1 of the tiles that have one, and so on.  A tile of one piece writes out, the
-// others leave partials that prompt_merge_kernel joins.
+// keys come first (a ragged batch of 12, heads of 256: 88 -> 79 us).  A sequence's items come
+// by piece, first every tile's piece 0, the longest tile first, then piece 1 of the tiles that
+// have one, and so on.  A tile of one piece writes out, the others leave partials that
+// prompt_merge_kernel joins.
 struct PromptParams {
   qws_heads q, k, v, out;
   float* part;

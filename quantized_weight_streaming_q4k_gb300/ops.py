@@ -406,7 +406,8 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
         L.qws_prefix_attention_workspace_bytes(n_prefix, lens, B, n_q, n_kv, hd), workspace, dev,
         stream)
     check(L.qws_prefix_attention(
-        C.byref(qh), kp, vp, shape_p[1], n_prefix, kc, vc, shape_c[2], lens, C.byref(oh), B, n_q, n_kv, hd, scale, softcap,
+        C.byref(qh), kp, vp, shape_p[1], n_prefix, kc, vc, shape_c[2], lens, C.byref(oh), B, n_q,
+        n_kv, hd, scale, softcap,
         None if ws is None else ws.data_ptr(), nbytes, stream_handle(stream)))
     return out
 
