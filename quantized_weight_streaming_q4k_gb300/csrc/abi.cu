@@ -432,7 +432,7 @@ qws_status check_offsets(const char* fn, const char* name, const int64_t* cu, in
 qws_status check_scale(const char* fn, float scale, float softcap) {
   if (!std::isfinite(scale) || !(softcap >= 0.f) || !std::isfinite(softcap))
     return fail(QWS_ERR_SHAPE, "%s: scale must be finite and softcap >= 0", fn);
-  // the tensor cores' form takes scores by scale / softcap: 0 times infinity would be NaN
+  // so far below the scale, a softcap leaves nothing of a score but its sign
   if (softcap > 0.f && !std::isfinite(scale / softcap))
     return fail(QWS_ERR_SHAPE, "%s: scale / softcap must be finite", fn);
   return QWS_OK;

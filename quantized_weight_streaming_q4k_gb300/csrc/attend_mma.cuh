@@ -144,19 +144,26 @@ __device__ __forceinline__ void split2(float2 x, uint32_t& hi, uint32_t& lo) {
   lo = pack_f16x2(r.x, r.y);
 }
 
-// y = scale * tanh(y), for a thread's scores of a tile.  tanh(y) = y P(y^2), P fitted to
-// tanh(y) / y in y^2 with a relative error below 6e-9 (1e-7 with the roundings): with four
-// terms while |y| <= 1/4 in the whole warp, which scores well within the cap are, with
-// eight to 1; beyond, 1 - 2 / (1 + e^2|y|), which is 1.2e-7 absolute on values above 0.76.
-// The library's tanhf costs some 60 instructions a score here, four times the rest of the
-// softmax; this 4 or 7.
+// The softcap of a thread's scores of a tile, x in units of log 2: with c = cap log2 e and
+// y = x / c, c tanh(y) = x P(y^2).  P is fitted to tanh(y) / y in y^2: with four terms, which
+// hold it to 6e-9 while |y| <= 1/4 in the whole warp (scores well within the cap are), with
+// eight to 1, where they leave 2.3e-8 (tanh in f32: 9e-8 and 1.2e-7 with the roundings);
+// beyond, 1 - 2 / (1 + e^2|y|), which is 1.2e-7 absolute on values above 0.76.  The library's
+// tanhf costs some 60 instructions a score here, four times the rest of the softmax; this 4
+// or 7.  As a factor on x, P loses nothing where the cap is so far above the scores that y,
+// or 1 / c, is subnormal or zero: it is 1 there.
+struct SoftCap {
+  float c, inv;
+  __device__ __forceinline__ explicit SoftCap(float cap)
+      : c(cap * kLog2e), inv(fminf(1.f / (cap * kLog2e), 3.4028235e38f)) {}   // 0 * inf is NaN
+};
 template <int kN>
-__device__ __forceinline__ float2 tanh_poly(float2 y, const float (&c)[kN]) {
+__device__ __forceinline__ float2 tanh_ratio(float2 y, const float (&c)[kN]) {
   const float2 z = __fmul2_rn(y, y);
   float2 p = make_float2(c[kN - 1], c[kN - 1]);
 #pragma unroll
   for (int i = kN - 2; i >= 0; --i) p = __ffma2_rn(p, z, make_float2(c[i], c[i]));
-  return __fmul2_rn(y, p);
+  return p;
 }
 __device__ __forceinline__ float tanh_big(float y) {
   float r;
@@ -164,33 +171,35 @@ __device__ __forceinline__ float tanh_big(float y) {
   return copysignf(1.f - 2.f * r, y);
 }
 template <int kN>
-__device__ __forceinline__ void tanh_scaled(float (&y)[kN], float scale) {
+__device__ __forceinline__ void soft_caps(float (&x)[kN], SoftCap cap) {
   constexpr float kSmall[4] = {1.0f, -0.33333206f, 0.13323133f, -0.051327724f};
   constexpr float kAll[8] = {1.0f,          -0.333332777f,   0.133321598f,  -0.0538709126f,
                              0.0214648172f, -0.00791743957f, 0.00228222599f, -0.000353344454f};
-  const float2 s = make_float2(scale, scale);
-  float a = fabsf(y[0]);
+  const float2 inv = make_float2(cap.inv, cap.inv);
+  float a = fabsf(x[0]);
 #pragma unroll
-  for (int i = 1; i < kN; ++i) a = fmaxf(a, fabsf(y[i]));
+  for (int i = 1; i < kN; ++i) a = fmaxf(a, fabsf(x[i]));
+  a *= cap.inv;
   if (!__any_sync(0xFFFFFFFFu, a > 0.25f)) {
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {
-      const float2 r = __fmul2_rn(tanh_poly(make_float2(y[i], y[i + 1]), kSmall), s);
-      y[i] = r.x;
-      y[i + 1] = r.y;
+      const float2 v = make_float2(x[i], x[i + 1]);
+      const float2 r = __fmul2_rn(v, tanh_ratio(__fmul2_rn(v, inv), kSmall));
+      x[i] = r.x;
+      x[i + 1] = r.y;
     }
   } else {
     const bool big = __any_sync(0xFFFFFFFFu, a > 1.f);
 #pragma unroll
     for (int i = 0; i < kN; i += 2) {
-      float2 t = tanh_poly(make_float2(y[i], y[i + 1]), kAll);
+      const float2 v = make_float2(x[i], x[i + 1]), y = __fmul2_rn(v, inv);
+      float2 r = __fmul2_rn(v, tanh_ratio(y, kAll));
       if (big) {
-        t.x = fabsf(y[i]) > 1.f ? tanh_big(y[i]) : t.x;
-        t.y = fabsf(y[i + 1]) > 1.f ? tanh_big(y[i + 1]) : t.y;
+        r.x = fabsf(y.x) > 1.f ? cap.c * tanh_big(y.x) : r.x;
+        r.y = fabsf(y.y) > 1.f ? cap.c * tanh_big(y.y) : r.y;
       }
-      const float2 r = __fmul2_rn(t, s);
-      y[i] = r.x;
-      y[i + 1] = r.y;
+      x[i] = r.x;
+      x[i + 1] = r.y;
     }
   }
 }

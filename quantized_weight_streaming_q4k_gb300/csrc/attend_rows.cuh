@@ -81,8 +81,11 @@ __device__ __forceinline__ float warp_max(float v) {
 // two of differences; running maxima of partial results too.
 constexpr float kLog2e = 1.4426950408889634f;
 
+// tanh(y) is y to less than half a step where |y| < 2^-13; y itself may be subnormal there
 __device__ __forceinline__ float soft_cap(float s, float cap) {
-  return cap > 0.f ? cap * tanhf(s / cap) : s;
+  if (!(cap > 0.f)) return s;
+  const float y = s / cap;
+  return fabsf(y) < 0x1p-13f ? s : cap * tanhf(y);
 }
 
 // A CTA of kRowWarps warps, kR query rows a warp.  Keys come in tiles of 32

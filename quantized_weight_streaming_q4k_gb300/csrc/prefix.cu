@@ -269,7 +269,8 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (
   for (int c = 0; c < Cfg::kNC; ++c)
 #pragma unroll
     for (int i = 0; i < Cfg::kOC / 2; ++i) st.o[c][i] = make_float2(0.f, 0.f);
-  const float rowf = kCap ? qscale * (scale / cap) : qscale * scale * kLog2e;
+  const float rowf = qscale * scale * kLog2e;
+  const SoftCap soft(kCap ? cap : 1.f);
   const uint32_t t_o = lanes + Cfg::kTmO + static_cast<uint32_t>(part * Cfg::kOC);
   float alpha = 1.f, vs = 1.f;
   uint32_t w[kKeys];           // of every 16 keys hi, then lo
@@ -308,7 +309,7 @@ __device__ __forceinline__ void prefix_rows(MmaShared<Cfg>& sh, const uint32_t (
         x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
       }
     }
-    if constexpr (kCap) tanh_scaled<kKeys>(x, cap * kLog2e);
+    if constexpr (kCap) soft_caps<kKeys>(x, soft);
     if ((j + 1) * kTileKeys > keys) {
       const int left = keys - j * kTileKeys - kKeys * part;    // of this thread's keys, how many
 #pragma unroll

@@ -238,7 +238,8 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
   constexpr int kRun = kHold ? 32 : 16, kHeld = kHold ? kTileKeys / kRun : 1;
   dead = !__all_sync(0xFFFFFFFFu, mbar_wait(&sh.q_ready, 0));
   const float qs = q_unscale(sh, row);
-  const float rowf = kCap ? qs * (scale / cap) : qs * scale * kLog2e;
+  const float rowf = qs * scale * kLog2e;
+  const SoftCap soft(kCap ? cap : 1.f);
   uint32_t ph = 0;
 #pragma unroll 1
   for (int j = first; j < n; j += 2, ph ^= 1u) {
@@ -282,7 +283,7 @@ __device__ __forceinline__ bool tile_weights(MmaShared<Cfg>& sh, int first, int 
             __fmul2_rn(bits2(vr[i + 2], vr[i + 3]), __fmul2_rn(make_float2(k.z, k.w), f));
         x[i] = a.x; x[i + 1] = a.y; x[i + 2] = b.x; x[i + 3] = b.y;
       }
-      if constexpr (kCap) tanh_scaled<kRun>(x, cap * kLog2e);
+      if constexpr (kCap) soft_caps<kRun>(x, soft);
       if (masked) {
 #pragma unroll
         for (int i = 0; i < kRun; ++i)
