@@ -3,7 +3,10 @@
 Argument marshalling only: every function passes device pointers, sizes and
 the current CUDA stream to libqws.so; all arithmetic runs in its kernels.
 Outputs are allocated with torch when ``out`` is not given (PyTorch is the
-allocator, the library allocates nothing).
+allocator, the library allocates nothing).  With ``stream`` a call runs on
+that stream in place of the current one: its fresh outputs and workspaces
+belong to it, and the caller makes it wait for the inputs, and the current
+stream for the outputs.
 """
 from __future__ import annotations
 
@@ -45,9 +48,25 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
     return t.data_ptr()
 
 
-def _out(out, shape, like: torch.Tensor) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device, stream, returned: bool = True) -> torch.Tensor:
+    """A fresh tensor for a call's kernels: an output, or (not returned) a workspace.
+
+    It comes from the pool of the stream that the kernels run on.  A block of another
+    stream's pool may have belonged to a tensor that the other stream's queued work still
+    reads or writes, and nothing orders these kernels behind that work.  An output is the
+    current stream's too, so that it may be used there (behind a wait) and freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _out(out, shape, like: torch.Tensor, stream) -> torch.Tensor:
     if out is None:
-        return torch.empty(shape, dtype=torch.float32, device=like.device)
+        return _empty(shape, torch.float32, like.device, stream)
     return out
 
 
@@ -57,7 +76,7 @@ def workspace_bytes(op: int, rows: int = 0, hidden: int = 0, inter: int = 0, bat
 
 
 def _mv(name: str, W, x, rows: int, hidden: int, batch: int, out, stream):
-    y = _out(out, (batch, rows) if batch > 1 else (rows,), x)
+    y = _out(out, (batch, rows) if batch > 1 else (rows,), x, stream)
     fn = getattr(lib(), name)
     check(fn(_dev(W, "W", torch.uint8), _dev(x, "x", torch.float32),
              _dev(y, "y", torch.float32), rows, hidden, batch, stream_handle(stream)))
@@ -75,7 +94,7 @@ def q6k_matvec(W, x, rows: int, hidden: int, batch: int = 1, out=None, stream=No
 
 def matvec(fmt: int, W, x, rows: int, hidden: int, batch: int = 1, split_k: int = 1,
            workspace=None, out=None, stream=None):
-    y = _out(out, (batch, rows) if batch > 1 else (rows,), x)
+    y = _out(out, (batch, rows) if batch > 1 else (rows,), x, stream)
     ws_ptr, ws_bytes = (0, 0) if workspace is None else (_dev(workspace, "workspace"),
                                                           workspace.numel() * workspace.element_size())
     check(lib().qws_matvec(fmt, _dev(W, "W", torch.uint8), _dev(x, "x", torch.float32),
@@ -86,7 +105,7 @@ def matvec(fmt: int, W, x, rows: int, hidden: int, batch: int = 1, split_k: int 
 
 def q4_0_matvec(W, x, rows: int, hidden: int, batch: int = 1, split_k: int = 1, workspace=None,
                 out=None, stream=None):
-    y = _out(out, (batch, rows) if batch > 1 else (rows,), x)
+    y = _out(out, (batch, rows) if batch > 1 else (rows,), x, stream)
     ws_ptr, ws_bytes = (0, 0) if workspace is None else (_dev(workspace, "workspace"),
                                                           workspace.numel() * workspace.element_size())
     check(lib().qws_q4_0_matvec(_dev(W, "W", torch.uint8), _dev(x, "x", torch.float32),
@@ -97,9 +116,9 @@ def q4_0_matvec(W, x, rows: int, hidden: int, batch: int = 1, split_k: int = 1, 
 
 def q4k_qkv_proj(Wq, Wk, Wv, x, hidden: int, q_dim: int, kv_dim: int, out=None, stream=None):
     if out is None:
-        q = torch.empty(q_dim, dtype=torch.float32, device=x.device)
-        k = torch.empty(kv_dim, dtype=torch.float32, device=x.device)
-        v = torch.empty(kv_dim, dtype=torch.float32, device=x.device)
+        q = _empty(q_dim, torch.float32, x.device, stream)
+        k = _empty(kv_dim, torch.float32, x.device, stream)
+        v = _empty(kv_dim, torch.float32, x.device, stream)
     else:
         q, k, v = out
     check(lib().qws_q4k_qkv_proj(_dev(Wq, "Wq", torch.uint8), _dev(Wk, "Wk", torch.uint8),
@@ -114,24 +133,22 @@ def quantize_q8_0(x, n: int, batch: int = 1, out=None, stream=None):
     """x [batch, n] (or [n]) f32 -> Q8_0 blocks, uint8 [batch, n / 32 * 34] (or flat)."""
     nbytes = n // 32 * 34
     if out is None:
-        out = torch.empty((batch, nbytes) if batch > 1 else (nbytes,), dtype=torch.uint8,
-                          device=x.device)
+        out = _empty((batch, nbytes) if batch > 1 else (nbytes,), torch.uint8, x.device, stream)
     check(lib().qws_quantize_q8_0(_dev(x, "x", torch.float32), _dev(out, "xq", torch.uint8), n,
                                   batch, stream_handle(stream)))
     return out
 
 
-def _xq_out(out, n: int, batch: int, like):
+def _xq_out(out, n: int, batch: int, like, stream):
     if out is not None:
         return out
     nbytes = n // 32 * 34
-    return torch.empty((batch, nbytes) if batch > 1 else (nbytes,), dtype=torch.uint8,
-                       device=like.device)
+    return _empty((batch, nbytes) if batch > 1 else (nbytes,), torch.uint8, like.device, stream)
 
 
 def rms_norm_q8(x, w, eps: float, n: int, batch: int = 1, out=None, stream=None):
     """Q8_0 blocks of rms_norm(x, w) ([batch, n] or [n] f32 -> uint8 [.., n / 32 * 34])."""
-    xq = _xq_out(out, n, batch, x)
+    xq = _xq_out(out, n, batch, x, stream)
     check(lib().qws_rms_norm_q8(_dev(x, "x", torch.float32), _dev(w, "w", torch.float32),
                                 _dev(xq, "xq", torch.uint8), n, eps, batch,
                                 stream_handle(stream)))
@@ -140,7 +157,7 @@ def rms_norm_q8(x, w, eps: float, n: int, batch: int = 1, out=None, stream=None)
 
 def residual_rms_norm_q8(h, y, w, eps: float, n: int, batch: int = 1, out=None, stream=None):
     """h += y (in place), then the Q8_0 blocks of rms_norm(h, w)."""
-    xq = _xq_out(out, n, batch, h)
+    xq = _xq_out(out, n, batch, h, stream)
     check(lib().qws_residual_rms_norm_q8(_dev(h, "h", torch.float32), _dev(y, "y", torch.float32),
                                          _dev(w, "w", torch.float32), _dev(xq, "xq", torch.uint8),
                                          n, eps, batch, stream_handle(stream)))
@@ -149,7 +166,7 @@ def residual_rms_norm_q8(h, y, w, eps: float, n: int, batch: int = 1, out=None, 
 
 def q8_matvec(wfmt: int, W, xq, rows: int, hidden: int, batch: int = 1, out=None, stream=None):
     """y = W @ xq for Q4_0 / Q8_0 weights and Q8_0 activations xq."""
-    y = _out(out, (batch, rows) if batch > 1 else (rows,), xq)
+    y = _out(out, (batch, rows) if batch > 1 else (rows,), xq, stream)
     check(lib().qws_q8_matvec(wfmt, _dev(W, "W", torch.uint8), _dev(xq, "xq", torch.uint8),
                               _dev(y, "y", torch.float32), rows, hidden, batch,
                               stream_handle(stream)))
@@ -159,9 +176,9 @@ def q8_matvec(wfmt: int, W, xq, rows: int, hidden: int, batch: int = 1, out=None
 def q8_qkv_proj(wfmt: int, Wq, Wk, Wv, xq, hidden: int, q_dim: int, kv_dim: int, out=None,
                 stream=None):
     if out is None:
-        q = torch.empty(q_dim, dtype=torch.float32, device=xq.device)
-        k = torch.empty(kv_dim, dtype=torch.float32, device=xq.device)
-        v = torch.empty(kv_dim, dtype=torch.float32, device=xq.device)
+        q = _empty(q_dim, torch.float32, xq.device, stream)
+        k = _empty(kv_dim, torch.float32, xq.device, stream)
+        v = _empty(kv_dim, torch.float32, xq.device, stream)
     else:
         q, k, v = out
     check(lib().qws_q8_qkv_proj(wfmt, _dev(Wq, "Wq", torch.uint8), _dev(Wk, "Wk", torch.uint8),
@@ -176,10 +193,10 @@ def q4k_prefill_matmul(W, X, rows: int, hidden: int, n_tokens: int, workspace=No
                        stream=None):
     """Y [n_tokens, rows] = X [n_tokens, hidden] @ dequant_Q4_K(W)^T on the tensor cores
     (f16 operands, f32 accumulation)."""
-    Y = _out(out, (n_tokens, rows), X)
+    Y = _out(out, (n_tokens, rows), X, stream)
     need = workspace_bytes(OP_PREFILL, 0, hidden, 0, n_tokens, 0)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+        workspace = _empty(max(need, 16), torch.uint8, X.device, stream, returned=False)
     check(lib().qws_q4k_prefill_matmul(
         _dev(W, "W", torch.uint8), _dev(X, "X", torch.float32), _dev(Y, "Y", torch.float32),
         rows, hidden, n_tokens, _dev(workspace, "workspace"),
@@ -207,11 +224,10 @@ def kv_attention(q, k_cache, v_cache, n_q_heads: int, n_kv_heads: int, head_dim:
                  max_seq: int, n_ctx: int, scale: float, softcap: float = 0.0, workspace=None,
                  out=None, stream=None):
     """One query token q [n_q_heads, head_dim] over cache positions 0 .. n_ctx-1."""
-    y = out if out is not None else torch.empty((n_q_heads, head_dim), dtype=torch.float32,
-                                                device=q.device)
+    y = _out(out, (n_q_heads, head_dim), q, stream)
     need = workspace_bytes(OP_KV_ATTENTION, n_ctx, head_dim, n_q_heads, n_kv_heads)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 16), torch.uint8, q.device, stream, returned=False)
     check(lib().qws_kv_attention(
         _dev(q, "q", torch.float32), _dev(k_cache, "k_cache", torch.float32),
         _dev(v_cache, "v_cache", torch.float32), _dev(y, "out", torch.float32), n_q_heads,
@@ -274,24 +290,15 @@ def _host_ints(v, name: str):
 
 
 def _workspace(need: int, workspace, dev: int, stream):
-    """(tensor, bytes) of the caller's workspace, or of a fresh one kept for the stream."""
+    """(tensor, bytes) of the caller's workspace, or of a fresh one."""
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty(need, torch.uint8, dev, stream, returned=False)
     else:
         _here(workspace, "workspace", dev)
         _dev(workspace, "workspace")
     return workspace, workspace.numel() * workspace.element_size()
-
-
-def _new(shape, dev: int, stream) -> torch.Tensor:
-    t = torch.empty(shape, dtype=torch.float32, device=dev)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
 
 
 def embed_tokens(fmt: int, W, tokens, vocab: int, hidden: int, scale: float = 1.0, out=None,
@@ -306,7 +313,7 @@ def embed_tokens(fmt: int, W, tokens, vocab: int, hidden: int, scale: float = 1.
     if W.numel() < vocab * (hidden // block) * size:
         raise ValueError(f"W has {W.numel()} bytes, {vocab} rows of {hidden} need "
                          f"{vocab * (hidden // block) * size}")
-    out = _new((n, hidden), dev, stream) if out is None else out
+    out = _empty((n, hidden), torch.float32, dev, stream) if out is None else out
     check(lib().qws_embed_tokens(fmt, _dev(W, "W", torch.uint8),
                                  _vec(tokens, "tokens", dev, torch.int64, n),
                                  _vec(out, "out", dev, torch.float32, n * hidden), vocab, hidden,
@@ -325,8 +332,8 @@ def qk_norm_rope(q, k, positions, rot_dim: int, base: float, w_q=None, w_k=None,
     n_kv = k.shape[1]
     if k.shape[0] != n or k.shape[2] != hd:
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not match")
-    q_out = _new((n, n_q, hd), dev, stream) if q_out is None else q_out
-    k_out = _new((n, n_kv, hd), dev, stream) if k_out is None else k_out
+    q_out = _empty((n, n_q, hd), torch.float32, dev, stream) if q_out is None else q_out
+    k_out = _empty((n, n_kv, hd), torch.float32, dev, stream) if k_out is None else k_out
     qo, ko = _heads(q_out, "q_out", dev, n_q, hd), _heads(k_out, "k_out", dev, n_kv, hd)
     if q_out.shape[0] != n or k_out.shape[0] != n:
         raise ValueError(f"q_out and k_out must have {n} tokens")
@@ -358,7 +365,7 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu
         raise ValueError("cu_seqlens (and cu_seqlens_k) hold one offset more than sequences")
     if max(cu) > q.shape[0] or max(ck) > min(k.shape[0], v.shape[0]):
         raise ValueError("the offsets pass the end of q, k or v")
-    out = _new(q.shape, dev, stream) if out is None else out
+    out = _empty(q.shape, torch.float32, dev, stream) if out is None else out
     oh = _heads(out, "out", dev, n_q, hd)
     if max(cu) > out.shape[0]:
         raise ValueError("the offsets pass the end of out")
@@ -395,7 +402,7 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
     lens = _host_ints(n_ctx, "n_ctx")
     if len(lens) != B:
         raise ValueError(f"q has {B} rows, n_ctx {len(lens)}")
-    out = _new(q.shape, dev, stream) if out is None else out
+    out = _empty(q.shape, torch.float32, dev, stream) if out is None else out
     oh = _heads(out, "out", dev, n_q, hd)
     if out.shape[0] != B:
         raise ValueError(f"out must have {B} rows")
@@ -413,7 +420,7 @@ def prefix_attention(q, k_prefix, v_prefix, n_prefix: int, k_caches, v_caches, n
 
 
 def q4k_ffn_gate_up_geglu(Wg, Wu, x, hidden: int, inter: int, out=None, stream=None):
-    m = _out(out, (inter,), x)
+    m = _out(out, (inter,), x, stream)
     check(lib().qws_q4k_ffn_gate_up_geglu(_dev(Wg, "Wg", torch.uint8), _dev(Wu, "Wu", torch.uint8),
                                           _dev(x, "x", torch.float32), _dev(m, "m", torch.float32),
                                           hidden, inter, stream_handle(stream)))
@@ -422,10 +429,10 @@ def q4k_ffn_gate_up_geglu(Wg, Wu, x, hidden: int, inter: int, out=None, stream=N
 
 def q4k_ffn_gate_up_geglu_down(Wg, Wu, Wd, wd_fmt: int, x, hidden: int, inter: int,
                                workspace=None, out=None, stream=None):
-    y = _out(out, (hidden,), x)
+    y = _out(out, (hidden,), x, stream)
     need = workspace_bytes(OP_FFN, 0, hidden, inter, 1, 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream, returned=False)
     check(lib().qws_q4k_ffn_gate_up_geglu_down(
         _dev(Wg, "Wg", torch.uint8), _dev(Wu, "Wu", torch.uint8), _dev(Wd, "Wd", torch.uint8),
         wd_fmt, _dev(x, "x", torch.float32), _dev(y, "y", torch.float32), hidden, inter,
@@ -435,7 +442,7 @@ def q4k_ffn_gate_up_geglu_down(Wg, Wu, Wd, wd_fmt: int, x, hidden: int, inter: i
 
 
 def q4k_ffn_gate_up_silu(Wg, Wu, x, hidden: int, inter: int, out=None, stream=None):
-    m = _out(out, (inter,), x)
+    m = _out(out, (inter,), x, stream)
     check(lib().qws_q4k_ffn_gate_up_silu(_dev(Wg, "Wg", torch.uint8), _dev(Wu, "Wu", torch.uint8),
                                          _dev(x, "x", torch.float32), _dev(m, "m", torch.float32),
                                          hidden, inter, stream_handle(stream)))
@@ -444,10 +451,10 @@ def q4k_ffn_gate_up_silu(Wg, Wu, x, hidden: int, inter: int, out=None, stream=No
 
 def q4k_ffn_gate_up_silu_down(Wg, Wu, Wd, wd_fmt: int, x, hidden: int, inter: int,
                               workspace=None, out=None, stream=None):
-    y = _out(out, (hidden,), x)
+    y = _out(out, (hidden,), x, stream)
     need = workspace_bytes(OP_FFN, 0, hidden, inter, 1, 0)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _empty(need, torch.uint8, x.device, stream, returned=False)
     check(lib().qws_q4k_ffn_gate_up_silu_down(
         _dev(Wg, "Wg", torch.uint8), _dev(Wu, "Wu", torch.uint8), _dev(Wd, "Wd", torch.uint8),
         wd_fmt, _dev(x, "x", torch.float32), _dev(y, "y", torch.float32), hidden, inter,
@@ -459,7 +466,7 @@ def q4k_ffn_gate_up_silu_down(Wg, Wu, Wd, wd_fmt: int, x, hidden: int, inter: in
 def residual_rms_norm(h, y, w, eps: float, batch: int = 1, out=None, stream=None):
     """h += y (in place), returns x = rms_norm(h, w)."""
     n = h.numel() // batch
-    x = _out(out, tuple(h.shape), h)
+    x = _out(out, tuple(h.shape), h, stream)
     check(lib().qws_residual_rms_norm(_dev(h, "h", torch.float32), _dev(y, "y", torch.float32),
                                       _dev(w, "w", torch.float32), _dev(x, "x", torch.float32), n,
                                       float(eps), batch, stream_handle(stream)))
@@ -467,7 +474,7 @@ def residual_rms_norm(h, y, w, eps: float, batch: int = 1, out=None, stream=None
 
 
 def rms_norm(x, w, eps: float, batch: int = 1, out=None, stream=None):
-    y = _out(out, tuple(x.shape), x)
+    y = _out(out, tuple(x.shape), x, stream)
     n = x.numel() // batch
     check(lib().qws_rms_norm(_dev(x, "x", torch.float32), _dev(w, "w", torch.float32),
                              _dev(y, "y", torch.float32), n, float(eps), batch,
@@ -519,7 +526,7 @@ def decode_chain(layers, h, dims: dict, workspace=None, stream=None, w_final=Non
             raise ValueError(f"{name} has {t.numel()} elements, hidden is {dims['hidden']}")
     need = workspace_bytes(OP_DECODE_CHAIN, 0, dims["hidden"], dims["inter"], 1, 0)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
+        workspace = _empty(max(need, 1), torch.uint8, h.device, stream, returned=False)
     nbytes = workspace.numel() * workspace.element_size()
     if w_final is None and hn is None:
         check(lib().qws_decode_chain(arr, n, _dev(h, "h", torch.float32), C.byref(D),
@@ -562,7 +569,7 @@ def decode_kv(layers, h, dims: dict, k_caches, v_caches, max_seq: int, pos: int,
                     int(rot_dim), float(rope_base), float(attn_scale), float(softcap))
     need = decode_kv_workspace_bytes(dims, max_seq)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
+        workspace = _empty(max(need, 1), torch.uint8, h.device, stream, returned=False)
     check(lib().qws_decode_kv(arr, n, _dev(h, "h", torch.float32), C.byref(D), C.byref(kv),
                               _dev(workspace, "workspace"),
                               workspace.numel() * workspace.element_size(),
