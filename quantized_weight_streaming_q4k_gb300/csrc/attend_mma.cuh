@@ -215,17 +215,18 @@ __device__ __forceinline__ bool finite_bits(float x) {
 }
 
 template <class Cfg>
-__device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh, uint32_t full_count) {
+__device__ __forceinline__ void mma_init_barriers(MmaShared<Cfg>& sh, uint32_t key_count,
+                                                  uint32_t value_count) {
   for (int s = 0; s < Cfg::kStages; ++s) {
-    mbar_init(&sh.k_full[s], full_count);
+    mbar_init(&sh.k_full[s], key_count);
     mbar_init(&sh.k_empty[s], 1);
-    mbar_init(&sh.v_full[s], full_count);
+    mbar_init(&sh.v_full[s], value_count);
     mbar_init(&sh.v_empty[s], 1);
   }
   for (int s = 0; s < Cfg::kMetas; ++s) {
-    mbar_init(&sh.meta_full[s], full_count);
+    mbar_init(&sh.meta_full[s], key_count);
     mbar_init(&sh.meta_free[s], Cfg::kSoftWarps);
-    mbar_init(&sh.vmeta_full[s], full_count);
+    mbar_init(&sh.vmeta_full[s], value_count);
     mbar_init(&sh.vmeta_free[s], Cfg::kRowsWarps);
   }
   for (int s = 0; s < 2; ++s) {
@@ -669,6 +670,35 @@ __device__ __forceinline__ void pack_keys(const float* K, int64_t stride, int n,
   }
 }
 
+// Which of a tile's value rows share its scale: those within 2^16 of the smallest that is not
+// zero, or those within 2^16 of the largest that is finite, whichever leaves out fewer.  a, b:
+// the largest magnitudes of rows lane and lane + 32, infinite for a row with an infinity or
+// NaN.  By a whole warp, the same in every lane.
+struct ValueScale {
+  uint32_t out[2];       // rows left out
+  float top;             // the largest magnitude of the others
+};
+__device__ __forceinline__ ValueScale choose_value_scale(float a, float b) {
+  float lo = fminf(a > 0.f ? a : INFINITY, b > 0.f ? b : INFINITY);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+  const float hi = warp_max(fmaxf(a == INFINITY ? 0.f : a, b == INFINITY ? 0.f : b));
+  const float top = lo * 65536.0f, low = hi * (1.0f / 65536.0f);     // top: may be infinite
+  const auto count = [](bool x, bool y) {
+    return __popc(__ballot_sync(0xFFFFFFFFu, x)) + __popc(__ballot_sync(0xFFFFFFFFu, y));
+  };
+  const bool big_a = a == INFINITY || a > top, big_b = b == INFINITY || b > top;
+  const bool few_a = a == INFINITY || (a > 0.f && a < low);
+  const bool few_b = b == INFINITY || (b > 0.f && b < low);
+  const bool large = count(big_a, big_b) <= count(few_a, few_b);
+  const bool out_a = large ? big_a : few_a, out_b = large ? big_b : few_b;
+  ValueScale sc;
+  sc.out[0] = __ballot_sync(0xFFFFFFFFu, out_a);
+  sc.out[1] = __ballot_sync(0xFFFFFFFFu, out_b);
+  sc.top = warp_max(fmaxf(out_a ? 0.f : a, out_b ? 0.f : b));
+  return sc;
+}
+
 // Their values, likewise, with one scale for the tile.
 template <class Cfg>
 __device__ __forceinline__ void pack_values(const float* V, int64_t stride, int n, uint8_t* dst,
@@ -691,34 +721,18 @@ __device__ __forceinline__ void pack_values(const float* V, int64_t stride, int 
     if (lane == 0) vmax[warp + 8 * i] = fin ? b : INFINITY;
   }
   __syncthreads();
-  // the rows within 2^16 of the smallest non-zero row, or within 2^16 of the largest that
-  // is finite: whichever leaves out fewer
-  const float a = vmax[lane], b = vmax[lane + 32];
-  float lo = fminf(a > 0.f ? a : INFINITY, b > 0.f ? b : INFINITY);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-  const float hi = warp_max(fmaxf(a == INFINITY ? 0.f : a, b == INFINITY ? 0.f : b));
-  const float top = lo * 65536.0f, low = hi * (1.0f / 65536.0f);     // top: may be infinite
-  const auto count = [](bool x, bool y) {
-    return __popc(__ballot_sync(0xFFFFFFFFu, x)) + __popc(__ballot_sync(0xFFFFFFFFu, y));
-  };
-  const bool big_a = a == INFINITY || a > top, big_b = b == INFINITY || b > top;
-  const bool few_a = a == INFINITY || (a > 0.f && a < low);
-  const bool few_b = b == INFINITY || (b > 0.f && b < low);
-  const bool large = count(big_a, big_b) <= count(few_a, few_b);      // the same in all warps
-  const bool out_a = large ? big_a : few_a, out_b = large ? big_b : few_b;
-  const uint32_t ma = __ballot_sync(0xFFFFFFFFu, out_a), mb = __ballot_sync(0xFFFFFFFFu, out_b);
-  const int e = split_exp(warp_max(fmaxf(out_a ? 0.f : a, out_b ? 0.f : b)));
+  const ValueScale sc = choose_value_scale(vmax[lane], vmax[lane + 32]);      // the same in all warps
+  const int e = split_exp(sc.top);
   if (threadIdx.x == 0) {
     meta->vscale = exp2i(-e);
-    meta->left_out[0] = ma;
-    meta->left_out[1] = mb;
+    meta->left_out[0] = sc.out[0];
+    meta->left_out[1] = sc.out[1];
     meta->pad = 0;
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = warp + 8 * i;
-    const bool out = ((r < 32 ? ma : mb) >> (r & 31)) & 1u;
+    const bool out = ((r < 32 ? sc.out[0] : sc.out[1]) >> (r & 31)) & 1u;
 #pragma unroll
     for (int c = 0; c < kPL; ++c) y[i][c] = out ? 0.f : y[i][c];
     store_split_row<Cfg>(y[i], exp2i(e), r, lane, dst);

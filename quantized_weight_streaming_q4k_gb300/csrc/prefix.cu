@@ -59,10 +59,11 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
 // The converters bound it next (with a maximum over every row and a scale of its own
 // they took 12200 cycles a tile).  So a piece has one scale for its keys and one for its
 // values, taken from its first run of rows: that run's largest value at [2^7, 2^8).
-// Rows whose largest scaled value is in [2^-3, 65504] keep their 22 bits with it, which
+// Rows whose largest scaled value is in [2^-3, 65504], or zero, keep 22 bits with it, which
 // one vote checks; the others, 2^8 times larger or 2^10 times smaller than that run, are
-// rare: such a key gets a scale of its own, such a value row is left out of the tile and
-// added at the end in f32.  64 rows against 32768 keys of 4 heads of 256: 67 us, 4.0 TB/s
+// rare.  Such a key gets a scale of its own.  A tile with such a value row is laid out once
+// more, with a scale of its own, which the tile after next goes on with, by a warp that is
+// there for this (prefix_refit).  64 rows against 32768 keys of 4 heads of 256: 67 us, 4.0 TB/s
 // (268 MB at the copy rate: 40 us), some 8000 cycles a tile.
 template <int kHd>
 struct PrefixCfg : MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1> {
@@ -82,13 +83,16 @@ constexpr int kMaxPieceTiles = 64;
 template <int kHd>
 struct PrefixShared {
   uint64_t stg_full[PrefixCfg<kHd>::kStaging], stg_empty[PrefixCfg<kHd>::kStaging];
+  uint64_t v_done[2];                // the converters are done with a slot's values
   uint32_t left_out[kMaxPieceTiles][2];
+  uint32_t misfit[kMaxPieceTiles];   // the scale in force did not fit the tile's values
+  float scale[2][2];                 // in force, of the keys and of the values of a slot
   float vmax[2][PrefixCfg<kHd>::kConvWarps];
   MmaShared<PrefixCfg<kHd>> mma;
 };
 
 // 640 threads, 96 registers each at launch; per scheduler 2 softmax warps at 160, a
-// helper at 40 and 2 converters at 56: 2 x 160 + 40 + 2 x 56 = 472 of 5 x 96.
+// helper at 48 and 2 converters at 56: 2 x 160 + 48 + 2 x 56 of 5 x 96.
 
 template <int kHd>
 __device__ __forceinline__ void prefix_load(PrefixShared<kHd>& sh, uint8_t* staging,
@@ -139,7 +143,6 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
     if (!dead) dead = !__all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
   };
   bool seen = false;           // the next run of rows was seen to be there
-  float k_scale = 1.f, v_scale = 1.f;           // powers of two
 #pragma unroll 1
   for (int jh = 0; jh < 2 * n; ++jh) {
     const int j = jh >> 1, slot = j & 1;
@@ -153,7 +156,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
           (static_cast<uint32_t>(j / Cfg::kDepth) & 1u) ^ 1u, dead);
     uint8_t* dst = (is_v ? v_ring : k_ring) + stage * Cfg::kUnit;
     TileMeta& meta = sh.mma.meta[slot];
-    uint32_t out_lo = 0, out_hi = 0;              // rows of the tile this warp leaves out
+    bool misfit = false;                          // values that need another scale
 #pragma unroll 1
     for (int r = 0; r < Cfg::kRuns; ++r) {
       const int rows = min(Cfg::kRun, keys - j * kTileKeys - r * Cfg::kRun);
@@ -187,9 +190,11 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
 #pragma unroll
         for (int w = 0; w < Cfg::kConvWarps; ++w) a = fmaxf(a, sh.vmax[is_v][w]);
         const int e = a > 0.f ? max(split_exp(a) - 7, -126) : 0;
-        (is_v ? v_scale : k_scale) = exp2i(e);
+        if (lane < 2) sh.scale[is_v][lane] = exp2i(e);        // by every warp, the same
+        __syncwarp();
       }
-      const float sc = is_v ? v_scale : k_scale;
+      // a power of two; vmeta_free has shown this warp what became of the slot's last tile
+      const float sc = sh.scale[is_v][slot];
       // bit i: row i has a value of 2^-3 or more; bit 31: some value does not fit
       uint32_t has = 0;
 #pragma unroll
@@ -205,7 +210,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
         at.next();
         seen = mbar_test(&sh.stg_full[at.stage], at.phase);
       }
-      float mine = 1.0f / k_scale;        // lane i: 2^-e of key row i
+      float mine = 1.0f / sc;        // lane i: 2^-e of key row i
       float by[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) by[i] = sc;
@@ -217,10 +222,7 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
           const bool in = fin && (am == 0.f || (am * sc >= 0.125f && am * sc <= 65504.f));
           if (in) continue;
           if (is_v) {
-            const int row = r * Cfg::kRun + cw + 8 * i;
-            (row < 32 ? out_lo : out_hi) |= 1u << (row & 31);
-#pragma unroll
-            for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
+            misfit = true;
           } else {
             const int e = split_exp(am);
             by[i] = exp2i(e);
@@ -234,15 +236,94 @@ __device__ __forceinline__ void prefix_convert(PrefixShared<kHd>& sh, const uint
       for (int i = 0; i < kRows; ++i)
         store_split_at<typename Cfg::Base>(x[i], by[i], lane, at_rows + i * 1024 + place);
     }
-    if (is_v) {
-      if ((out_lo | out_hi) && lane < 2) atomicOr(&sh.left_out[j][lane], lane ? out_hi : out_lo);
-      if (cw == 0 && lane == 0) meta.vscale = 1.0f / v_scale;
+    if (is_v && lane == 0) {
+      if (cw == 0) meta.vscale = 1.0f / sh.scale[1][slot];
+      if (misfit) sh.misfit[j] = 1;
     }
     fence_proxy_async_smem();                     // generic stores -> visible to the MMAs
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&(is_v ? sh.mma.v_full : sh.mma.k_full)[stage]);
-      mbar_arrive(is_v ? &sh.mma.vmeta_full[slot] : &sh.mma.meta_full[slot]);
+      if (is_v) {
+        mbar_arrive(&sh.v_done[slot]);            // prefix_refit hands them on
+      } else {
+        mbar_arrive(&sh.mma.k_full[stage]);
+        mbar_arrive(&sh.mma.meta_full[slot]);
+      }
+    }
+  }
+  if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttLoad);
+}
+
+// One warp hands the converters' tiles of values on to the MMAs.  A tile that the scale in force
+// did not fit it lays out once more, over what is there, from memory: with the scale and the
+// rows left out that pack_values would choose.  The tile after next goes on with that scale, its
+// largest value at [2^7, 2^8).  It takes 25 us at head_dim 256 (9 at 64), the time of some six
+// tiles: a value row 2^12 times the others among a piece's first (16 rows over 16384 positions,
+// 4 heads of 256) costs 47 -> 123 us, a scale that is wrong for every tile 47 -> 190; with
+// its rows left out one by one the first took 4.4 ms.  As part of the converters' code,
+// by the last of them, it cost ordinary values 40 %; this way 2 (32 x 32768: 72.3 -> 73.9 us).
+template <int kHd>
+__device__ __forceinline__ void prefix_refit(PrefixShared<kHd>& sh, const float* V, uint8_t* v_ring,
+                                             int keys, int n) {
+  using Cfg = PrefixCfg<kHd>;
+  constexpr int kPL = kHd / 32, kAt = 16 / kPL < 4 ? 16 / kPL : 4;      // rows in flight
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  bool dead = false;
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int slot = j & 1, stage = (j % Cfg::kDepth) * Cfg::kNC;
+    if (!dead)
+      dead = !__all_sync(0xFFFFFFFFu,
+                         mbar_wait(&sh.v_done[slot], static_cast<uint32_t>(j >> 1) & 1u));
+    if (__any_sync(0xFFFFFFFFu, sh.misfit[j] != 0)) {
+      const float* from = V + static_cast<int64_t>(j) * kTileKeys * kHd;
+      const int there = min(kTileKeys, keys - j * kTileKeys);
+      float x[kAt][kPL], a = 0.f, b = 0.f;       // rows; the largest of rows lane and lane + 32
+      const auto load = [&](int r) {
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+#pragma unroll
+          for (int c = 0; c < kPL; ++c) x[i][c] = 0.f;
+          if (r + i < there) load_row<kPL>(from + (r + i) * kHd, lane, x[i]);
+        }
+      };
+#pragma unroll 1
+      for (int r = 0; r < kTileKeys; r += kAt) {
+        load(r);
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          bool fin;
+          const float m = row_amax<kPL>(x[i], fin), top = fin ? m : INFINITY;
+          if (r + i == lane) a = top;
+          if (r + i == lane + 32) b = top;
+        }
+      }
+      const ValueScale sc = choose_value_scale(a, b);
+      const int e = split_exp(sc.top);
+#pragma unroll 1
+      for (int r = 0; r < kTileKeys; r += kAt) {
+        load(r);
+#pragma unroll
+        for (int i = 0; i < kAt; ++i) {
+          const bool out = ((r < 32 ? sc.out[0] : sc.out[1]) >> ((r + i) & 31)) & 1u;
+#pragma unroll
+          for (int c = 0; c < kPL; ++c) x[i][c] = out ? 0.f : x[i][c];
+          store_split_row<typename Cfg::Base>(x[i], exp2i(e), r + i, lane,
+                                              v_ring + stage * Cfg::kUnit);
+        }
+      }
+      if (lane == 0) {
+        sh.mma.meta[slot].vscale = exp2i(-e);
+        sh.left_out[j][0] = sc.out[0];
+        sh.left_out[j][1] = sc.out[1];
+        if (sc.top > 0.f) sh.scale[1][slot] = exp2i(max(e - 7, -126));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
+    if (lane == 0) {
+      mbar_arrive(&sh.mma.v_full[stage]);
+      mbar_arrive(&sh.mma.vmeta_full[slot]);
     }
   }
   if (dead && lane == 0) atomicOr(&g_err_prefix, kErrAttLoad);
@@ -416,12 +497,14 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
   const int ka = piece * p.chunk, keys = min(p.n_prefix, ka + p.chunk) - ka;
   const int n = (keys + kTileKeys - 1) / kTileKeys;
   if (threadIdx.x < 2 * kMaxPieceTiles) sh.left_out[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+  if (threadIdx.x < kMaxPieceTiles) sh.misfit[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::kStaging; ++s) {
       mbar_init(&sh.stg_full[s], 1);
       mbar_init(&sh.stg_empty[s], Cfg::kConvWarps);
     }
-    mma_init_barriers<Cfg>(sh.mma, Cfg::kConvWarps);
+    for (int s = 0; s < 2; ++s) mbar_init(&sh.v_done[s], Cfg::kConvWarps);
+    mma_init_barriers<Cfg>(sh.mma, Cfg::kConvWarps, 1);
   }
   if (warp == Cfg::kMmaQk) {
     tmem_alloc(&sh.mma.tmem, 512);
@@ -438,9 +521,10 @@ __global__ void __launch_bounds__(PrefixCfg<kHd>::kThreads, 1)
     regs_dec<56>();
     prefix_convert<kHd>(sh, staging, k_ring, v_ring, keys, n);
   } else if (warp >= Cfg::kRowsWarps) {
-    regs_dec<40>();
+    regs_dec<48>();
     if (warp == Cfg::kLoadK && lane == 0)
       prefix_load<kHd>(sh, staging, p.kp + at, p.vp + at, keys, n);
+    if (warp == Cfg::kLoadV) prefix_refit<kHd>(sh, p.vp + at, v_ring, keys, n);
     if (warp == Cfg::kMmaQk) mma_issue_qk<Cfg>(sh.mma, k_ring, nullptr, n, &g_err_prefix);
     if (warp == Cfg::kMmaPv) mma_issue_pv<Cfg>(sh.mma, v_ring, n, &g_err_prefix);
   } else {

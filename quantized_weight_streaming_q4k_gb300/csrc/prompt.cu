@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
   pdl_launch_dependents();
   const int warp = static_cast<int>(threadIdx.x >> 5), lane = static_cast<int>(threadIdx.x & 31);
   // before the item is looked up, which takes the other warps as long
-  if (warp == Cfg::kMmaPv && lane == 0) mma_init_barriers<Cfg>(sh, 1);
+  if (warp == Cfg::kMmaPv && lane == 0) mma_init_barriers<Cfg>(sh, 1, 1);
   if (warp == Cfg::kMmaQk) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();

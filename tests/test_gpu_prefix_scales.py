@@ -1,0 +1,122 @@
+"""prefix_attention on shared values of very different sizes: the results, and that a piece whose
+first rows do not stand for the others takes about the time of one whose first rows do."""
+import pytest
+import torch
+
+import attention_forms as forms
+from quantized_weight_streaming_q4k_gb300 import build, ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    torch.cuda.set_device(0)
+    yield
+    assert ops.device_error() == 0
+
+
+def normal(seed, *shape):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(82000 + seed)
+    return torch.randn(shape, device="cuda", generator=g)
+
+
+def large_first_row(t):
+    t[:, 5] *= 2.0 ** 12
+
+
+def zero_first_rows(t):
+    t *= 2.0 ** -10
+    t[:, :64] = 0.0
+
+
+def small_first_rows(t):
+    t[:, :64] *= 2.0 ** -13
+
+
+def half_larger(t):
+    t[:, t.shape[1] // 2:] *= 2.0 ** 13
+
+
+def every_second_tile_larger(t):
+    for a in range(0, t.shape[1], 128):
+        t[:, a:a + 64] *= 2.0 ** 12
+
+
+def two_tiles_in_four_larger(t):
+    # whatever scale a tile hands on is wrong for the tile after next
+    for a in range(0, t.shape[1], 256):
+        t[:, a:a + 128] *= 2.0 ** 12
+
+
+def growing(t):
+    n = t.shape[1]
+    t *= torch.exp2(torch.arange(n, device=t.device) * (30.0 / n))[:, None]
+
+
+SHAPES = [large_first_row, zero_first_rows, small_first_rows, half_larger, every_second_tile_larger,
+          two_tiles_in_four_larger, growing]
+
+
+@pytest.mark.parametrize("change", SHAPES)
+@pytest.mark.parametrize("nq,nkv,hd,n_prefix", [(8, 4, 256, 6000), (4, 1, 128, 5000),
+                                                (4, 2, 64, 4500), (3, 1, 32, 9000)])
+def test_values(change, nq, nkv, hd, n_prefix):
+    q, kp, vp = normal(1, 5, nq, hd), normal(2, nkv, n_prefix, hd), normal(3, nkv, n_prefix, hd)
+    kc, vc = normal(4, 5, nkv, 9, hd), normal(5, 5, nkv, 9, hd)
+    change(vp)
+    args = (q, kp, vp, n_prefix, kc, vc, [9, 0, 1, 5, 2], hd ** -0.5)
+    got = ops.prefix_attention(*args)
+    assert torch.equal(got, ops.prefix_attention(*args))
+    ref = forms.prefix_forms(*args, 0.0, torch.float64)
+    forms.assert_as_good_as_f32(got, forms.prefix_forms(*args, 0.0, torch.float32), ref)
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+def test_far_rows_do_not_cost_the_near_ones_their_bits(hd):
+    # rows 2^40 apart: of the small ones' columns, which the large rows leave zero, every bit counts
+    q, kp, vp = normal(6, 3, 4, hd), normal(7, 2, 3000, hd), normal(8, 2, 3000, hd)
+    far = torch.arange(3000, device="cuda") % 97 == 11
+    vp[:, far] *= 2.0 ** 40
+    vp[:, far, : hd // 2] = 0.0
+    own = normal(9, 3, 2, 4, hd)
+    args = (q, kp, vp, 3000, own, own, [4, 0, 1], hd ** -0.5)
+    got = ops.prefix_attention(*args)[..., : hd // 2]
+    ref = forms.prefix_forms(*args, 0.0, torch.float64)[..., : hd // 2]
+    plain = forms.prefix_forms(*args, 0.0, torch.float32)[..., : hd // 2]
+    forms.assert_as_good_as_f32(got, plain, ref)
+
+
+def best_time(args, rounds=9):
+    """Seconds of a call in a captured graph, the best of some: the slow form took milliseconds."""
+    ops.prefix_attention(*args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ops.prefix_attention(*args)
+    times = []
+    for _ in range(rounds):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        graph.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times) * 1e-3
+
+
+@pytest.mark.parametrize("change", SHAPES)
+@pytest.mark.parametrize("hd", [64, 256])
+def test_time(change, hd):
+    # a tile whose values the scale in force does not fit is laid out once more, by one warp, in the
+    # time of six or seven tiles; with the rows left out it took up to ninety times
+    nkv, n = 1024 // hd, 16384
+    q, kp, vp = normal(10, 16, 2 * nkv, hd), normal(11, nkv, n, hd), normal(12, nkv, n, hd)
+    own = normal(13, 16, nkv, 1, hd)
+    args = (q, kp, vp, n, own, own, [1] * 16, hd ** -0.5)
+    usual = best_time(args)
+    change(vp)
+    changed = best_time(args)
+    print(f"{usual * 1e6:.1f} us, {change.__name__} {changed * 1e6:.1f} us")
+    assert changed <= (10 if change is two_tiles_in_four_larger else 6) * usual
