@@ -547,13 +547,21 @@ qws_status qws_prompt_attention(const qws_heads* q, const qws_heads* k, const qw
   QWS_TRY(check_offsets(fn, "cu_q", cu_q, n_seqs));
   QWS_TRY(check_offsets(fn, "cu_k", cu_k, n_seqs));
   QWS_TRY(check_scale(fn, scale, softcap));
-  QWS_TRY(check_heads(fn, "q", q));
-  QWS_TRY(check_heads(fn, "k", k));
-  QWS_TRY(check_heads(fn, "v", v));
-  QWS_TRY(check_out_heads(fn, "out", out, cu_q[n_seqs], n_q_heads, head_dim));
-  if (out->data == q->data || out->data == k->data || out->data == v->data)
-    return fail(QWS_ERR_SHAPE, "%s: out must not be q, k or v", fn);
   if (cu_q[n_seqs] == cu_q[0]) return ok();
+  // a tensor without elements has no address: without a key that a query could see, k and v
+  // are not looked at
+  bool keys = false;
+  for (int s = 0; s < n_seqs; ++s) keys = keys || (cu_q[s + 1] > cu_q[s] && cu_k[s + 1] > cu_k[s]);
+  QWS_TRY(check_heads(fn, "q", q));
+  if (keys) {
+    QWS_TRY(check_heads(fn, "k", k));
+    QWS_TRY(check_heads(fn, "v", v));
+  } else if (!k || !v) {
+    return fail(QWS_ERR_NULL, "%s: k or v is NULL", fn);
+  }
+  QWS_TRY(check_out_heads(fn, "out", out, cu_q[n_seqs], n_q_heads, head_dim));
+  if (out->data == q->data || (keys && (out->data == k->data || out->data == v->data)))
+    return fail(QWS_ERR_SHAPE, "%s: out must not be q, k or v", fn);
   if (!aligned(ws, 16)) return fail(QWS_ERR_ALIGN, "%s: ws is not 16-byte aligned", fn);
   size_t need = 0;
   cudaError_t e = cudaSuccess;

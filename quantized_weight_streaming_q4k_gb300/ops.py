@@ -369,8 +369,6 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu
     oh = _heads(out, "out", dev, n_q, hd)
     if max(cu) > out.shape[0]:
         raise ValueError("the offsets pass the end of out")
-    if cu[0] == cu[n]:
-        return out
     L = lib()
     ws, nbytes = _workspace(
         L.qws_prompt_attention_workspace_bytes(cu, ck, n, n_q, n_kv, hd), workspace, dev, stream)
