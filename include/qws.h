@@ -281,9 +281,9 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   [n_tokens] int64 (device, 8-byte aligned), any sign.  An output may be its
  *   own input (same pointer and strides); otherwise outputs overlap no input
  *   and not one another.  rot_dim even, 0 < rot_dim <= head_dim;
- *   base >= 1; eps >= 0; n_tokens >= 0.  The angle modulo a turn is exact to
- *   2^-53 of the rotation per position, whatever the position; its sine and
- *   cosine and the rotation are f32.
+ *   base >= 1; eps >= 0; n_tokens >= 0.  The angle modulo a turn is off by at
+ *   most 6 x 2^-53 radians per position; its sine and cosine and the rotation
+ *   are f32.
  *
  * qws_prompt_attention: causal attention of packed sequences.  Sequence s has
  *   query tokens cu_q[s] .. cu_q[s+1]-1 and keys cu_k[s] .. cu_k[s+1]-1; query
@@ -301,9 +301,19 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   captured graphs that do, need one each.  Keys that a row does not see may
  *   hold anything, infinities and NaN included.
  *   Accuracy, here and in qws_prefix_attention: f32 sums; a score is within
- *   (head_dim + 32) 2^-24 max_t sum_i |scale q_i k_ti|, whichever kernel runs (on
- *   the tensor cores every f32 is two f16 and every product three).  Beside value
- *   rows within a factor of 2^16 of one another, rows far off cost time, not bits.
+ *   (head_dim + 32) 2^-24 max_t sum_i |scale q_i k_ti| + |scale| sum_i (dq |k_ti| +
+ *   |q_i| dk), where dq and dk are zero on the CUDA cores (up to 2^16 pairs of a query
+ *   row and a key; qws_prefix_attention: up to 256 positions, and own positions).  On the tensor cores every
+ *   f32 is two f16 with a power-of-two scale, every product three of the four: dq is
+ *   2^-39 of the largest of q's head, dk 2^-39 of the largest of k's head, and a value is
+ *   within 2^-22 of itself or, if that is more, 2^-39 of the largest of its 64-key tile.
+ *   In qws_prefix_attention dk is up to 2^-22 of the largest of k's head, and a value's
+ *   error up to 2^-22 of the largest of its head.  So a channel keeps fewer bits than in
+ *   f32 if it is far below the others of its head in k and far above them in q, or is far
+ *   below the others in v: from 2^15 on by and large.  Rows keep theirs: a value row further
+ *   than 2^16 from most of its tile's is added in f32, which costs some 1 to 10 us each.
+ *   Weights and the softcap's tanh are within 2^-22.  A query or key that holds an
+ *   infinity counts as one that holds a NaN there.
  *
  * qws_prefix_attention: one decode step of a batch over a shared prefix.  Row
  *   b of q attends to positions 0 .. n_prefix-1 of the shared caches k_prefix,

@@ -15,7 +15,9 @@
 //
 // The angle: FP64 arithmetic is slow on this GPU, and f32 loses the angle of
 // a far position.  The rotation per position in turns, f_i / 2 pi, is rounded
-// on the host to a 64-bit fixed-point fraction F_i (error 2^-53 relative);
+// on the host to a 64-bit fixed-point fraction F_i.  In radians it is off by at most
+// 6 x 2^-53: two powers, 2 pi, a division and a product, each 2^-53 of f_i <= 1, and the
+// rounded exponent x of base^-x, x ln(base) base^-x <= 1 / e of that.
 // pos * F_i modulo 2^64 by one integer product IS the fraction of a turn, exact
 // for any position.  Its top two bits (rounded) are the quadrant, the rest,
 // at most 1/8 turn either way, is rounded once to f32 for sinpi / cospi: an
