@@ -300,18 +300,20 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   the same arguments (0: may be NULL).  Scratch: calls that overlap, or
  *   captured graphs that do, need one each.  Keys that a row does not see may
  *   hold anything, infinities and NaN included.
- *   Accuracy, here and in qws_prefix_attention: f32 sums; a score is within
+ *   ws holds K and V once more where the tensor cores are used, from 2^16 pairs of a
+ *   query row and a key on, and partial results where a sequence is cut.
+ *   Accuracy, here and in qws_prefix_attention: f32 sums, and a score within
  *   (head_dim + 32) 2^-24 max_t sum_i |scale q_i k_ti| + |scale| sum_i (dq |k_ti| +
- *   |q_i| dk), where dq and dk are zero on the CUDA cores (up to 2^16 pairs of a query
- *   row and a key; qws_prefix_attention: up to 256 positions, and own positions).  On the tensor cores every
- *   f32 is two f16 with a power-of-two scale, every product three of the four: dq is
- *   2^-39 of the largest of q's head, dk 2^-39 of the largest of k's head, and a value is
- *   within 2^-22 of itself or, if that is more, 2^-39 of the largest of its 64-key tile.
- *   In qws_prefix_attention dk is up to 2^-22 of the largest of k's head, and a value's
- *   error up to 2^-22 of the largest of its head.  So a channel keeps fewer bits than in
- *   f32 if it is far below the others of its head in k and far above them in q, or is far
- *   below the others in v: from 2^15 on by and large.  Rows keep theirs: a value row further
- *   than 2^16 from most of its tile's is added in f32, which costs some 1 to 10 us each.
+ *   |q_i| dk).  On the CUDA cores (fewer pairs; qws_prefix_attention: own positions,
+ *   and up to 256 in all) dq and dk are zero.  On the tensor cores every f32 is two f16
+ *   with a power-of-two scale, every product three of the four: dq is 2^-39 of the
+ *   largest of q's head, dk 2^-39 of the largest of k's head, and a value is within
+ *   2^-22 of itself or, if that is more, 2^-39 of the largest of its 64-key tile.  In
+ *   qws_prefix_attention dk is up to 2^-22 of the largest of k's head, a value's error up
+ *   to 2^-22 of the largest of its head.  So a channel keeps fewer bits than in f32 if it
+ *   is far below the others of its head in k and far above them in q, or far below the
+ *   others in v: from 2^15 on by and large.  Rows keep theirs: a value row further than
+ *   2^16 from most of its tile's is added in f32, which costs some 1 to 10 us each.
  *   Weights and the softcap's tanh are within 2^-22.  A query or key that holds an
  *   infinity counts as one that holds a NaN there.
  *
@@ -323,7 +325,8 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   position is zero.  Caches 16-byte aligned; k_prefix and v_prefix may be
  *   NULL when n_prefix is 0, the own caches when every n_ctx is 0.
  *   0 <= n_prefix <= max_prefix <= 2^30, 0 <= n_ctx[b] <= max_seq <= 2^30 (host
- *   array), batch >= 0.  out overlaps neither q nor a cache.  ws as above, qws_prefix_attention_workspace_bytes.
+ *   array), batch >= 0.  out overlaps neither q nor a cache.  ws as above,
+ *   qws_prefix_attention_workspace_bytes (partial results).
  *   Positions from the lengths on may hold anything.
  * ---------------------------------------------------------------------- */
 typedef struct {

@@ -63,7 +63,7 @@ __device__ __forceinline__ int64_t prefix_part(const PrefixParams& p, int piece,
 // one vote checks; the others, 2^8 times larger or 2^10 times smaller than that run, are
 // rare.  Such a key gets a scale of its own.  A tile with such a value row is laid out once
 // more, with a scale of its own, which the tile after next goes on with, by a warp that is
-// there for this (prefix_refit).  64 rows against 32768 keys of 4 heads of 256: 67 us, 4.0 TB/s
+// there for this (prefix_refit).  64 rows against 32768 keys of 4 heads of 256: 69 us, 3.9 TB/s
 // (268 MB at the copy rate: 40 us), some 8000 cycles a tile.
 template <int kHd>
 struct PrefixCfg : MmaCfg<kHd, (kHd > 128 ? 1 : kHd > 64 ? 2 : 4), true, 1> {
@@ -813,7 +813,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 namespace {
 
 // Shared and own positions of the longest sequence up to which one CTA a sequence and kv
-// head takes them all.
+// head takes them all.  Device time this way / in three kernels, at 96, 256 and 384 positions: 4
+// sequences of 8 q / 4 kv heads of 256 6.7 / 14.4, 14.0 / 14.5, 19.8 / 14.8 us; 32 of 256
+// 7.5 / 17.0, 15.5 / 21.1, 21.9 / 21.8; 32 of 8 / 4 heads of 128 6.2 / 10.8, 13.2 / 12.4, 18.6 / 12.5.
+// Four heads a kv head make it longer: 4 of 8 / 2 heads of 64 8.3 / 8.8, 19.1 / 10.4.
 constexpr int64_t kFewKeys = 256;
 
 struct PrefixPlan {

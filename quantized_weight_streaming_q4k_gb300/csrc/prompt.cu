@@ -580,10 +580,12 @@ __global__ void __launch_bounds__(PromptCfg<kHd>::kThreads, 1)
 // ------------------------------------------------------------ host side
 namespace {
 
-// (query row, key) pairs of all heads above which the tensor cores, whose two or three
-// launches and packing take 13 us at least, take a call; device time on CUDA cores / tensor
-// cores: 128 tokens of 8 q / 4 kv heads of 256 (2^16 pairs) 21.5 / 19.2 us, of 16 / 4 heads of
-// 128 (2^17) 23.5 / 13.3 us, 64 tokens of 8 / 4 heads of 256 (2^14) 11.3 us / not less than 13.
+// (query row, key) pairs of all heads from which the tensor cores, whose two or three
+// launches and packing take 8 us (head_dim 32) to 17 (256) at least, take a call.  Device time
+// on CUDA cores / tensor cores at half of it, at it and at twice: 4 q / 4 kv heads of 32 6.6 / 7.9,
+// 8.9 / 8.3, 12.4 / 9.4 us; 8 / 2 of 64 7.2 / 8.7, 9.1 / 9.1, 13.4 / 9.9; 8 / 4 of 128 10.3 / 11.3,
+// 13.3 / 12.1, 18.6 / 12.8; 8 / 4 of 256 16.0 / 16.9, 21.5 / 18.2, 25.8 / 19.5.  A few queries
+// on 2000 keys, just below: 8.7 / 11.6, 10.4 / 11.6, 13.2 / 15.6, 24.3 / 24.7.
 constexpr int64_t kMmaFrom = 1 << 16;
 // Up to this many tiles of four rows a warp, one row a warp: each then still has its SM.
 // 37 tokens of 8 q / 4 kv heads of 256: 16.7 -> 9.4 us.  Longer prompts read the keys more
@@ -630,6 +632,9 @@ void order_seqs(const int64_t* cu_q, const int64_t* cu_k, int s0, int n, int* or
 // after kWeighed placements for all the lengths no other length is weighed.  512 queries on
 // 8000 keys 8 us, 64 single ones on 8000 keys each 95, 4000 prompts of 20 tokens beside one of
 // 2000 240 (item by item 600; 128 queries on 2^24 keys 9, and were 190).
+//
+// kItemSteps: an item of 3100 to 3800 cycles a tile has some 15000 beside its tiles (its Q,
+// first scores, output and the next launch).
 constexpr int64_t kItemSteps = 5;
 constexpr int64_t kJoinSteps = 2;        // of prompt_merge_kernel
 constexpr int kPlaced = 2048, kWeighed = 16384;
@@ -719,7 +724,7 @@ PromptPlan plan_prompt(const int64_t* cu_q, const int64_t* cu_k, int n_seqs, int
     pairs += nq * group * std::max<int64_t>(1, nk - std::min(nq, nk) / 2);
     if (nq) longest = std::max(longest, nk);
   }
-  pl.mma = pairs * n_kv > kMmaFrom;
+  pl.mma = pairs * n_kv >= kMmaFrom;
   int64_t tiles = 0;           // of 4 rows a warp
   for (int s = 0; s < n_seqs; ++s)
     tiles += ceil_div(cu_q[s + 1] - cu_q[s], 4 * kRowWarps / group) * n_kv;

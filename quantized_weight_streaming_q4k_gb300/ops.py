@@ -351,8 +351,8 @@ def prompt_attention(q, k, v, cu_seqlens, scale: float, softcap: float = 0.0, cu
                      workspace=None, out=None, stream=None):
     """Causal attention of packed sequences: q [T, n_q, hd], k and v [Tk, n_kv, hd], sequence s
     at rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (host integers) of q, and of k and v, or at
-    cu_seqlens_k there; its last query sees all of its keys.  Rows of out behind the last
-    sequence are left as they were."""
+    cu_seqlens_k there; its last query sees all of its keys.  Rows of out that belong to no
+    sequence are left as they were (in a fresh out: whatever the memory held)."""
     dev = torch.cuda.current_device()
     qh = _heads(q, "q", dev)
     _, n_q, hd = q.shape
