@@ -6,7 +6,7 @@
 // hi*hi + hi*lo + lo*hi, accumulated in f32.  Before the split a query row and
 // a key row are each scaled by a power of two that puts their largest value in
 // [2^14, 2^15), the values of a tile by one for the whole tile; the weights
-// are at most 2^14.  So a value keeps 22 bits, or 2^-40 of the largest it
+// are at most 2^14.  So a value keeps 22 bits, or 2^-39 of the largest it
 // is scaled with.  A key whose values would spoil its tile's scale or be spoilt by it (one
 // that is not finite, or further than 2^16 from the tile's others, which may be keys that
 // most rows do not even see) is left out of the tile and added at the end, in f32, by the

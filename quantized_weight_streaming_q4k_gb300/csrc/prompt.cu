@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(256)
 // and P V(j+1) do not wait for one tile's softmax.  8192 positions, 8 q / 4 kv heads of 256:
 // 616 -> 525 us; 16 q / 4 kv heads of 128: 619 -> 572 us, with a softcap 785 -> 683 us.  Since
 // then Q K^T takes two passes (for accuracy) and the scores stay in registers up to head_dim
-// 128: 540, 542 and 632 us (the MMAs at the measured rate: 428 us).  At head_dim 256 a tile
+// 128: 541, 544 and 605 us (the MMAs at the measured rate: 428 us).  At head_dim 256 a tile
 // takes 3780 cycles; below, the softmax's instructions bind (1400 a scheduler and tile).
 template <int kHd>
 struct PromptCfg : MmaCfg<kHd, (kHd > 128 ? 1 : 0), false, 2> {
