@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import attention_forms as forms
 from quantized_weight_streaming_q4k_gb300 import build, ops
 
 pytestmark = pytest.mark.gpu
@@ -31,6 +32,26 @@ def test_sequences_whose_keys_have_no_queries():
     k = torch.ones(50, 2, 64, device="cuda")
     got = ops.prompt_attention(q, k, k, [0, 40, 40], 1.0, cu_seqlens_k=[0, 0, 50])
     assert not got.any()
+
+
+@pytest.mark.parametrize("last", [600, 0])
+def test_a_whole_table_of_sequences_without_keys(last):
+    # 128 sequences a launch: the first launch has no keys, the second some
+    g = torch.Generator(device="cuda")
+    g.manual_seed(86000)
+    lens, ctx = [10] * 128 + [600], [0] * 128 + [last]
+    q = torch.randn(sum(lens), 4, 64, device="cuda", generator=g)
+    k = torch.randn(last, 2, 64, device="cuda", generator=g)
+    cu, ck = ([sum(n[:i]) for i in range(len(n) + 1)] for n in (lens, ctx))
+    got = ops.prompt_attention(q, k, k, cu, 0.125, cu_seqlens_k=ck)
+    assert not got[:1280].any()
+    if last:
+        # (pieces, and so roundings, go by all lengths of a call: not the bits of a call of its own)
+        args = (q[1280:], k, k, [0, 600], [0, 600], 0.125, 0.0)
+        ref = forms.prompt_forms(*args, torch.float64)
+        forms.assert_as_good_as_f32(got[1280:], forms.prompt_forms(*args, torch.float32), ref)
+    else:
+        assert not got.any()
 
 
 def test_offsets_that_decrease_are_refused_without_rows_too():

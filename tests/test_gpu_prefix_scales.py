@@ -74,6 +74,36 @@ def test_values(change, nq, nkv, hd, n_prefix):
     forms.assert_as_good_as_f32(got, forms.prefix_forms(*args, 0.0, torch.float32), ref)
 
 
+@pytest.mark.parametrize("change", [large_first_row, two_tiles_in_four_larger])
+@pytest.mark.parametrize("nq,nkv,hd,n_prefix,batch,cap", [(4, 1, 64, 700, 300, 0.0), (8, 4, 256, 900, 70, 30.0),
+                                                          (3, 1, 128, 1500, 100, 2.0)])
+def test_more_rows_than_a_tile(change, nq, nkv, hd, n_prefix, batch, cap):
+    # more than 128 rows a kv head, more sequences than a launch takes; keys that do not fit either
+    q, kp, vp = normal(14, batch, nq, hd), normal(15, nkv, n_prefix, hd), normal(16, nkv, n_prefix, hd)
+    kc, vc = normal(17, batch, nkv, 3, hd), normal(18, batch, nkv, 3, hd)
+    change(vp)
+    kp[:, 40:60] *= 2.0 ** -20
+    args = (q, kp, vp, n_prefix, kc, vc, [b % 4 for b in range(batch)], hd ** -0.5, cap)
+    got = ops.prefix_attention(*args)
+    ref = forms.prefix_forms(*args, torch.float64)
+    forms.assert_as_good_as_f32(got, forms.prefix_forms(*args, torch.float32), ref)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_in_its_column(bad):
+    q, kp, vp = normal(19, 3, 4, 64), normal(20, 2, 1500, 64), normal(21, 2, 1500, 64)
+    every_second_tile_larger(vp)
+    own = normal(22, 3, 2, 4, 64)
+    args = (q, kp, vp, 1500, own, own, [4, 0, 1], 0.125)
+    want = ops.prefix_attention(*args)
+    vp[1, 700, 7] = bad
+    got = ops.prefix_attention(*args)
+    assert not torch.isfinite(got[:, 2:, 7]).any()
+    got[:, 2:, 7] = want[:, 2:, 7]
+    # the rest as before, to plain f32's rounding of values up to 2^14
+    assert torch.all((got - want).abs() <= 2.0 ** -21 * vp[0].abs().max())
+
+
 @pytest.mark.parametrize("hd", [64, 256])
 def test_far_rows_do_not_cost_the_near_ones_their_bits(hd):
     # rows 2^40 apart: of the small ones' columns, which the large rows leave zero, every bit counts

@@ -75,3 +75,23 @@ def test_outputs_may_be_freed_while_the_current_stream_reads_them():
         more = [call(side) for _ in range(3)]              # would take the block again
         assert bool(same)
         del more
+
+
+@pytest.mark.parametrize("name", ["qk_norm_rope", "prompt_attention", "prefix_attention"])
+def test_a_side_stream_inside_a_captured_graph(name):
+    call, side = calls()[name], torch.cuda.Stream()
+    want = call(None).clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        a = call(side)                                     # both at once, each its memory
+        b = call(None)
+        here.wait_stream(side)
+        c = a + b
+    for _ in range(3):
+        c.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want) and torch.equal(c, want * 2)
