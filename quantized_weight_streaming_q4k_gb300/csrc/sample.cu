@@ -31,17 +31,15 @@
 #include <cmath>
 
 #include "launch.h"
+#include "sample_plan.h"
 
 namespace qws {
 
-constexpr int kSaThreads = 1024;
 constexpr int kSaWarps = kSaThreads / 32;
 constexpr int kSaBins = 2048;
-constexpr int kSaMaxCluster = 16;
 constexpr int kSaFew = kSaThreads;           // candidates that one CTA puts in order
 constexpr int kSaRank = kSaThreads / 4;      // of which it orders by counting, a quarter a thread
 static_assert(kSaWarps == 32 && kSaFew * 8 <= kSaBins * 4, "a list in place of a histogram");
-constexpr int kSaMaxSlice = 43 * 1024;       // logits of a CTA, in shared memory
 
 // 2^(-k/1024) in units of 2^-45, by the exponential's power series at compile time
 struct ExpTable {
@@ -848,25 +846,28 @@ static cudaLaunchConfig_t sample_config(int n_rows, int size, size_t smem, cudaS
 }
 
 // Clusters of that size that the device runs at once: 152 SMs hold 76 of 2, 23 of 6, but 15 of 8
-// and 7 of 16, whose SMs have to be neighbours.
-static int clusters_at_once(int size) {
-  static std::atomic<int> known[64][kSaMaxCluster + 1];
+// and 7 of 16, whose SMs have to be neighbours; none of a size for which too few are in reach.  Asked
+// once a device and size (some microseconds); a question that fails is not an answer and is not kept.
+static cudaError_t clusters_at_once(int size, int* n) {
+  static std::atomic<int> known[64][kSaMaxCluster + 1];      // 0: not asked; else the answer + 1
   int dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev < 64) {
-    const int n = known[dev][size].load(std::memory_order_relaxed);
-    if (n) return n;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int k = dev < 64 ? known[dev][size].load(std::memory_order_relaxed) : 0;
+  if (k) {
+    *n = k - 1;
+    return cudaSuccess;
   }
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = sample_config(1, size, kSaMaxSlice * 4, nullptr, attr);
   cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, sample_kernel, &cfg) != cudaSuccess) {
+  e = cudaOccupancyMaxActiveClusters(n, sample_kernel, &cfg);
+  if (e != cudaSuccess) {
     cudaGetLastError();
-    n = 0;
+    return e;
   }
-  n = std::max(n, 1);
-  if (dev < 64) known[dev][size].store(n, std::memory_order_relaxed);
-  return n;
+  if (dev < 64) known[dev][size].store(*n + 1, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 cudaError_t launch_sample(const float* logits, int64_t stride, int vocab, int n_rows,
@@ -875,20 +876,17 @@ cudaError_t launch_sample(const float* logits, int64_t stride, int vocab, int n_
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_once(sample_kernel, kSaMaxSlice * 4, true, done);
   if (e != cudaSuccess) return e;
-  // As many CTAs a row as its logits need, and more, down to two logits a thread, while the rows
-  // do not take more turns for it: 64 rows of 262144, top_k 64, 61 us with 6 CTAs, 79 with 8; 9 rows
-  // 21.6 with 6, 17.5 with 10, 29 with 12; a row of 32000 17 with 1, 10.7 with 16.
-  const int least = (vocab + kSaMaxSlice - 1) / kSaMaxSlice;
-  int size = least;
-  int turns = 0;
-  for (int i = least; i <= kSaMaxCluster; ++i) {
-    if (i > least && vocab < 2 * kSaThreads * i) break;
-    const int at_once = clusters_at_once(i), n = (n_rows + at_once - 1) / at_once;
-    if (turns == 0 || n <= turns) {
-      turns = n;
-      size = i;
+  cudaError_t asked = cudaSuccess;
+  const int size = sample_cluster_size(vocab, n_rows, [&](int i) {
+    int n = 0;
+    const cudaError_t a = clusters_at_once(i, &n);
+    if (a != cudaSuccess) {
+      asked = a;
+      return 0;
     }
-  }
+    return n;
+  });
+  if (size == 0) return asked != cudaSuccess ? asked : cudaErrorInvalidClusterSize;
   SampleParams p{logits, stride, vocab, 0, 0, {}, u, temperature, top_p, min_p, top_k, out};
   p.slice = ((vocab + size - 1) / size + 3) / 4 * 4;
   p.vec = reinterpret_cast<uintptr_t>(logits) % 16 == 0 && (stride % 4 == 0 || n_rows == 1);
