@@ -395,7 +395,8 @@ qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const
  *   floor(x * id + 8.5)), all in f32; d is stored rounded to binary16.
  *   Padding tokens have their q_out and store nothing.  A key is off by 2^-24 of
  *   itself and some 2^-40 of its head's largest before it is quantised (the angle as
- *   in qws_qk_norm_rope).  x finite; |x| < 2^60 with a norm; what is stored is at most 8
+ *   in qws_qk_norm_rope).  0 <= eps < 2^100.  x finite; |x| < 2^60 with a norm, and as small as
+ *   f32 goes, eps 0 included; a head of zeros stays zeros.  What is stored is at most 8
  *   (Q8_0: 127) times 65504, the largest f16.  Two tokens of a call
  *   with the same sequence and position: every two bytes stored are the one's or
  *   the other's.

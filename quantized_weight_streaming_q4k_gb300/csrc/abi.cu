@@ -732,8 +732,8 @@ qws_status qws_paged_kv_append(const qws_paged_kv* kv, const qws_heads* q, const
     return fail(QWS_ERR_SHAPE, "%s: need an even 0 <= rot_dim <= head_dim", fn);
   if (rot_dim && (!(base >= 1.0) || !std::isfinite(base)))
     return fail(QWS_ERR_SHAPE, "%s: need a finite base >= 1", fn);
-  if (!(eps >= 0.0) || !std::isfinite(eps))
-    return fail(QWS_ERR_SHAPE, "%s: eps must be finite and >= 0", fn);
+  if (!(eps >= 0.0 && eps < 0x1p100))
+    return fail(QWS_ERR_SHAPE, "%s: need 0 <= eps < 2^100", fn);
   if (n_tokens == 0) return ok();
   const cudaError_t e = qws::launch_paged_append(
       c, kv->fmt, q, *k, *v, q_out, w_q, w_k, seqs, positions, n_tokens, n_q_heads, kv->head_dim,

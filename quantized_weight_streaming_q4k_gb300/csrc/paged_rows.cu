@@ -17,7 +17,7 @@
 // some 430 instructions a row of 256 on average, a key row twice that.  One CTA a token,
 // as in qk_norm_rope: its threads compute the token's sines and cosines once into shared memory
 // while the warps' first rows are in flight; then a warp a head, one copy of the code for all.
-// 4096 tokens of 8 + 4 + 4 heads of 256, Q4_0, take 34.5 us (105 MB: 3.0 TB/s).  Before: 60 with
+// 4096 tokens of 8 + 4 + 4 heads of 256, Q4_0, take 33.1 us (105 MB: 3.2 TB/s).  Before: 60 with
 // queries in pairs too, 50 with the rows' code four times over, 44 with the angles in order, which
 // a warp reads with four conflicts each.  More rows in flight per warp: 47 to 51.
 #include <cuda_runtime.h>
@@ -154,13 +154,20 @@ __device__ __forceinline__ void load_weights(const float* w, int lane, float (&x
 constexpr int kApWarps = 4;
 constexpr int kApMaxHalf = 128;    // rot_dim <= head_dim <= 256
 
+// Heads whose mean square and eps together are below kSmall are taken kUp times as large, and eps
+// kUp^2 times: their squares have remainders below f32's range then, and its reciprocal leaves it
+// from 2^-128 on.  Above it nothing is lost (mean: from squares of 2^-90 on within 2^-59), below
+// it |x| < 2^-41, so the squares of kUp x stay below 2^118, and those of subnormal x above 2^-98.
+// What is left, a head of zeros, ends as zeros by the mean's lower limit.
+constexpr float kSmall = 0x1p-90f, kUp = 0x1p100f, kLeast = 0x1p-125f;
+
 struct AppendParams {
   PagedView c;
   qws_heads q, k, v, qo;
   const float *w_q, *w_k;
   const int64_t *seqs, *positions;
   int n_q, rot;                    // n_q 0: no queries; rot 0: no rotation
-  Pair eps;
+  Pair eps, eps_up;                // eps; the same times kUp^2
   uint64_t turn[kApMaxHalf];       // rotation per position, in 2^-64 turns
 };
 
@@ -296,12 +303,20 @@ __global__ void __launch_bounds__(kApWarps * 32, 8)
   // a query: nothing is decided by its last bit, so f32 as in qk_norm_rope
   auto finish_query = [&](int r, float (&v)[kPL]) {
     if (p.w_q) {
-      float ss = 0.f, w[kPL];
+      float mean, w[kPL];
       load_weights<kPL>(p.w_q, lane, w);
+#pragma unroll 1
+      for (bool up = false;; up = true) {
+        float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < kPL; ++j) ss = fmaf(v[j], v[j], ss);
-      ss = warp_sum(ss);
-      const float rs = 1.0f / sqrtf(ss * (1.0f / kHd) + p.eps.h);
+        for (int j = 0; j < kPL; ++j) ss = fmaf(v[j], v[j], ss);
+        mean = warp_sum(ss) * (1.0f / kHd) + (up ? p.eps_up.h : p.eps.h);
+        if (up) mean = fmaxf(mean, kLeast);
+        if (up || !(mean < kSmall)) break;
+#pragma unroll
+        for (int j = 0; j < kPL; ++j) v[j] *= kUp;
+      }
+      const float rs = 1.0f / sqrtf(mean);
 #pragma unroll
       for (int j = 0; j < kPL; ++j) v[j] = v[j] * rs * w[j];
     }
@@ -347,17 +362,26 @@ __global__ void __launch_bounds__(kApWarps * 32, 8)
       if (p.w_k) {
         float w[kPL];
         load_weights<kPL>(p.w_k, lane, w);
-        Pair ss{0.f, 0.f};
+        Pair mean;
+#pragma unroll 1
+        for (bool up = false;; up = true) {
+          Pair ss{0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kPL; ++j) {
-          const Pair q = two_prod(v[j], v[j]), t = two_sum(ss.h, q.h);
-          ss = {t.h, __fadd_rn(ss.l, __fadd_rn(t.l, q.l))};
+          for (int j = 0; j < kPL; ++j) {
+            const Pair q = two_prod(v[j], v[j]), t = two_sum(ss.h, q.h);
+            ss = {t.h, __fadd_rn(ss.l, __fadd_rn(t.l, q.l))};
+          }
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            ss = add(ss, Pair{__shfl_xor_sync(0xFFFFFFFFu, ss.h, o),
+                              __shfl_xor_sync(0xFFFFFFFFu, ss.l, o)});
+          mean = add(Pair{ss.h * (1.0f / kHd), ss.l * (1.0f / kHd)}, up ? p.eps_up : p.eps);
+          if (up) mean.h = fmaxf(mean.h, kLeast);
+          if (up || !(mean.h < kSmall)) break;
+#pragma unroll
+          for (int j = 0; j < kPL; ++j) v[j] *= kUp;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          ss = add(ss, Pair{__shfl_xor_sync(0xFFFFFFFFu, ss.h, o),
-                            __shfl_xor_sync(0xFFFFFFFFu, ss.l, o)});
-        const Pair rs = rsqrt_pair(add(Pair{ss.h * (1.0f / kHd), ss.l * (1.0f / kHd)}, p.eps));
+        const Pair rs = rsqrt_pair(mean);
 #pragma unroll
         for (int j = 0; j < kPL; ++j) {
           const Pair x = two_prod(v[j], rs.h), z = two_prod(x.h, w[j]);
@@ -463,6 +487,9 @@ cudaError_t launch_paged_append(const PagedView& c, int fmt, const qws_heads* q,
   p.rot = rot_dim;
   p.eps.h = static_cast<float>(eps);
   p.eps.l = static_cast<float>(eps - static_cast<double>(p.eps.h));
+  const double up = eps < kSmall ? eps * kUp * kUp : 0.0;      // (else no head is below kSmall)
+  p.eps_up.h = static_cast<float>(up);
+  p.eps_up.l = static_cast<float>(up - static_cast<double>(p.eps_up.h));
   for (int i = 0; i < kApMaxHalf; ++i) p.turn[i] = 0;
   if (rot_dim) rotation_turns(rot_dim, base, p.turn);
   return fmt == QWS_Q4_0 ? launch_append_fmt<QWS_Q4_0>(p, n_tokens, head_dim, st)
