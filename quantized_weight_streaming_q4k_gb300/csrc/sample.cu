@@ -744,7 +744,12 @@ __global__ void __launch_bounds__(kSaThreads) sample_kernel(const SampleParams p
       // than a second search, by weights (9 rows of 262144, top_k 1000: 43 us for 59); without
       // it the border alone and the draw by all CTAs are sooner done (18 for 31 us, a row; 64: 84 for 97).
       int few = d.use_p ? kSaFew : kSaRank;
-      const Steps steps{top, (kSaBins - 1) / (top - key_value(lo))};
+      // Steps no lower than 128 max(T, 1) below the largest, where weights end at 32 T: a mask's
+      // -1e4, -1e9 or lowest f32 would have all other logits in one bin (a row of 262144 with nine in
+      // ten masked so, top_k 64 and top_p: 14 us, and 33 with steps down to the smallest).
+      const float low = __fsub_rd(top, 128.f * fmaxf(T, 1.f));
+      const uint32_t from = min(max(lo, order_key(low)), top_key);
+      const Steps steps{top, (kSaBins - 1) / (top - key_value(from))};
       cut = find_cut<false>(team, keys, n, lo, top_key, steps, above, whole, few,
                             [](uint32_t) { return 1ull; }, [&](u64) { return d.k; });
       if (few) return choose_few(team, keys, n, i0, cut, lo, steps, w, d, p.out + row);
