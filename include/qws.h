@@ -405,8 +405,12 @@ qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const
  *   Rows of padding are zero.
  * qws_paged_kv_attention: row t of q attends to positions 0 .. positions[t] of
  *   sequence seqs[t], as in qws_kv_attention; its own key and value have been
- *   appended before.  Several tokens of a sequence (a few proposed ones, the
- *   pieces of prompts) are rows of their own.  Rows of padding are zero.  n_q_heads /
+ *   appended before.  Several tokens of a sequence (a few proposed ones) are rows of
+ *   their own; side by side in the call they share what is read and unpacked.
+ *   tokens_per_seq >= 0 says how many there are, about: it chooses the form that is
+ *   fastest for them, and any number gives the same rows but for their last bits.  0: more
+ *   than one if the call has more tokens than the table has rows, so a table with spare
+ *   rows should say.  Rows of padding are zero.  n_q_heads /
  *   n_kv_heads in 1..4.  out overlaps neither q nor the pages.  ws: device,
  *   16-byte aligned, >= qws_paged_kv_attention_workspace_bytes, scratch.
  *   Positions behind a row's own may hold anything, infinities and NaN included.
@@ -442,6 +446,7 @@ typedef struct {
   int64_t n_pages;
   const int32_t* table;
   int64_t n_seqs, max_pages;
+  int tokens_per_seq;   /* of qws_paged_kv_attention; 0: not known */
 } qws_paged_kv;
 
 /* bytes of one kv head's part of a page; 0 for a format or size that is not taken */

@@ -54,7 +54,7 @@ class QwsPagedKv(C.Structure):
     _fields_ = [
         ("fmt", C.c_int), ("page_size", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
         ("pages", C.c_void_p), ("n_pages", C.c_int64), ("table", C.c_void_p),
-        ("n_seqs", C.c_int64), ("max_pages", C.c_int64),
+        ("n_seqs", C.c_int64), ("max_pages", C.c_int64), ("tokens_per_seq", C.c_int),
     ]
 
 

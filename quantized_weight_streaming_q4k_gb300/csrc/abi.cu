@@ -787,13 +787,15 @@ qws_status qws_paged_kv_attention(const qws_paged_kv* kv, const qws_heads* q,
   if (out->data == q->data || out->data == kv->pages)
     return fail(QWS_ERR_SHAPE, "%s: out must not be q or the pages", fn);
   QWS_TRY(check_scale(fn, scale, softcap));
+  if (kv->tokens_per_seq < 0) return fail(QWS_ERR_SHAPE, "%s: tokens_per_seq < 0", fn);
   if (n_tokens == 0) return ok();
   const int group = n_q_heads / kv->n_kv_heads;
   QWS_TRY(check_ws(fn, ws, ws_bytes,
                    qws::paged_attention_workspace_bytes(n_tokens, group, kv->n_kv_heads,
                                                         kv->head_dim)));
   const cudaError_t e = qws::launch_paged_attention(
-      c, kv->fmt, *q, *out, seqs, positions, n_tokens, group, kv->head_dim, scale, softcap, ws,
+      c, kv->fmt, *q, *out, seqs, positions, n_tokens, kv->tokens_per_seq, group, kv->head_dim,
+      scale, softcap, ws,
       reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, fn, "");
   return ok();

@@ -219,9 +219,9 @@ cudaError_t launch_paged_gather(const PagedView& c, int fmt, const qws_heads& k,
 size_t paged_attention_workspace_bytes(int64_t n_tokens, int group, int n_kv, int head_dim);
 cudaError_t launch_paged_attention(const PagedView& c, int fmt, const qws_heads& q,
                                    const qws_heads& out, const int64_t* seqs,
-                                   const int64_t* positions, int64_t n_tokens, int group,
-                                   int head_dim, float scale, float cap, void* ws,
-                                   cudaStream_t st);
+                                   const int64_t* positions, int64_t n_tokens,
+                                   int tokens_per_seq, int group, int head_dim, float scale,
+                                   float cap, void* ws, cudaStream_t st);
 unsigned read_clear_paged_errors();
 unsigned read_clear_pattn_errors();
 // the next tokens (sample.cu)

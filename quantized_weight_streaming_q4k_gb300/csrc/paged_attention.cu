@@ -817,11 +817,15 @@ __global__ void __launch_bounds__(kPjThreads)
   *reinterpret_cast<float4*>(to) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
 }
 
-// Two rows a kv head fit the form with two blocks side by side, unless head_dim is one block.
-// Several tokens of a sequence share their pages' bytes in the form of four rows; there are
-// some only if there are more tokens than sequences.
-static int rows_of(int64_t n_tokens, int64_t n_seqs, int group, int head_dim) {
-  return group > 2 || head_dim == 32 || n_tokens > n_seqs ? 4 : 2;
+// Rows of an item: the query rows that a kv head's codes are unpacked for, group times the
+// neighbouring tokens of a sequence, if they are two and head_dim is more than one block (see kRows), else
+// four.  12 sequences of up to 4099 positions, Q4_0, heads of 256, two query heads a kv head, in four rows
+// and in two: four tokens each 21.5 and 29.0 us, two 17.3 and 18.9; one query head, heads of 128:
+// 16.0 and 22.2, 16.0 and 14.8.  How many there are only the caller knows, the table may have
+// rows to spare; without a word from it, more tokens than rows must mean some.
+static int rows_of(int64_t n_tokens, int64_t n_seqs, int tokens_per_seq, int group, int head_dim) {
+  const int64_t tokens = tokens_per_seq ? tokens_per_seq : n_tokens > n_seqs ? 4 : 1;
+  return head_dim == 32 || group * tokens > 2 ? 4 : 2;
 }
 
 size_t paged_attention_workspace_bytes(int64_t, int, int, int head_dim) {
@@ -851,11 +855,11 @@ cudaError_t launch_paged_fmt(const PagedAttnParams& p, int rows, int grid, cudaS
 
 cudaError_t launch_paged_attention(const PagedView& c, int fmt, const qws_heads& q,
                                    const qws_heads& out, const int64_t* seqs,
-                                   const int64_t* positions, int64_t n_tokens, int group,
-                                   int head_dim, float scale, float cap, void* ws,
-                                   cudaStream_t st) {
+                                   const int64_t* positions, int64_t n_tokens,
+                                   int tokens_per_seq, int group, int head_dim, float scale,
+                                   float cap, void* ws, cudaStream_t st) {
   const int grid = device_sms();
-  const int rows = rows_of(n_tokens, c.n_seqs, group, head_dim);
+  const int rows = rows_of(n_tokens, c.n_seqs, tokens_per_seq, group, head_dim);
   PagedAttnParams p{c, q, out, seqs, positions, 0, group, rows / group, scale, cap, nullptr, nullptr};
   p.parts = static_cast<float*>(ws);
   p.joins = reinterpret_cast<int4*>(p.parts + static_cast<size_t>(grid) * 2 * 4 * (head_dim + 2));

@@ -517,13 +517,19 @@ def paged_kv_gather(fmt: int, pages, table, seqs, positions, head_dim: int, k_ou
 
 
 def paged_kv_attention(fmt: int, pages, table, q, seqs, positions, scale: float,
-                       softcap: float = 0.0, workspace=None, out=None, stream=None):
+                       softcap: float = 0.0, workspace=None, out=None, stream=None,
+                       tokens_per_seq: int = 0):
     """q [T, n_q, hd]: row t attends to positions 0 .. positions[t] of sequence seqs[t] in the
-    pages (int64 both, on the device; negative: padding, a row of zeros)."""
+    pages (int64 both, on the device; negative: padding, a row of zeros).  tokens_per_seq: how
+    many neighbouring rows a sequence has, about, for the form that is fastest for them; 0: more
+    than one if there are more rows than the table has."""
     dev = torch.cuda.current_device()
     qh = _heads(q, "q", dev)
     n, n_q, hd = q.shape
     kv = _paged(fmt, pages, table, hd, dev)
+    if tokens_per_seq < 0:
+        raise ValueError(f"tokens_per_seq = {tokens_per_seq} < 0")
+    kv.tokens_per_seq = min(tokens_per_seq, n)
     out, oh = _out_heads(out, (n, n_q, hd), "out", dev, stream)
     if n == 0:
         return out
