@@ -452,11 +452,15 @@ def _paged(fmt: int, pages, table, head_dim: int, dev: int):
     if len(shape) != 3 or len(rows) != 2 or not pages.is_contiguous() or not table.is_contiguous():
         raise ValueError("pages must be [n_pages, n_kv, bytes] and table [n_seqs, max_pages], "
                          "contiguous")
-    # the library refuses other formats and head sizes itself
+    # the library refuses other formats and head sizes itself, but sees 32 bits of them
+    if fmt not in (Q4_0, Q8_0):
+        fmt = 0
     slab = {Q4_0: 18 * head_dim, Q8_0: 34 * head_dim}.get(fmt, 0) or shape[2] or 1
     if shape[2] == 0 or shape[2] % slab:
         raise ValueError(f"a kv head's part of a page has {shape[2]} bytes, not a multiple of "
                          f"{slab}, those of 16 positions")
+    if shape[2] // slab > 4096:
+        raise ValueError(f"a page has {shape[2] // slab * 16} positions, at most 65536 are taken")
     return _lib.QwsPagedKv(fmt, shape[2] // slab * 16, shape[1], head_dim, pages.data_ptr(),
                            shape[0], table.data_ptr(), rows[0], rows[1])
 
@@ -493,7 +497,8 @@ def paged_kv_append(fmt: int, pages, table, k, v, seqs, positions, rot_dim: int 
             None if w_q is None else _vec(w_q, "w_q", dev, torch.float32, hd),
             None if w_k is None else _vec(w_k, "w_k", dev, torch.float32, hd),
             _vec(seqs, "seqs", dev, torch.int64, n),
-            _vec(positions, "positions", dev, torch.int64, n), n, n_q, rot_dim, base, eps,
+            _vec(positions, "positions", dev, torch.int64, n), n, n_q,
+            max(-1, min(rot_dim, hd + 1)), base, eps,       # (the library sees 32 bits of it)
             stream_handle(stream)))
     return q_out
 
