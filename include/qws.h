@@ -397,9 +397,10 @@ qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const
  *   itself and some 2^-40 of its head's largest before it is quantised (the angle as
  *   in qws_qk_norm_rope).  0 <= eps < 2^100.  x finite; |x| < 2^60 with a norm, and as small as
  *   f32 goes, eps 0 included; a head of zeros stays zeros.  What is stored is at most 8
- *   (Q8_0: 127) times 65504, the largest f16.  Two tokens of a call
- *   with the same sequence and position: every two bytes stored are the one's or
- *   the other's.
+ *   (Q8_0: 127) times 65504, the largest f16.  A call gives a place in the pages (a
+ *   sequence's position, or that of another that shares the page) to one token: of two with
+ *   the same place every two bytes stored are the one's or the other's, another mix with
+ *   every run, unless their rows are equal.
  * qws_paged_kv_gather: k_out and v_out, the f32 values (scale * code, rounded at
  *   most once) of the tokens' rows: cached context for qws_prompt_attention.
  *   Rows of padding are zero.
@@ -436,8 +437,9 @@ qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const
  *   qws_embed_tokens' tokens.  1 <= vocab <= 2^19; temperature finite.
  *   Weights are held to about 2^-42 of themselves and 2^-45 of the largest (less
  *   than that is never drawn); their sums are exact.
- * All four calls: identical results run to run.  A row of qws_paged_kv_attention may
- * differ in its last bits with the other rows of its call, which it is split by.
+ * All four calls: identical results run to run, but for two tokens' rows in one place (see
+ * append).  A row of qws_paged_kv_attention may differ in its last bits with the other rows of its
+ * call, which it is split by.
  * ---------------------------------------------------------------------- */
 typedef struct {
   qws_format fmt;   /* QWS_Q4_0 or QWS_Q8_0 */
