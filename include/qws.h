@@ -281,7 +281,8 @@ qws_status qws_kv_attention(const float* q, const float* k_cache, const float* v
  *   [n_tokens] int64 (device, 8-byte aligned), any sign.  An output may be its
  *   own input (same pointer and strides); otherwise outputs overlap no input
  *   and not one another.  rot_dim even, 0 < rot_dim <= head_dim;
- *   base >= 1; eps >= 0; n_tokens >= 0.  The angle modulo a turn is off by at
+ *   base >= 1; eps >= 0; n_tokens >= 0.  Squares and their sum are f32: exact to its
+ *   last bits for mean x^2 + eps from 2^-100 to 2^119.  The angle modulo a turn is off by at
  *   most 6 x 2^-53 radians per position; its sine and cosine and the rotation
  *   are f32.
  *
@@ -411,7 +412,10 @@ qws_status qws_prefix_attention(const qws_heads* q, const float* k_prefix, const
  *   tokens_per_seq >= 0 says how many there are, about: it chooses the form that is
  *   fastest for them, and any number gives the same rows but for their last bits.  0: more
  *   than one if the call has more tokens than the table has rows, so a table with spare
- *   rows should say.  Rows of padding are zero.  n_q_heads /
+ *   rows should say.  For the pieces of prompts there are qws_paged_kv_gather and
+ *   qws_prompt_attention: here every two or four rows read their pages again.  (64 tokens
+ *   of a sequence of 8000 positions, 8 / 4 heads of 256, Q4_0: 73 us in either way; 16 tokens 27
+ *   here and 66 there, 512 tokens 493 and 115.)  Rows of padding are zero.  n_q_heads /
  *   n_kv_heads in 1..4.  out overlaps neither q nor the pages.  ws: device,
  *   16-byte aligned, >= qws_paged_kv_attention_workspace_bytes, scratch.
  *   Positions behind a row's own may hold anything, infinities and NaN included.
