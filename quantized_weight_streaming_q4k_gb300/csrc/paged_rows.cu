@@ -14,7 +14,7 @@
 // rate here.
 //
 // Bound by instructions: 4 bytes read a value, 4 (queries) or 18/32 (keys, values) written, but
-// some 430 instructions a row of 256 on average, a key row twice that.  One CTA a token,
+// some 440 instructions a row of 256 on average, a key row twice that.  One CTA a token,
 // as in qk_norm_rope: its threads compute the token's sines and cosines once into shared memory
 // while the warps' first rows are in flight; then a warp a head, one copy of the code for all.
 // 4096 tokens of 8 + 4 + 4 heads of 256, Q4_0, take 33.1 us (105 MB: 3.2 TB/s).  Before: 60 with
